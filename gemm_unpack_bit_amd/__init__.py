@@ -22,6 +22,8 @@ GROUP = 128
 W2, W4, W8, LUT4, OUTLIER4, CODEBOOK, W4A8, W4A8_SPLIT, W4A8_ASYM = 2, 4, 8, 16, 17, 18, 19, 20, 21
 LAYOUT_VERSION = 1  # QGEMV_LAYOUT_VERSION of the header this binding follows
 
+KV_NO_PAGES, KV_TABLE_FULL, KV_BAD_INDEX, KV_SHARED = 1, 2, 4, 8  # bits of a cache's status
+
 _lib = None
 
 _vp = ctypes.c_void_p
@@ -64,6 +66,16 @@ _SIGS = {
     "qgemv_dequant_lut4": (_i, [_i, _i, _vp, _vp, _vp, _vp, _vp]),
     "qgemv_gemv_f16": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp]),
     "qgemv_spmv_tilecoo": (_i, [_i, _i, _i, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp]),
+    # include/qgemv_attn.h
+    "qgemv_attn_prompt_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "qgemv_attn_prompt": (_i, [_i, _i, _i, _i, _i, _i, _i, _i, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "qgemv_attn_tree_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "qgemv_attn_tree": (_i, [_i, _vp, _i, _i, _i, ctypes.c_float, _vp, _vp, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "qgemv_kv_workspace_bytes": (_sz, [_i, _i]),
+    "qgemv_kv_reserve": (_i, [_vp, _vp, _vp, _vp, _sz, _vp]),
+    "qgemv_kv_write": (_i, [_vp, _i, _i, _vp, _vp, _vp, _vp, _vp]),
+    "qgemv_kv_fork": (_i, [_vp, _vp, _vp, _vp, _sz, _vp]),
+    "qgemv_kv_compact": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -569,3 +581,22 @@ def stream_read(buf, sink, nbytes=None, workgroups=1024, threads=512, offset=0):
         raise ValueError("range outside buf")
     _check("qgemv_stream_read", lib().qgemv_stream_read(_vp(buf.data_ptr() + offset), nbytes, _ptr(sink),
                                                         workgroups, threads, _stream(buf)))
+
+
+# ---------------------------------------------------------------------------
+# attention and the paged key/value cache
+# ---------------------------------------------------------------------------
+
+_ATTENTION = ("KvCache", "attn_prompt", "attn_prompt_workspace_bytes", "attn_tree", "attn_tree_workspace_bytes",
+              "kv_compact", "kv_fork", "kv_reserve", "kv_write")
+
+
+def __getattr__(name):
+    """The names of ``attention`` (imported with torch at their first use)."""
+    if name in _ATTENTION:
+        from . import attention
+
+        for n in _ATTENTION:
+            globals()[n] = getattr(attention, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

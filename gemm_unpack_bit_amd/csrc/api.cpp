@@ -18,21 +18,26 @@ const char* tune_env(const char* name) {
   static const bool on = std::getenv("QGEMV_TUNING") != nullptr;
   return on ? std::getenv(name) : nullptr;
 }
-}  // namespace qg
 
 namespace {
-
 thread_local int g_last_hip_error = 0;
-
-// qgemv_gemm_uniform: batches of at most this many rows run as 16-row slices
-// of the decode kernel
-constexpr int QGEMV_GEMM_SLICE_MAX_M = 64;
+}
 
 int hip_status(hipError_t e) {
   if (e == hipSuccess) return QGEMV_OK;
   g_last_hip_error = (int)e;
   return QGEMV_ERR_HIP;
 }
+int last_hip_error() { return g_last_hip_error; }
+}  // namespace qg
+
+namespace {
+
+using qg::hip_status;
+
+// qgemv_gemm_uniform: batches of at most this many rows run as 16-row slices
+// of the decode kernel
+constexpr int QGEMV_GEMM_SLICE_MAX_M = 64;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -203,7 +208,7 @@ const char* qgemv_status_string(int status) {
   return "unknown status";
 }
 
-int qgemv_last_hip_error(void) { return g_last_hip_error; }
+int qgemv_last_hip_error(void) { return qg::last_hip_error(); }
 
 size_t qgemv_packed_words(int bits, int layout, int rows, int cols) {
   if (!valid_bits(bits) || rows < 0 || cols < 0) return 0;

@@ -1,0 +1,322 @@
+// C ABI of the attention and cache calls (qgemv_attn.h): argument checks and
+// dispatch.  Host-only code; kernels live in attn_*.hip and kv_pages.hip.
+#include "qgemv_attn.h"
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "attn.hpp"
+#include "kernels.hpp"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// bytes [begin, end) that an array touches
+struct Span {
+  uintptr_t begin, end;
+};
+bool overlap(const Span& a, const Span& b) { return a.begin < b.end && b.begin < a.end; }
+Span span(const void* p, int64_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(p);
+  return {x, x + (bytes > 0 ? (uintptr_t)bytes : 0)};
+}
+Span span(const qgemv_heads& x, int tokens, int heads, int dim) {
+  if (tokens < 1 || heads < 1) return span(x.data, 0);
+  return span(x.data, 2 * ((tokens - 1) * x.token + (heads - 1) * x.head + dim));
+}
+
+constexpr int64_t STRIDE_MAX = (int64_t)1 << 40;  // (products with 32-bit counts stay in 64 bits once checked)
+
+// strides in range and, for an output, no element shared
+int check_heads(const qgemv_heads& x, int tokens, int heads, int dim, bool output) {
+  if (x.token < 0 || x.head < 0 || x.token > STRIDE_MAX || x.head > STRIDE_MAX) return QGEMV_ERR_SHAPE;
+  if (tokens > 0 && heads > 0) {
+    const double reach = (double)(tokens - 1) * x.token + (double)(heads - 1) * x.head + dim;
+    if (reach >= 4.6e18 / 2) return QGEMV_ERR_SHAPE;
+    if (output) {
+      const bool t1 = tokens == 1, h1 = heads == 1;
+      const bool heads_in_token = (h1 || x.head >= dim) && (t1 || x.token >= (heads - 1) * x.head + dim);
+      const bool tokens_in_head = (t1 || x.token >= dim) && (h1 || x.head >= (tokens - 1) * x.token + dim);
+      if (!heads_in_token && !tokens_in_head) return QGEMV_ERR_SHAPE;
+    }
+  }
+  return QGEMV_OK;
+}
+bool aligned_heads(const qgemv_heads& x) { return aligned(x.data, 16) && x.token % 8 == 0 && x.head % 8 == 0; }
+
+int check_kind(int dtype, int head_dim) {
+  if (dtype != QGEMV_F16 && dtype != QGEMV_BF16) return QGEMV_ERR_UNSUPPORTED;
+  return head_dim == 64 || head_dim == 128 ? QGEMV_OK : QGEMV_ERR_UNSUPPORTED;
+}
+
+int check_counts(int tokens, int rows, int heads, int heads_kv) {
+  if (tokens < 0 || rows < 0 || heads < 1 || heads_kv < 1 || heads % heads_kv) return QGEMV_ERR_SHAPE;
+  if ((int64_t)tokens * heads >= (int64_t)1 << 31 || rows >= 1 << 24) return QGEMV_ERR_SHAPE;
+  return QGEMV_OK;
+}
+
+// workgroups of the wide prompt kernel (0 where it is not the one that runs)
+int64_t prompt_grid(int tokens, int tokens_k, int rows, int heads, int heads_kv) {
+  const int group = heads / heads_kv;
+  if (!tokens || !rows || qg::narrow_tiles(tokens, rows, group)) return 0;
+  return (int64_t)qg::prompt_tiles(tokens, rows, group) * heads_kv * qg::prompt_splits(tokens, tokens_k, rows, heads_kv, group);
+}
+
+int check_scale(float scale) { return std::isfinite(scale) && scale >= 0.f ? QGEMV_OK : QGEMV_ERR_VALUE; }
+
+// The pools of a cache and its bookkeeping: null, format, shape, alignment.
+// Every call but qgemv_kv_write and the attention changes refs and tables.
+int check_cache(const qgemv_kv_cache* c, bool state) {
+  if (!c || !c->k || !c->v || !c->tables) return QGEMV_ERR_NULL;
+  if (state && (!c->lens || !c->refs || !c->status)) return QGEMV_ERR_NULL;
+  if (c->head_dim != 64 && c->head_dim != 128) return QGEMV_ERR_UNSUPPORTED;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return QGEMV_ERR_UNSUPPORTED;
+  if (c->layers < 1 || c->pages < 1 || c->heads_kv < 1 || c->rows < 0 || c->rows > 65535 || c->max_pages < 1)
+    return QGEMV_ERR_SHAPE;
+  if ((int64_t)c->max_pages * c->page_size >= (int64_t)1 << 31 || c->heads_kv > 65536 || c->layers > 65536 ||
+      (double)c->layers * c->pages * c->page_size * c->heads_kv * c->head_dim >= 1e15 ||
+      (int64_t)c->layers * c->heads_kv * c->head_dim >= (int64_t)1 << 32)  // (a launch's threads: a thread per 16 bytes)
+    return QGEMV_ERR_SHAPE;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->tables, 4)) return QGEMV_ERR_ALIGN;
+  if (state && (!aligned(c->lens, 4) || !aligned(c->refs, 4) || !aligned(c->status, 4))) return QGEMV_ERR_ALIGN;
+  return QGEMV_OK;
+}
+
+int64_t pool_bytes(const qgemv_kv_cache& c) {
+  return (int64_t)2 * c.layers * c.pages * c.page_size * c.heads_kv * c.head_dim;
+}
+
+qg::KvArgs cache_args(const qgemv_kv_cache& c) {
+  qg::KvArgs a;
+  a.layers = c.layers;
+  a.pages = c.pages;
+  a.page_shift = __builtin_ctz((unsigned)c.page_size);
+  a.heads_kv = c.heads_kv;
+  a.head_dim = c.head_dim;
+  a.rows = c.rows;
+  a.max_pages = c.max_pages;
+  a.k = c.k;
+  a.v = c.v;
+  a.tables = c.tables;
+  a.lens = c.lens;
+  a.refs = c.refs;
+  a.status = c.status;
+  return a;
+}
+
+size_t up16(size_t n) { return (n + 15) / 16 * 16; }
+
+int scratch(int rows, int pages, void* ws, size_t ws_bytes, qg::KvScratch* w) {
+  if (!ws || ws_bytes < qgemv_kv_workspace_bytes(rows, pages)) return QGEMV_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return QGEMV_ERR_ALIGN;
+  char* p = reinterpret_cast<char*>(ws);
+  w->free_list = reinterpret_cast<int32_t*>(p);
+  w->src = reinterpret_cast<int32_t*>(p + up16((size_t)pages * 4));
+  w->dst = reinterpret_cast<int32_t*>(p + up16((size_t)pages * 4) + up16((size_t)rows * 4));
+  return QGEMV_OK;
+}
+
+// attention: o against what the call reads and its workspace
+bool writes_input(const Span& o, const Span& ws, const Span* in, int n) {
+  for (int i = 0; i < n; ++i)
+    if (overlap(o, in[i]) || overlap(ws, in[i])) return true;
+  return overlap(o, ws);
+}
+
+hipStream_t stream_of(qgemv_stream_t s) { return reinterpret_cast<hipStream_t>(s); }
+
+}  // namespace
+
+extern "C" {
+
+size_t qgemv_attn_prompt_workspace_bytes(int tokens, int tokens_k, int batch, int heads, int heads_kv, int head_dim) {
+  if (check_counts(tokens, batch, heads, heads_kv) || tokens_k < 0 || !tokens || !batch) return 0;
+  if (head_dim != 64 && head_dim != 128) return 0;
+  const int group = heads / heads_kv, rt = qg::narrow_tiles(tokens, batch, group);
+  if (rt) return qg::partial_bytes(2 * qg::NARROW_WORKGROUPS, 16 * rt, head_dim);
+  const int splits = qg::prompt_splits(tokens, tokens_k, batch, heads_kv, group);
+  if (splits == 1) return 0;
+  return qg::partial_bytes((size_t)qg::prompt_tiles(tokens, batch, group) * heads_kv * splits, qg::WIDE_BM, head_dim);
+}
+
+int qgemv_attn_prompt(int dtype, int causal, int tokens, int tokens_k, int batch, int heads, int heads_kv,
+                      int head_dim, float scale, const qgemv_heads* q, const qgemv_heads* k, const qgemv_heads* v,
+                      const int32_t* cu_q, const int32_t* cu_k, const qgemv_heads* o, void* ws, size_t ws_bytes,
+                      qgemv_stream_t stream) {
+  if (!q || !k || !v || !o || !cu_q || !cu_k || !q->data || !k->data || !v->data || !o->data) return QGEMV_ERR_NULL;
+  int rc = check_kind(dtype, head_dim);
+  if (rc) return rc;
+  if ((rc = check_counts(tokens, batch, heads, heads_kv))) return rc;
+  if (tokens_k < 0 || prompt_grid(tokens, tokens_k, batch, heads, heads_kv) >= 1 << 24) return QGEMV_ERR_SHAPE;
+  if ((rc = check_heads(*q, tokens, heads, head_dim, false)) || (rc = check_heads(*k, tokens_k, heads_kv, head_dim, false)) ||
+      (rc = check_heads(*v, tokens_k, heads_kv, head_dim, false)) || (rc = check_heads(*o, tokens, heads, head_dim, true)))
+    return rc;
+  if ((rc = check_scale(scale))) return rc;
+  if (!aligned_heads(*q) || !aligned_heads(*k) || !aligned_heads(*v) || !aligned_heads(*o) || !aligned(cu_q, 4) ||
+      !aligned(cu_k, 4))
+    return QGEMV_ERR_ALIGN;
+  const size_t need = qgemv_attn_prompt_workspace_bytes(tokens, tokens_k, batch, heads, heads_kv, head_dim);
+  const Span so = span(*o, tokens, heads, head_dim), sw = span(ws, need && ws ? (int64_t)need : 0);
+  const Span in[] = {span(*q, tokens, heads, head_dim), span(*k, tokens_k, heads_kv, head_dim),
+                     span(*v, tokens_k, heads_kv, head_dim), span(cu_q, 4 * ((int64_t)batch + 1)),
+                     span(cu_k, 4 * ((int64_t)batch + 1))};
+  if (writes_input(so, sw, in, 5)) return QGEMV_ERR_VALUE;
+  if (need && (!ws || ws_bytes < need)) return QGEMV_ERR_WORKSPACE;
+  if (need && !aligned(ws, 16)) return QGEMV_ERR_ALIGN;
+  if (!tokens || !batch) return QGEMV_OK;
+  qg::AttnArgs a{};
+  a.bf16 = dtype == QGEMV_BF16;
+  a.head_dim = head_dim;
+  a.heads = heads;
+  a.heads_kv = heads_kv;
+  a.group = heads / heads_kv;
+  a.tokens = tokens;
+  a.rows = batch;
+  a.causal = causal != 0;
+  a.scale = scale * 1.4426950408889634f;
+  a.q = q->data, a.q_token = q->token, a.q_head = q->head;
+  a.k = k->data, a.k_token = k->token, a.k_head = k->head;
+  a.v = v->data, a.v_token = v->token, a.v_head = v->head;
+  a.o = o->data, a.o_token = o->token, a.o_head = o->head;
+  a.cu = cu_q;
+  a.cu_k = cu_k;
+  a.tokens_k = tokens_k;
+  a.ws = reinterpret_cast<float*>(ws);
+  const int rt = qg::narrow_tiles(tokens, batch, a.group);
+  return qg::hip_status(rt ? qg::launch_attn_narrow(a, rt, stream_of(stream)) : qg::launch_attn_wide(a, stream_of(stream)));
+}
+
+size_t qgemv_attn_tree_workspace_bytes(int tokens, int rows, int heads, int heads_kv, int head_dim) {
+  if (check_counts(tokens, rows, heads, heads_kv) || !tokens || !rows) return 0;
+  if (head_dim != 64 && head_dim != 128) return 0;
+  const int rt = qg::narrow_tiles(tokens, rows, heads / heads_kv);
+  if (rt) return qg::partial_bytes(2 * qg::NARROW_WORKGROUPS, 16 * rt, head_dim);
+  return qg::partial_bytes(2 * qg::WIDE_WORKGROUPS, qg::WIDE_BM, head_dim);
+}
+
+int qgemv_attn_tree(int dtype, const qgemv_kv_cache* c, int layer, int tokens, int heads, float scale,
+                    const qgemv_heads* q, const int32_t* cu, const int32_t* pos, const uint64_t* mask,
+                    int mask_words, const qgemv_heads* o, void* ws, size_t ws_bytes, qgemv_stream_t stream) {
+  if (!c || !c->k || !c->v || !c->tables || !q || !q->data || !o || !o->data || !cu || !pos) return QGEMV_ERR_NULL;
+  int rc = check_kind(dtype, c->head_dim);
+  if (rc) return rc;
+  if ((rc = check_cache(c, false))) return rc;
+  if ((rc = check_counts(tokens, c->rows, heads, c->heads_kv))) return rc;
+  if (layer < 0 || layer >= c->layers || mask_words < 0 || mask_words > 1 << 20 || (mask != nullptr) != (mask_words > 0))
+    return QGEMV_ERR_SHAPE;
+  if ((rc = check_heads(*q, tokens, heads, c->head_dim, false)) || (rc = check_heads(*o, tokens, heads, c->head_dim, true)))
+    return rc;
+  if ((rc = check_scale(scale))) return rc;
+  if (!aligned_heads(*q) || !aligned_heads(*o) || !aligned(cu, 4) || !aligned(pos, 4) || !aligned(mask, 8))
+    return QGEMV_ERR_ALIGN;
+  const size_t need = qgemv_attn_tree_workspace_bytes(tokens, c->rows, heads, c->heads_kv, c->head_dim);
+  const Span so = span(*o, tokens, heads, c->head_dim), sw = span(ws, need && ws ? (int64_t)need : 0);
+  const Span in[] = {span(*q, tokens, heads, c->head_dim), span(c->k, pool_bytes(*c)), span(c->v, pool_bytes(*c)),
+                     span(c->tables, (int64_t)4 * c->rows * c->max_pages), span(cu, 4 * ((int64_t)c->rows + 1)),
+                     span(pos, (int64_t)4 * c->rows), span(mask, (int64_t)8 * tokens * mask_words)};
+  if (writes_input(so, sw, in, 7)) return QGEMV_ERR_VALUE;
+  if (need && (!ws || ws_bytes < need)) return QGEMV_ERR_WORKSPACE;
+  if (need && !aligned(ws, 16)) return QGEMV_ERR_ALIGN;
+  if (!tokens || !c->rows) return QGEMV_OK;
+  qg::AttnArgs a{};
+  a.bf16 = dtype == QGEMV_BF16;
+  a.head_dim = c->head_dim;
+  a.heads = heads;
+  a.heads_kv = c->heads_kv;
+  a.group = heads / c->heads_kv;
+  a.tokens = tokens;
+  a.rows = c->rows;
+  a.causal = 1;
+  a.scale = scale * 1.4426950408889634f;
+  const int64_t row = (int64_t)c->heads_kv * c->head_dim, in_layer = (int64_t)c->pages * c->page_size * row;
+  a.q = q->data, a.q_token = q->token, a.q_head = q->head;
+  a.k = c->k + layer * in_layer, a.k_token = row, a.k_head = c->head_dim;
+  a.v = c->v + layer * in_layer, a.v_token = row, a.v_head = c->head_dim;
+  a.o = o->data, a.o_token = o->token, a.o_head = o->head;
+  a.cu = cu;
+  a.tables = c->tables;
+  a.pos = pos;
+  a.pages = c->pages;
+  a.page_shift = __builtin_ctz((unsigned)c->page_size);
+  a.max_pages = c->max_pages;
+  a.mask = mask;
+  a.mask_words = mask_words;
+  a.ws = reinterpret_cast<float*>(ws);
+  const int rt = qg::narrow_tiles(tokens, a.rows, a.group);
+  return qg::hip_status(rt ? qg::launch_attn_narrow(a, rt, stream_of(stream)) : qg::launch_attn_wide(a, stream_of(stream)));
+}
+
+size_t qgemv_kv_workspace_bytes(int rows, int pages) {
+  if (rows < 0 || pages < 1) return 0;
+  return up16((size_t)pages * 4) + 2 * up16((size_t)rows * 4);
+}
+
+int qgemv_kv_reserve(const qgemv_kv_cache* c, const int32_t* cu, int32_t* pos, void* ws, size_t ws_bytes,
+                     qgemv_stream_t stream) {
+  int rc = check_cache(c, true);
+  if (rc) return rc;
+  if (!cu || !pos) return QGEMV_ERR_NULL;
+  if (!aligned(cu, 4) || !aligned(pos, 4)) return QGEMV_ERR_ALIGN;
+  qg::KvScratch w;
+  if ((rc = scratch(c->rows, c->pages, ws, ws_bytes, &w))) return rc;
+  if (!c->rows) return QGEMV_OK;
+  return qg::hip_status(qg::launch_kv_reserve(cache_args(*c), cu, pos, w, stream_of(stream)));
+}
+
+int qgemv_kv_write(const qgemv_kv_cache* c, int layer, int tokens, const qgemv_heads* k, const qgemv_heads* v,
+                   const int32_t* cu, const int32_t* pos, qgemv_stream_t stream) {
+  int rc = check_cache(c, false);
+  if (rc) return rc;
+  if (!k || !v || !k->data || !v->data || !cu || !pos) return QGEMV_ERR_NULL;
+  if (layer < 0 || layer >= c->layers || tokens < 0 || tokens >= 1 << 26) return QGEMV_ERR_SHAPE;
+  if ((rc = check_heads(*k, tokens, c->heads_kv, c->head_dim, false)) ||
+      (rc = check_heads(*v, tokens, c->heads_kv, c->head_dim, false)))
+    return rc;
+  if (!aligned_heads(*k) || !aligned_heads(*v) || !aligned(cu, 4) || !aligned(pos, 4)) return QGEMV_ERR_ALIGN;
+  const Span pk = span(c->k, pool_bytes(*c)), pv = span(c->v, pool_bytes(*c));
+  const Span ik = span(*k, tokens, c->heads_kv, c->head_dim), iv = span(*v, tokens, c->heads_kv, c->head_dim);
+  if (overlap(pk, ik) || overlap(pk, iv) || overlap(pv, ik) || overlap(pv, iv)) return QGEMV_ERR_VALUE;
+  if (!tokens || !c->rows) return QGEMV_OK;
+  qg::KvWriteArgs a{cache_args(*c), layer, tokens, k->data, v->data, k->token, k->head, v->token, v->head, cu, pos};
+  return qg::hip_status(qg::launch_kv_write(a, stream_of(stream)));
+}
+
+int qgemv_kv_fork(const qgemv_kv_cache* c, const int32_t* parents, const qgemv_kv_cache* out, void* ws,
+                  size_t ws_bytes, qgemv_stream_t stream) {
+  int rc = check_cache(c, true);
+  if (rc) return rc;
+  if ((rc = check_cache(out, true))) return rc;
+  if (!parents) return QGEMV_ERR_NULL;
+  if (out->layers != c->layers || out->pages != c->pages || out->page_size != c->page_size ||
+      out->heads_kv != c->heads_kv || out->head_dim != c->head_dim || out->max_pages != c->max_pages)
+    return QGEMV_ERR_SHAPE;
+  if (!aligned(parents, 4)) return QGEMV_ERR_ALIGN;
+  const Span ct = span(c->tables, (int64_t)4 * c->rows * c->max_pages), cl = span(c->lens, (int64_t)4 * c->rows);
+  const Span ot = span(out->tables, (int64_t)4 * out->rows * out->max_pages), ol = span(out->lens, (int64_t)4 * out->rows);
+  if (out->k != c->k || out->v != c->v || out->refs != c->refs || out->status != c->status || overlap(ct, ot) ||
+      overlap(ct, ol) || overlap(cl, ot) || overlap(cl, ol))
+    return QGEMV_ERR_VALUE;
+  qg::KvScratch w;
+  const int rows = c->rows > out->rows ? c->rows : out->rows;
+  if ((rc = scratch(rows, c->pages, ws, ws_bytes, &w))) return rc;
+  if (!rows) return QGEMV_OK;
+  return qg::hip_status(qg::launch_kv_fork(cache_args(*c), parents, cache_args(*out), w, stream_of(stream)));
+}
+
+int qgemv_kv_compact(const qgemv_kv_cache* c, const int32_t* pos, const int32_t* keep, int max_keep,
+                     const int32_t* count, void* ws, size_t ws_bytes, qgemv_stream_t stream) {
+  int rc = check_cache(c, true);
+  if (rc) return rc;
+  if (!pos || !count || (max_keep > 0 && !keep)) return QGEMV_ERR_NULL;
+  if (max_keep < 0) return QGEMV_ERR_SHAPE;
+  if (!aligned(pos, 4) || !aligned(keep, 4) || !aligned(count, 4)) return QGEMV_ERR_ALIGN;
+  qg::KvScratch w;
+  if ((rc = scratch(c->rows, c->pages, ws, ws_bytes, &w))) return rc;
+  if (!c->rows) return QGEMV_OK;
+  return qg::hip_status(qg::launch_kv_compact(cache_args(*c), pos, keep, max_keep, count, w, stream_of(stream)));
+}
+
+}  // extern "C"

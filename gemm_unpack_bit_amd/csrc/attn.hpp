@@ -1,0 +1,98 @@
+// Internal interface of the attention and cache kernels (api_attn.cpp calls
+// the launchers; attn_*.hip and kv_pages.hip hold the kernels).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace qg {
+
+// the paged cache as the kernels take it (page_size = 1 << page_shift)
+struct KvArgs {
+  int layers, pages, page_shift, heads_kv, head_dim, rows, max_pages;
+  uint16_t *k, *v;
+  int32_t *tables, *lens, *refs, *status;
+};
+
+struct KvScratch {
+  int32_t* free_list;  // [pages]: free pages found, lowest first
+  int32_t* src;        // [rows] fork: the page to copy from, or -1; compact: 1 if the row is compacted
+  int32_t* dst;        // [rows] fork: the page to copy to
+};
+
+// status bits (QGEMV_KV_*)
+enum { KV_NO_PAGES = 1, KV_TABLE_FULL = 2, KV_BAD_INDEX = 4, KV_SHARED = 8 };
+
+hipError_t launch_kv_reserve(const KvArgs& c, const int32_t* cu, int32_t* pos, const KvScratch& w, hipStream_t s);
+
+struct KvWriteArgs {
+  KvArgs c;
+  int layer, tokens;
+  const uint16_t *k, *v;
+  int64_t k_token, k_head, v_token, v_head;
+  const int32_t *cu, *pos;
+};
+hipError_t launch_kv_write(const KvWriteArgs& a, hipStream_t s);
+
+hipError_t launch_kv_fork(const KvArgs& c, const int32_t* parents, const KvArgs& out, const KvScratch& w,
+                          hipStream_t s);
+hipError_t launch_kv_compact(const KvArgs& c, const int32_t* pos, const int32_t* keep, int max_keep,
+                             const int32_t* count, const KvScratch& w, hipStream_t s);
+
+// Attention.  One form for both sources of keys: packed rows (tables NULL;
+// cu_k, k_token .. v_head) or one layer of a paged cache (tables set; k and v
+// point at the layer, a page holds [page_size][heads_kv][head_dim]).
+struct AttnArgs {
+  int bf16, head_dim, heads, heads_kv, group;  // group = heads / heads_kv
+  int tokens, rows;
+  int causal;     // packed keys only
+  float scale;    // score scale times log2(e): the kernels work in powers of two
+  const uint16_t *q, *k, *v;
+  uint16_t* o;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
+  const int32_t* cu;
+  // packed keys
+  int tokens_k;
+  const int32_t* cu_k;
+  // paged keys
+  const int32_t *tables, *pos;
+  int pages, page_shift, max_pages;
+  const uint64_t* mask;
+  int mask_words;
+  float* ws;
+};
+
+// The choice of kernel, its split of the keys, and so the workspace, depend on
+// the sizes that the host knows (not on lengths on the device).
+constexpr int NARROW_WORKGROUPS = 512;
+constexpr int WIDE_WORKGROUPS = 512;
+constexpr int WIDE_BM = 128;
+constexpr size_t partial_bytes(size_t slots, int bm, int d) { return slots * bm * (size_t)(d + 2) * 4; }
+
+// 16-row tiles a wave of the narrow kernel holds (1 or 2) for the average
+// row's queries, or 0: the wide kernel
+inline int narrow_tiles(int tokens, int rows, int group) {
+  const int64_t avg = ((int64_t)tokens + rows - 1) / rows * group;
+  return avg <= 16 ? 1 : avg <= 32 ? 2 : 0;
+}
+inline int prompt_tiles(int tokens, int rows, int group) { return (int)((int64_t)tokens * group / WIDE_BM) + rows; }
+// parts of the keys of each tile, where whole tiles would leave compute units
+// idle: up to 512 workgroups, of at least 4 key tiles on average
+inline int prompt_splits(int tokens, int tokens_k, int rows, int heads_kv, int group) {
+  const int64_t items = (int64_t)prompt_tiles(tokens, rows, group) * heads_kv;
+  const int64_t most = tokens_k / rows / 256;
+  const int64_t s = 512 / items < most ? 512 / items : most;
+  return s < 1 ? 1 : (int)s;
+}
+
+// workgroups of the kernels that join partial results: a wave per query token
+// and head, in a loop beyond 2^20 workgroups
+inline unsigned join_blocks(const AttnArgs& a) {
+  const int64_t n = ((int64_t)a.tokens * a.heads + 3) / 4;
+  return (unsigned)(n < 1 << 20 ? n : 1 << 20);
+}
+
+hipError_t launch_attn_narrow(const AttnArgs& a, int rt, hipStream_t s);
+hipError_t launch_attn_wide(const AttnArgs& a, hipStream_t s);
+
+}  // namespace qg

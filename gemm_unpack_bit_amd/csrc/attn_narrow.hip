@@ -1,0 +1,327 @@
+// Attention for few query rows per key head: decode (one token per row) and
+// small drafted trees, over paged or packed keys.
+//
+// Mathematics.  For one key head the query rows are r = t * group + g (token
+// t, head g of the group), so grouped heads share one read of the keys and
+// values.  Over the keys in steps of 32 a wave keeps, per row, the running
+// maximum m, the sum l = sum 2^(x - m) and the output sums O = sum 2^(x - m) v,
+// x = score * scale * log2(e); a step with a new maximum scales l and O by
+// 2^(m_old - m_new).
+//
+// Bound: memory.  Each key and value is read once, straight from global
+// memory into registers, with no LDS on the way:
+// - S^T = K Q^T on the matrix cores (16 x 16 x 32): a lane's A operand is 8
+//   consecutive elements of one key, one 16-byte load.
+// - O^T = V^T P^T: the matrix product may take its 32 keys in any order if
+//   both operands agree, so a lane keeps the scores where S^T left them (the
+//   keys 4 q + i and 16 + 4 q + i of lane quarter q) as B operand, and for A
+//   needs 8 keys of one output column.  It loads D / 16 columns of its 8 keys
+//   (16 lanes read a key's whole row) and pairs the keys of a column by one
+//   byte permute per two elements.  The output columns are then
+//   D / 16 * m + j for matrix row m of product j: again only an order.
+// - row statistics are per lane (row = lane % 16): the maximum crosses the
+//   four lane quarters by two swaps, the sum only once at the end.
+// The waves of a workgroup take the steps of its key range in turn, each with
+// its own m, l, O, joined in LDS at the end.  Few rows leave few tiles, so the
+// key axis is split over workgroups (Units).
+#include "attn_common.hpp"
+
+namespace qg {
+namespace {
+
+constexpr int KB = 128;      // keys of a unit: 32 per wave
+constexpr int WAVES = 4;
+
+// RT: 16-row tiles of query rows held by a wave (BM = 16 RT rows)
+template <typename E, int D, int RT, bool PAGED>
+__global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, int workgroups, int least) {
+  constexpr int BM = 16 * RT;
+  constexpr int KS = D / 32;  // matrix steps along head_dim
+  constexpr int DL = D / 16;  // output columns of a lane
+  constexpr int DW = DL / 2;  // ... in 32-bit words
+  constexpr int PITCH = D + 4;
+  typedef uint32_t vw __attribute__((ext_vector_type(DW)));
+  using U = Units<BM, KB, PAGED>;
+  __shared__ __attribute__((aligned(16))) float o_s[WAVES][BM][PITCH];
+  __shared__ float m_s[WAVES][BM], l_s[WAVES][BM];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n16 = lane & 15, quarter = lane >> 4;
+  const Split sp = U::split(a, workgroups, least);
+  int64_t u = (int64_t)blockIdx.x * sp.per;
+  const int64_t u_end = u + sp.per < sp.total ? u + sp.per : sp.total;
+  const int64_t u_begin = u;
+  const Partials<BM, D> parts(a.ws, 2 * (int64_t)workgroups);
+
+  while (u < u_end) {
+    const Place at = U::place(a, u);
+    const Row r = row_of<PAGED>(a, at.b);
+    const int per_item = U::units(r);
+    const int64_t item = (u - at.first) / per_item;
+    const int ku = (int)(u - at.first - item * per_item);  // first unit in the item
+    const int64_t left = u_end - u;
+    const int ku_end = (int)(ku + left < per_item ? ku + left : per_item);
+    const int h = (int)(item % a.heads_kv), tile = (int)(item / a.heads_kv);
+    const int rows = r.n * a.group;
+
+    // the wave's query rows: lane column n16 of each 16-row tile
+    u4 qf[RT][KS];
+    Sight<PAGED> sight[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int row = tile * BM + 16 * i + n16;
+      const int t = row / a.group, g = row - t * a.group;
+      const bool live = row < rows;
+      sight[i].init(a, r, live ? t : r.n);
+      const uint16_t* q = a.q + (live ? (int64_t)(r.q0 + t) * a.q_token + (int64_t)(h * a.group + g) * a.q_head : 0);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        qf[i][s] = u4{0, 0, 0, 0};
+        if (live) qf[i][s] = *reinterpret_cast<const u4*>(q + 32 * s + 8 * quarter);
+      }
+    }
+    // keys that every row of the tile sees
+    const int first_t = tile * BM / a.group;
+    int common;
+    if constexpr (PAGED) common = a.mask ? r.pos : r.pos + first_t + 1;
+    else common = a.causal ? r.pos + first_t + 1 : r.keys;
+    common = common < r.keys ? common : r.keys;
+
+    f4 o[RT][DL];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      m[i] = NEG_INF;
+      l[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < DL; ++j) o[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    const uint16_t* kh = a.k + (int64_t)h * a.k_head;
+    const uint16_t* vh = a.v + (int64_t)h * a.v_head;
+    // where the 16 keys from key kb (a multiple of 16) on start; a tile past
+    // the row's last key falls back on the last one that has any
+    auto tile_at = [&](int kb, int64_t& ko, int64_t& vo, int& last) {
+      const int top = (r.keys - 1) & ~15;
+      kb = kb < top ? kb : top;
+      last = r.keys - 1 - kb;  // keys past it are read from its place
+      int64_t tok;
+      if constexpr (PAGED) {
+        const int page = a.tables[(int64_t)at.b * a.max_pages + (kb >> a.page_shift)];
+        const int ok = (unsigned)page < (unsigned)a.pages ? page : 0;
+        tok = ((int64_t)ok << a.page_shift) + (kb & ((1 << a.page_shift) - 1));
+      } else {
+        tok = (int64_t)r.k0 + kb;
+      }
+      ko = tok * a.k_token;
+      vo = tok * a.v_token;
+    };
+
+    const int k_end = ku_end * KB < r.keys ? ku_end * KB : r.keys;
+    for (int kb = ku * KB + 32 * wave; kb < k_end; kb += 32 * WAVES) {
+      int64_t ko[2], vo[2];
+      int last[2];
+      tile_at(kb, ko[0], vo[0], last[0]);
+      tile_at(kb + 16, ko[1], vo[1], last[1]);
+      u4 kf[2][KS];
+      vw vf[8];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint16_t* p = kh + ko[x] + (int64_t)min(n16, last[x]) * a.k_token + 8 * quarter;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) kf[x][s] = *reinterpret_cast<const u4*>(p + 32 * s);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          vf[4 * x + i] = *reinterpret_cast<const vw*>(vh + vo[x] + (int64_t)min(4 * quarter + i, last[x]) * a.v_token +
+                                                       DL * n16);
+
+      const bool masked = kb + 32 > common;
+      uint64_t seen[RT];
+      uint64_t odd = 0;  // keys of the step with a value that is not finite (masked steps)
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) seen[i] = sight[i].window(a, r, kb) >> (4 * quarter);
+        // a weight of 0 does not cancel a value that is infinite or NaN:
+        // take those out and add them for the rows that see them
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t f = 0;
+#pragma unroll
+          for (int w = 0; w < DW; ++w) {
+            const uint32_t x = nonfinite<E>(vf[i][w]);
+            f |= x;
+            // halves to clear: 0x8000 of a half becomes 0xFFFF
+            vf[i][w] &= ~((x - (x >> 15)) | x);
+          }
+          if (f) bad |= 1u << i;
+        }
+        if (__any(bad))
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int qd = 0; qd < 4; ++qd)
+              if (__ballot(bad >> i & 1) >> (16 * qd) & 0xFFFF) odd |= 1ull << ((i < 4 ? i : 12 + i) + 4 * qd);
+      }
+
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        f4 sc[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          sc[x] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < KS; ++s) sc[x] = E::mfma16(kf[x][s], qf[i][s], sc[x]);
+        }
+        if (masked) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[x][e] = seen[i] >> (16 * x + e) & 1 ? sc[x][e] : NEG_INF;
+        }
+        float mx = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
+                         fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
+        mx = quarter_max(mx);
+        mx = mx == NEG_INF ? NEG_INF : mx * a.scale;
+        if (__any(mx > m[i])) {
+          const float mn = fmaxf(m[i], mx), w = mn == NEG_INF ? 1.f : exp2_(m[i] - mn);
+          m[i] = mn;
+          l[i] *= w;
+#pragma unroll
+          for (int j = 0; j < DL; ++j) o[i][j] *= w;
+        }
+        const float base = m[i] == NEG_INF ? 0.f : m[i] - E::LIFT;
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = sc[e >> 2][e & 3];
+          p[e] = x == NEG_INF ? 0.f : exp2_(fmaf(x, a.scale, -base));
+          l[i] += p[e];
+        }
+        const u4 pf = u4{E::pack(p[0], p[1]), E::pack(p[2], p[3]), E::pack(p[4], p[5]), E::pack(p[6], p[7])};
+#pragma unroll
+        for (int j = 0; j < DL; ++j) {
+          u4 va;
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            va[w] = __builtin_amdgcn_perm(vf[2 * w + 1][j / 2], vf[2 * w][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
+          o[i][j] = E::mfma16(va, pf, o[i][j]);
+        }
+        if (odd) {
+          const uint64_t mine = sight[i].window(a, r, kb);
+          for (uint64_t left_keys = odd; left_keys; left_keys &= left_keys - 1) {
+            const int key = __builtin_ctzll(left_keys), x = key >> 4;
+            const uint16_t* v = vh + vo[x] + (int64_t)min(key & 15, last[x]) * a.v_token;
+#pragma unroll
+            for (int j = 0; j < DL; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint16_t y = v[DL * (4 * quarter + e) + j];
+                if (mine >> key & 1 && nonfinite<E>(y) & 0x8000u) o[i][j][e] += E::value(y);
+              }
+          }
+        }
+      }
+    }
+
+    // join the waves
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int row = 16 * i + n16;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < DL; j += 4)
+          *reinterpret_cast<f4*>(&o_s[wave][row][DL * (4 * quarter + e) + j]) =
+              f4{o[i][j][e], o[i][j + 1][e], o[i][j + 2][e], o[i][j + 3][e]};
+      const float sum = quarter_sum(l[i]);
+      if (quarter == 0) m_s[wave][row] = m[i], l_s[wave][row] = sum;
+    }
+    __syncthreads();
+    const bool whole = ku == 0 && ku_end == per_item;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (u != u_begin);
+    constexpr int TPR = 64 * WAVES / 16;  // 16 threads per row, DL columns each
+    static_assert(TPR == 16, "a row's columns are DL per thread");
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int row = 16 * i + (threadIdx.x >> 4), col = DL * (threadIdx.x & 15);
+      float M = NEG_INF;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) M = fmaxf(M, m_s[w][row]);
+      const float base = M == NEG_INF ? 0.f : M;
+      float sum = 0.f, acc[DL] = {};
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        const float f = exp2_(m_s[w][row] - base);
+        sum += f * l_s[w][row];
+#pragma unroll
+        for (int j = 0; j < DL; ++j) acc[j] += f * o_s[w][row][col + j];
+      }
+      const int qr = tile * BM + row;
+      if (whole) {
+        if (qr < rows) {
+          const int t = qr / a.group, g = qr - t * a.group;
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          vw y;
+#pragma unroll
+          for (int j = 0; j < DW; ++j) y[j] = E::pack(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+          *reinterpret_cast<vw*>(a.o + (int64_t)(r.q0 + t) * a.o_token + (int64_t)(h * a.group + g) * a.o_head + col) = y;
+        }
+      } else {
+        float* po = parts.o_at(slot, row) + col;
+#pragma unroll
+        for (int j = 0; j < DL; j += 4)
+          *reinterpret_cast<f4*>(po + j) = f4{acc[j], acc[j + 1], acc[j + 2], acc[j + 3]};
+        if ((threadIdx.x & 15) == 0) {
+          float* ml = parts.ml_at(slot, row);
+          ml[0] = M;
+          ml[1] = sum;
+        }
+      }
+    }
+    __syncthreads();  // the buffers are free for the next segment
+    u += ku_end - ku;
+  }
+}
+
+// One wave per query token and head: joins the parts of an item that lay in
+// several workgroups.
+template <typename E, int D, int RT, bool PAGED>
+__global__ void __launch_bounds__(256) attn_narrow_join_kernel(AttnArgs a, int workgroups, int least) {
+  constexpr int BM = 16 * RT;
+  using U = Units<BM, KB, PAGED>;
+  const int n = a.tokens * a.heads;
+  for (int64_t w = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6)); w < n; w += (int64_t)gridDim.x * 4)
+    U::template join<E, D>(a, (int)w, workgroups, least);
+}
+
+template <typename E, int D, int RT, bool PAGED>
+hipError_t launch(const AttnArgs& a, hipStream_t s) {
+  const int least = 1;
+  hipLaunchKernelGGL((attn_narrow_kernel<E, D, RT, PAGED>), dim3(NARROW_WORKGROUPS), dim3(64 * WAVES), 0, s, a,
+                     NARROW_WORKGROUPS, least);
+  hipLaunchKernelGGL((attn_narrow_join_kernel<E, D, RT, PAGED>), dim3(join_blocks(a)), dim3(256), 0, s, a,
+                     NARROW_WORKGROUPS, least);
+  return hipGetLastError();
+}
+
+template <int D, int RT, bool PAGED>
+hipError_t launch_e(const AttnArgs& a, hipStream_t s) {
+  return a.bf16 ? launch<BF16, D, RT, PAGED>(a, s) : launch<F16, D, RT, PAGED>(a, s);
+}
+template <int RT, bool PAGED>
+hipError_t launch_d(const AttnArgs& a, hipStream_t s) {
+  return a.head_dim == 128 ? launch_e<128, RT, PAGED>(a, s) : launch_e<64, RT, PAGED>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_attn_narrow(const AttnArgs& a, int rt, hipStream_t s) {
+  if (a.tables) return rt == 1 ? launch_d<1, true>(a, s) : launch_d<2, true>(a, s);
+  return rt == 1 ? launch_d<1, false>(a, s) : launch_d<2, false>(a, s);
+}
+
+}  // namespace qg

@@ -1,0 +1,443 @@
+// Attention for many query rows per key head: whole prompts over packed keys
+// and drafted trees over a paged cache.
+//
+// Mathematics as in attn_narrow.hip (query rows r = t * group + g, running
+// maximum and sums, powers of two).
+//
+// Bound: the matrix cores (2 * head_dim multiplications for each of the two
+// products a score), with the exponentials close behind.  A workgroup of four
+// waves takes 128 query rows and walks the keys in tiles of 64; a wave owns 32
+// rows and all keys of the tile.
+// - S^T = K Q^T by 32 x 32 x 16 products: K fragments from LDS, the wave's
+//   queries in registers.  A lane then holds 16 scores of ONE query row
+//   (lane % 32) per 32 keys, so maximum, exponentials and sum are lane-local;
+//   one swap joins the two lane halves.
+// - O^T = V^T P^T: the lane's scores of 16 keys, rounded, are its B operand as
+//   they stand (the product may take the keys in any order if both operands
+//   agree: half h of the lanes holds the keys 4 h + {0..3} and 8 + 4 h +
+//   {0..3}).  The A operand, 8 keys of one value column, comes from the
+//   row-major tile in LDS by transposing reads (4 keys of 16 columns each).
+//   The output sums are per lane of one query row too, so rescaling is a
+//   multiplication by a lane's own factor.
+// - K and V tiles go from global memory straight into LDS (16 bytes a lane, no
+//   registers), the next tile's while this one is computed.  A tile's row is
+//   stored in 16-byte pieces whose place is xor-ed with a permutation of the
+//   row's low bits, so that both the reads of one piece of many rows and the
+//   transposing reads of four neighbouring rows spread over the banks.
+#include "attn_common.hpp"
+
+namespace qg {
+namespace {
+
+constexpr int KB = 64;   // keys of a tile
+constexpr int WAVES = 4;
+constexpr int BM = 32 * WAVES;
+
+__device__ __forceinline__ f16v zero16() {
+  f16v z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+
+typedef short s4v __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s4v* lds_s4;
+
+// A segment: key tiles [u0, u1) of `units` of one item, and where the result
+// goes (slot < 0: the output).
+struct Segment {
+  Row r;
+  int b, h, tile, u0, u1;
+  int64_t slot;
+};
+
+template <typename E, int D>
+struct Tiles {
+  static constexpr int PC = D / 8;               // 16-byte pieces of a row
+  static constexpr int RPL = 64 / PC;            // rows of one wave-wide load
+  static constexpr int LOADS = KB / WAVES / RPL;  // loads per wave for one tile of K or V
+  static __device__ __forceinline__ int swz(int row) {
+    return D == 128 ? ((row & 3) << 2 | (row >> 2 & 3)) : ((row & 1) << 2 | (row >> 1 & 3));
+  }
+};
+
+template <typename E, int D, bool PAGED>
+__device__ __forceinline__ void run_segment(const AttnArgs& a, const Segment& g, const Partials<BM, D>& parts,
+                                            uint16_t (&ks)[2][KB * D], uint16_t (&vs)[2][KB * D], uint32_t* flag) {
+  using T = Tiles<E, D>;
+  constexpr int QS = D / 16;  // matrix steps along head_dim
+  constexpr int DB = D / 32;  // output blocks of 32 columns
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c32 = lane & 31, half = lane >> 5;
+  const Row& r = g.r;
+  const int rows = r.n * a.group;
+
+  // the wave's query rows, one per lane column
+  const int row = g.tile * BM + 32 * wave + c32;
+  const bool live = row < rows;
+  const int t = row / a.group, gh = row - t * a.group;
+  Sight<PAGED> sight;
+  sight.init(a, r, live ? t : r.n);
+  u4 qf[QS];
+  const uint16_t* q =
+      a.q + (live ? (int64_t)(r.q0 + t) * a.q_token + (int64_t)(g.h * a.group + gh) * a.q_head : 0);
+#pragma unroll
+  for (int s = 0; s < QS; ++s) {
+    qf[s] = u4{0, 0, 0, 0};
+    if (live) qf[s] = *reinterpret_cast<const u4*>(q + 16 * s + 8 * half);
+  }
+  const bool active = g.tile * BM + 32 * wave < rows;  // (wave-uniform)
+  // keys that every row of the tile sees, and the keys that any sees
+  const int t0 = g.tile * BM / a.group;
+  const int t1 = min((g.tile * BM + BM - 1) / a.group, r.n - 1);
+  int common, most;
+  if constexpr (PAGED) {
+    common = a.mask ? r.pos : r.pos + t0 + 1;
+    most = a.mask ? r.keys : r.pos + t1 + 1;
+  } else {
+    common = a.causal ? r.pos + t0 + 1 : r.keys;
+    most = a.causal ? r.pos + t1 + 1 : r.keys;
+  }
+  common = min(common, r.keys);
+  most = min(most, r.keys);
+  const int u1 = min(g.u1, (most + KB - 1) / KB);
+
+  // loads of tile u: wave w brings rows 16 w .. 16 w + 15
+  const uint16_t* kh = a.k + (int64_t)g.h * a.k_head;
+  const uint16_t* vh = a.v + (int64_t)g.h * a.v_head;
+  auto load = [&](int u, int buf) {
+    const int top = (r.keys - 1) & ~15;
+    const int kb = min(u * KB + 16 * wave, top);  // (rows past the last key are read from its place)
+    const int last = r.keys - 1 - kb;
+    int64_t tok;
+    if constexpr (PAGED) {
+      const int page = a.tables[(int64_t)g.b * a.max_pages + (kb >> a.page_shift)];
+      const int ok = (unsigned)page < (unsigned)a.pages ? page : 0;
+      tok = ((int64_t)ok << a.page_shift) + (kb & ((1 << a.page_shift) - 1));
+    } else {
+      tok = (int64_t)r.k0 + kb;
+    }
+    const uint16_t* kp = kh + tok * a.k_token;
+    const uint16_t* vp = vh + tok * a.v_token;
+#pragma unroll
+    for (int i = 0; i < T::LOADS; ++i) {
+      const int in = T::RPL * i + lane / T::PC;  // row in the wave's 16
+      const int piece = (lane % T::PC) ^ T::swz(in);
+      const int from = min(in, last);
+      typedef __attribute__((address_space(1))) const void* gp;
+      typedef __attribute__((address_space(3))) void* lp;
+      __builtin_amdgcn_global_load_lds((gp)(kp + (int64_t)from * a.k_token + 8 * piece),
+                                       (lp)&ks[buf][(16 * wave + T::RPL * i) * D], 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((gp)(vp + (int64_t)from * a.v_token + 8 * piece),
+                                       (lp)&vs[buf][(16 * wave + T::RPL * i) * D], 16, 0, 0);
+    }
+  };
+
+  f16v o[DB];
+#pragma unroll
+  for (int i = 0; i < DB; ++i) o[i] = zero16();
+  float m = NEG_INF, l = 0.f;
+
+  auto compute = [&](int u, int buf) {
+    const int kb = u * KB;
+    const bool masked = kb + KB > common;
+    uint64_t odd = 0;
+    if (masked) {
+      // A weight of 0 does not cancel a value that is infinite or NaN: find
+      // the keys that have one, clear it in LDS and add it further down for
+      // the rows that see it.
+      if (threadIdx.x < 2) flag[threadIdx.x] = 0;
+      __syncthreads();
+      // thread: a quarter of key threadIdx.x / 4's row
+      const int key = threadIdx.x >> 2;
+      u4* p = reinterpret_cast<u4*>(&vs[buf][key * D + (threadIdx.x & 3) * (D / 4)]);
+      uint32_t f = 0;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        u4 w = p[i];
+        uint32_t any = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x = nonfinite<E>(w[j]);
+          any |= x;
+          w[j] &= ~((x - (x >> 15)) | x);
+        }
+        if (any) p[i] = w;
+        f |= any;
+      }
+      if (f) atomicOr(&flag[key >> 5], 1u << (key & 31));
+      __syncthreads();
+      odd = (uint64_t)__builtin_amdgcn_readfirstlane(flag[1]) << 32 | __builtin_amdgcn_readfirstlane(flag[0]);
+    }
+    if (!active) return;
+
+    f16v sc[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      sc[x] = zero16();
+      const int krow = 32 * x + c32;
+#pragma unroll
+      for (int s = 0; s < QS; ++s) {
+        const u4 kf = *reinterpret_cast<const u4*>(&ks[buf][krow * D + 8 * ((2 * s + half) ^ T::swz(krow))]);
+        sc[x] = E::mfma32(kf, qf[s], sc[x]);
+      }
+    }
+    if (masked) {
+      const uint64_t seen = sight.window(a, r, kb) >> (4 * half);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[x][i] = seen >> (32 * x + 8 * (i / 4) + i % 4) & 1 ? sc[x][i] : NEG_INF;
+    }
+    float mx = NEG_INF;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[x][i]);
+    mx = half_max(mx);
+    mx = mx == NEG_INF ? NEG_INF : mx * a.scale;
+    if (__any(mx > m)) {
+      const float mn = fmaxf(m, mx), w = mn == NEG_INF ? 1.f : exp2_(m - mn);
+      m = mn;
+      l *= w;
+#pragma unroll
+      for (int i = 0; i < DB; ++i) o[i] *= w;
+    }
+    const float base = m == NEG_INF ? 0.f : m - E::LIFT;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float s = sc[x][i];
+        sc[x][i] = s == NEG_INF ? 0.f : exp2_(fmaf(s, a.scale, -base));
+        l += sc[x][i];
+      }
+    // lane in the 16-lane group of a transposing read: row i16 / 4 of the
+    // four, columns 4 (i16 % 4) .. of the group's 16
+    const int i16 = lane & 15, g2 = lane >> 4 & 1;
+#pragma unroll
+    for (int k4 = 0; k4 < 4; ++k4) {
+      const int x = k4 >> 1, e = 8 * (k4 & 1);
+      const u4 pf = u4{E::pack(sc[x][e], sc[x][e + 1]), E::pack(sc[x][e + 2], sc[x][e + 3]),
+                       E::pack(sc[x][e + 4], sc[x][e + 5]), E::pack(sc[x][e + 6], sc[x][e + 7])};
+#pragma unroll
+      for (int db = 0; db < DB; ++db) {
+        s4v v[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int vrow = 16 * k4 + 8 * y + 4 * half + (i16 >> 2);
+          const int piece = (4 * db + 2 * g2 + (i16 >> 1 & 1)) ^ T::swz(vrow);
+          v[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)&vs[buf][vrow * D + 8 * piece + 4 * (i16 & 1)]);
+        }
+        const u2 lo = __builtin_bit_cast(u2, v[0]), hi = __builtin_bit_cast(u2, v[1]);
+        o[db] = E::mfma32(u4{lo[0], lo[1], hi[0], hi[1]}, pf, o[db]);
+      }
+    }
+    if (odd) {
+      const uint64_t mine = sight.window(a, r, kb);
+      for (; odd; odd &= odd - 1) {
+        const int key = __builtin_ctzll(odd), at = min(kb + key, r.keys - 1);
+        int64_t tok;
+        if constexpr (PAGED) {
+          const int page = a.tables[(int64_t)g.b * a.max_pages + (at >> a.page_shift)];
+          tok = ((int64_t)((unsigned)page < (unsigned)a.pages ? page : 0) << a.page_shift) +
+                (at & ((1 << a.page_shift) - 1));
+        } else {
+          tok = (int64_t)r.k0 + at;
+        }
+        const uint16_t* v = vh + tok * a.v_token;
+        if (mine >> key & 1)
+#pragma unroll
+          for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint16_t y = v[32 * db + 8 * (i / 4) + 4 * half + i % 4];
+              if (nonfinite<E>(y) & 0x8000u) o[db][i] += E::value(y);
+            }
+      }
+    }
+  };
+
+  // tile u from buffer (u - u0) % 2: its loads were issued one tile ago; the
+  // barrier after the wait also says that every wave is past the tile before,
+  // whose buffer the next loads overwrite
+  if (g.u0 < u1) load(g.u0, 0);
+  for (int u = g.u0; u < u1; u += 2) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      if (u + y < u1) {
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0
+        __syncthreads();
+        if (u + y + 1 < u1) load(u + y + 1, y ^ 1);
+        compute(u + y, y);
+      }
+    }
+  }
+  __syncthreads();  // the buffers are free for the next segment
+
+  l = half_sum(l);
+  if (g.slot < 0) {
+    if (live) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint16_t* out = a.o + (int64_t)(r.q0 + t) * a.o_token + (int64_t)(g.h * a.group + gh) * a.o_head;
+#pragma unroll
+      for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<u2*>(out + 32 * db + 8 * i + 4 * half) =
+              u2{E::pack(o[db][4 * i] * inv, o[db][4 * i + 1] * inv),
+                 E::pack(o[db][4 * i + 2] * inv, o[db][4 * i + 3] * inv)};
+    }
+  } else if (live) {
+    const int pr = 32 * wave + c32;
+    float* po = parts.o_at(g.slot, pr);
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<f4*>(po + 32 * db + 8 * i + 4 * half) =
+            f4{o[db][4 * i], o[db][4 * i + 1], o[db][4 * i + 2], o[db][4 * i + 3]};
+    if (half == 0) {
+      float* ml = parts.ml_at(g.slot, pr);
+      ml[0] = m;
+      ml[1] = l;
+    }
+  }
+}
+
+// Packed prompts: one item (128-row tile and key head) per workgroup, or one
+// of `splits` parts of its keys.  The tiles of sequence b have the numbers from
+// rows_before(b) / 128 + b on, which is at least as many as it needs and can be
+// looked up without a sum over the sequences.
+__device__ __forceinline__ int first_tile(const AttnArgs& a, int b) {
+  return (int)((int64_t)a.cu[b] * a.group / BM) + b;
+}
+
+// tile number -> sequence and tile in it; false: no such tile
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, Row& r, int& b, int& in) {
+  b = find_row(a.rows, tile, [&](int i) { return first_tile(a, i); });
+  r = row_of<false>(a, b);
+  in = tile - first_tile(a, b);
+  return in >= 0 && (int64_t)in * BM < (int64_t)r.n * a.group;
+}
+
+// the part [u0, u1) of a tile's key tiles that split s takes
+__device__ __forceinline__ void split_range(const AttnArgs& a, const Row& r, int in, int splits, int s, int& u0,
+                                            int& u1) {
+  const int t1 = min((in * BM + BM - 1) / a.group, r.n - 1);
+  int most = a.causal ? r.pos + t1 + 1 : r.keys;
+  most = max(0, min(most, r.keys));
+  const int units = (most + KB - 1) / KB;
+  u0 = (int)((int64_t)units * s / splits);
+  u1 = (int)((int64_t)units * (s + 1) / splits);
+}
+
+template <typename E, int D>
+__global__ void __launch_bounds__(64 * WAVES, 2) attn_prompt_kernel(AttnArgs a, int tiles, int splits) {
+  __shared__ __attribute__((aligned(16))) uint16_t ks[2][KB * D], vs[2][KB * D];
+  __shared__ uint32_t flag[2];
+  Segment g;
+  // key head fastest: workgroups go to the XCDs round robin, so with 8 key
+  // heads each XCD's cache serves one head's keys and values.  Late tiles,
+  // which have the most keys under a causal mask, start first.
+  const int id = blockIdx.x;
+  g.h = id % a.heads_kv;
+  const int s = id / a.heads_kv % splits;
+  const int tile = tiles - 1 - id / a.heads_kv / splits;
+  if (!find_tile(a, tile, g.r, g.b, g.tile)) return;
+  split_range(a, g.r, g.tile, splits, s, g.u0, g.u1);
+  g.slot = splits == 1 ? -1 : ((int64_t)tile * a.heads_kv + g.h) * splits + s;
+  const Partials<BM, D> parts(a.ws, (int64_t)tiles * a.heads_kv * splits);
+  run_segment<E, D, false>(a, g, parts, ks, vs, flag);
+}
+
+// one wave: joins the parts of query token w / heads, head w % heads
+template <typename E, int D>
+__device__ __forceinline__ void join_prompt(const AttnArgs& a, int w, int tiles, int splits) {
+  const int token = w / a.heads, head = w - token * a.heads, h = head / a.group;
+  const int b = find_row(a.rows, token, [&](int i) { return a.cu[i]; });
+  const Row r = row_of<false>(a, b);
+  const int t = token - r.q0;
+  if (t < 0 || t >= r.n) return;
+  const int qr = t * a.group + head - h * a.group;
+  const int64_t tile = first_tile(a, b) + qr / BM;
+  const Partials<BM, D> parts(a.ws, (int64_t)tiles * a.heads_kv * splits);
+  join_row<E>(parts, qr % BM, splits, [&](int i) { return (tile * a.heads_kv + h) * splits + i; },
+              a.o + (int64_t)token * a.o_token + (int64_t)head * a.o_head);
+}
+
+template <typename E, int D>
+__global__ void __launch_bounds__(256) attn_prompt_join_kernel(AttnArgs a, int tiles, int splits) {
+  const int n = a.tokens * a.heads;
+  for (int64_t w = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6)); w < n; w += (int64_t)gridDim.x * 4)
+    join_prompt<E, D>(a, (int)w, tiles, splits);
+}
+
+// Trees over the paged cache: the units of all items shared out evenly
+// (Units), so rows of very different lengths keep every workgroup busy.
+template <typename E, int D>
+__global__ void __launch_bounds__(64 * WAVES, 2) attn_tree_kernel(AttnArgs a, int workgroups, int least) {
+  using U = Units<BM, KB, true>;
+  __shared__ __attribute__((aligned(16))) uint16_t ks[2][KB * D], vs[2][KB * D];
+  __shared__ uint32_t flag[2];
+  const Split sp = U::split(a, workgroups, least);
+  const int64_t u_begin = (int64_t)blockIdx.x * sp.per;
+  const int64_t u_end = u_begin + sp.per < sp.total ? u_begin + sp.per : sp.total;
+  const Partials<BM, D> parts(a.ws, 2 * (int64_t)workgroups);
+  for (int64_t u = u_begin; u < u_end;) {
+    const Place at = U::place(a, u);
+    Segment g;
+    g.b = at.b;
+    g.r = row_of<true>(a, at.b);
+    const int per_item = U::units(g.r);
+    const int64_t item = (u - at.first) / per_item;
+    const int64_t left = u_end - u;
+    g.u0 = (int)(u - at.first - item * per_item);
+    g.u1 = (int)(g.u0 + left < per_item ? g.u0 + left : per_item);
+    g.h = (int)(item % a.heads_kv);
+    g.tile = (int)(item / a.heads_kv);
+    const int next = g.u1;
+    g.slot = g.u0 == 0 && g.u1 == per_item ? -1 : 2 * (int64_t)blockIdx.x + (u != u_begin);
+    u += next - g.u0;
+    run_segment<E, D, true>(a, g, parts, ks, vs, flag);
+  }
+}
+
+template <typename E, int D>
+__global__ void __launch_bounds__(256) attn_tree_join_kernel(AttnArgs a, int workgroups, int least) {
+  using U = Units<BM, KB, true>;
+  const int n = a.tokens * a.heads;
+  for (int64_t w = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6)); w < n; w += (int64_t)gridDim.x * 4)
+    U::template join<E, D>(a, (int)w, workgroups, least);
+}
+
+template <typename E, int D>
+hipError_t prompt(const AttnArgs& a, hipStream_t s) {
+  const int tiles = prompt_tiles(a.tokens, a.rows, a.group);
+  const int splits = prompt_splits(a.tokens, a.tokens_k, a.rows, a.heads_kv, a.group);
+  const int64_t grid = (int64_t)tiles * a.heads_kv * splits;
+  hipLaunchKernelGGL((attn_prompt_kernel<E, D>), dim3((unsigned)grid), dim3(64 * WAVES), 0, s, a, tiles, splits);
+  if (splits > 1)
+    hipLaunchKernelGGL((attn_prompt_join_kernel<E, D>), dim3(join_blocks(a)), dim3(256), 0, s, a, tiles, splits);
+  return hipGetLastError();
+}
+
+template <typename E, int D>
+hipError_t tree(const AttnArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((attn_tree_kernel<E, D>), dim3(WIDE_WORKGROUPS), dim3(64 * WAVES), 0, s, a, WIDE_WORKGROUPS, 1);
+  hipLaunchKernelGGL((attn_tree_join_kernel<E, D>), dim3(join_blocks(a)), dim3(256), 0, s, a, WIDE_WORKGROUPS, 1);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_wide(const AttnArgs& a, hipStream_t s) {
+  if (a.tables) {
+    if (a.head_dim == 128) return a.bf16 ? tree<BF16, 128>(a, s) : tree<F16, 128>(a, s);
+    return a.bf16 ? tree<BF16, 64>(a, s) : tree<F16, 64>(a, s);
+  }
+  if (a.head_dim == 128) return a.bf16 ? prompt<BF16, 128>(a, s) : prompt<F16, 128>(a, s);
+  return a.bf16 ? prompt<BF16, 64>(a, s) : prompt<F16, 64>(a, s);
+}
+
+}  // namespace qg

@@ -10,6 +10,9 @@ namespace qg {
 // QGEMV_TUNING was set at the process's first call (api.cpp).
 const char* tune_env(const char* name);
 
+// The status of a HIP result; keeps the error for qgemv_last_hip_error (api.cpp).
+int hip_status(hipError_t e);
+
 struct UniformArgs {
   int bits, M, N, K;
   const uint16_t* x;
