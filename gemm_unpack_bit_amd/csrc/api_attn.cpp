@@ -29,6 +29,7 @@ Span span(const qgemv_heads& x, int tokens, int heads, int dim) {
 }
 
 constexpr int64_t STRIDE_MAX = (int64_t)1 << 40;  // (products with 32-bit counts stay in 64 bits once checked)
+constexpr int64_t KEY_STRIDE_MAX = (int64_t)1 << 26;  // 16 keys of a tile lie within 32-bit offsets of one another
 
 // strides in range and, for an output, no element shared
 int check_heads(const qgemv_heads& x, int tokens, int heads, int dim, bool output) {
@@ -76,7 +77,7 @@ int check_cache(const qgemv_kv_cache* c, bool state) {
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return QGEMV_ERR_UNSUPPORTED;
   if (c->layers < 1 || c->pages < 1 || c->heads_kv < 1 || c->rows < 0 || c->rows > 65535 || c->max_pages < 1)
     return QGEMV_ERR_SHAPE;
-  if ((int64_t)c->max_pages * c->page_size >= (int64_t)1 << 31 || c->heads_kv > 65536 || c->layers > 65536 ||
+  if ((int64_t)c->max_pages * c->page_size >= (int64_t)1 << 31 || (int64_t)c->heads_kv * c->head_dim >= KEY_STRIDE_MAX || c->layers > 65536 ||
       (double)c->layers * c->pages * c->page_size * c->heads_kv * c->head_dim >= 1e15 ||
       (int64_t)c->layers * c->heads_kv * c->head_dim >= (int64_t)1 << 32)  // (a launch's threads: a thread per 16 bytes)
     return QGEMV_ERR_SHAPE;
@@ -154,6 +155,7 @@ int qgemv_attn_prompt(int dtype, int causal, int tokens, int tokens_k, int batch
   if ((rc = check_heads(*q, tokens, heads, head_dim, false)) || (rc = check_heads(*k, tokens_k, heads_kv, head_dim, false)) ||
       (rc = check_heads(*v, tokens_k, heads_kv, head_dim, false)) || (rc = check_heads(*o, tokens, heads, head_dim, true)))
     return rc;
+  if (k->token >= KEY_STRIDE_MAX || v->token >= KEY_STRIDE_MAX) return QGEMV_ERR_SHAPE;
   if ((rc = check_scale(scale))) return rc;
   if (!aligned_heads(*q) || !aligned_heads(*k) || !aligned_heads(*v) || !aligned_heads(*o) || !aligned(cu_q, 4) ||
       !aligned(cu_k, 4))

@@ -15,12 +15,16 @@ typedef float f2v __attribute__((ext_vector_type(2)));
 // Element types.  LIFT: the softmax weights are held 2^LIFT times too large, as
 // are their sums, which cancels in the quotient; in fp16, whose normal numbers
 // end at 2^-14, weights down to 2^-24 of the largest then keep all their bits.
+// SLACK: the weights' reference m may lie that far (in powers of two) below the
+// largest score before sums are rescaled to a new one, so that after the first
+// few tiles they hardly ever are; the largest weight, 2^(LIFT + SLACK), still
+// is a normal fp16 number.
 // pack rounds two floats to nearest even; NONFINITE_* find
 // halves whose exponent is all ones: ((w & EXP) + ONE) has bit 15 of such a
 // half set, and the addition never carries into the next half.
 struct F16 {
   static constexpr uint32_t EXP = 0x7C007C00u, ONE = 0x04000400u;
-  static constexpr float LIFT = 10.f;
+  static constexpr float LIFT = 10.f, SLACK = 5.f;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2v{a, b}, h2));
   }
@@ -34,7 +38,7 @@ struct F16 {
 };
 struct BF16 {
   static constexpr uint32_t EXP = 0x7F807F80u, ONE = 0x00800080u;
-  static constexpr float LIFT = 0.f;
+  static constexpr float LIFT = 0.f, SLACK = 8.f;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2v{a, b}, b2v));
   }
@@ -70,6 +74,21 @@ __device__ __forceinline__ float quarter_max(float v) {
   const uint32_t u = __float_as_uint(half_max(v));
   const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
   return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+
+// The kernel's AttnArgs (its first argument), read again from the argument
+// segment: code outside a hot loop takes its fields from here, so that they do
+// not occupy scalar registers during the loop.
+__device__ __forceinline__ AttnArgs args_again() {
+  typedef __attribute__((address_space(4))) const uint32_t* words;
+  words p = (words)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  struct W {
+    uint32_t w[sizeof(AttnArgs) / 4];
+  } x;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(AttnArgs) / 4; ++i) x.w[i] = p[i];
+  return __builtin_bit_cast(AttnArgs, x);
 }
 
 // One row (sequence) as the kernels see it.

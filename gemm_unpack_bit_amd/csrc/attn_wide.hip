@@ -24,6 +24,8 @@
 //   stored in 16-byte pieces whose place is xor-ed with a permutation of the
 //   row's low bits, so that both the reads of one piece of many rows and the
 //   transposing reads of four neighbouring rows spread over the banks.
+#include <type_traits>
+
 #include "attn_common.hpp"
 
 namespace qg {
@@ -51,25 +53,33 @@ struct Segment {
   int64_t slot;
 };
 
-template <typename E, int D>
+template <int D>
 struct Tiles {
-  static constexpr int PC = D / 8;               // 16-byte pieces of a row
-  static constexpr int RPL = 64 / PC;            // rows of one wave-wide load
+  static constexpr int PC = D / 8;                // 16-byte pieces of a row
+  static constexpr int RPL = 64 / PC;             // rows of one wave-wide load
   static constexpr int LOADS = KB / WAVES / RPL;  // loads per wave for one tile of K or V
   static __device__ __forceinline__ int swz(int row) {
     return D == 128 ? ((row & 3) << 2 | (row >> 2 & 3)) : ((row & 1) << 2 | (row >> 1 & 3));
   }
 };
 
+// K and V tiles, two buffers each: separate arrays, so that reading one does
+// not wait for loads into another
+template <int D>
+struct __attribute__((aligned(16))) Buffers {
+  uint16_t t[KB * D];
+};
+
 template <typename E, int D, bool PAGED>
-__device__ __forceinline__ void run_segment(const AttnArgs& a, const Segment& g, const Partials<BM, D>& parts,
-                                            uint16_t (&ks)[2][KB * D], uint16_t (&vs)[2][KB * D], uint32_t* flag) {
-  using T = Tiles<E, D>;
+__device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buffers<D>& k0, Buffers<D>& k1, Buffers<D>& v0,
+                                            Buffers<D>& v1, uint32_t* flag) {
+  const AttnArgs a = args_again();
+  using T = Tiles<D>;
   constexpr int QS = D / 16;  // matrix steps along head_dim
   constexpr int DB = D / 32;  // output blocks of 32 columns
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c32 = lane & 31, half = lane >> 5;
-  const Row& r = g.r;
+  const Row r = g.r;
   const int rows = r.n * a.group;
 
   // the wave's query rows, one per lane column
@@ -100,103 +110,89 @@ __device__ __forceinline__ void run_segment(const AttnArgs& a, const Segment& g,
   }
   common = min(common, r.keys);
   most = min(most, r.keys);
-  const int u1 = min(g.u1, (most + KB - 1) / KB);
+  const int u0 = g.u0, u1 = min(g.u1, (most + KB - 1) / KB);
 
-  // loads of tile u: wave w brings rows 16 w .. 16 w + 15
+  // Loads of a tile: wave w brings rows 16 w .. 16 w + 15 of it, 16 rows of
+  // one page.  A lane's place in them is a 32-bit offset, the same for every
+  // tile but one that reaches past the row's last key, whose missing rows are
+  // read from the last key's place.
   const uint16_t* kh = a.k + (int64_t)g.h * a.k_head;
   const uint16_t* vh = a.v + (int64_t)g.h * a.v_head;
-  auto load = [&](int u, int buf) {
-    const int top = (r.keys - 1) & ~15;
-    const int kb = min(u * KB + 16 * wave, top);  // (rows past the last key are read from its place)
-    const int last = r.keys - 1 - kb;
-    int64_t tok;
+  const int top = (r.keys - 1) & ~15;
+  auto tok_of = [&](int u) -> int64_t {  // pool or array token of the wave's first row
+    const int kb = min(u * KB + 16 * wave, top);
     if constexpr (PAGED) {
       const int page = a.tables[(int64_t)g.b * a.max_pages + (kb >> a.page_shift)];
       const int ok = (unsigned)page < (unsigned)a.pages ? page : 0;
-      tok = ((int64_t)ok << a.page_shift) + (kb & ((1 << a.page_shift) - 1));
+      return ((int64_t)ok << a.page_shift) + (kb & ((1 << a.page_shift) - 1));
     } else {
-      tok = (int64_t)r.k0 + kb;
+      return (int64_t)r.k0 + kb;
     }
-    const uint16_t* kp = kh + tok * a.k_token;
-    const uint16_t* vp = vh + tok * a.v_token;
+  };
+  typedef __attribute__((address_space(1))) const void* gp;
+  typedef __attribute__((address_space(3))) void* lp;
+  auto lane_off = [&](int i, int64_t token, int last) -> uint32_t {  // bytes
+    const int in = T::RPL * i + lane / T::PC;  // row in the wave's 16
+    return 2u * ((uint32_t)min(in, last) * (uint32_t)token + 8u * (uint32_t)((lane % T::PC) ^ T::swz(in)));
+  };
+  auto put = [&](const uint16_t* base, uint32_t off, int i, Buffers<D>& buf) {
+    __builtin_amdgcn_global_load_lds((gp)(reinterpret_cast<const char*>(base) + off),
+                                     (lp)&buf.t[(16 * wave + T::RPL * i) * D], 16, 0, 0);
+  };
+  auto load = [&](const uint16_t* base, int64_t token, int u, Buffers<D>& buf) {
+    const int last = (u + 1) * KB <= r.keys ? 15 : r.keys - 1 - min(u * KB + 16 * wave, top);
 #pragma unroll
-    for (int i = 0; i < T::LOADS; ++i) {
-      const int in = T::RPL * i + lane / T::PC;  // row in the wave's 16
-      const int piece = (lane % T::PC) ^ T::swz(in);
-      const int from = min(in, last);
-      typedef __attribute__((address_space(1))) const void* gp;
-      typedef __attribute__((address_space(3))) void* lp;
-      __builtin_amdgcn_global_load_lds((gp)(kp + (int64_t)from * a.k_token + 8 * piece),
-                                       (lp)&ks[buf][(16 * wave + T::RPL * i) * D], 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((gp)(vp + (int64_t)from * a.v_token + 8 * piece),
-                                       (lp)&vs[buf][(16 * wave + T::RPL * i) * D], 16, 0, 0);
+    for (int i = 0; i < T::LOADS; ++i) put(base, lane_off(i, token, last), i, buf);
+  };
+
+  // A lane's places in a tile, in bytes.  K fragments: row lane % 32 (+ 32 x),
+  // piece 2 s + half, so k_at ^ 32 s; transposing reads of V: row 4 half + i16
+  // / 4 (+ 8 y + 16 k4) with i16 = lane % 16, columns 4 (i16 % 4) .. of the 16
+  // of the lane's group (+ 32 db), so v_at[y] ^ 64 db.  The compiler is kept
+  // from holding each of these in a register of its own.
+  uint32_t k_at, v_at[2];
+  {
+    const int i16 = lane & 15, g2 = lane >> 4 & 1;
+    k_at = 2 * D * c32 + 16 * (half ^ T::swz(c32));
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int vrow = 8 * y + 4 * half + (i16 >> 2);
+      v_at[y] = 2 * D * vrow + 16 * ((2 * g2 + (i16 >> 1 & 1)) ^ T::swz(vrow)) + 8 * (i16 & 1);
+    }
+  }
+
+  // S^T of a tile
+  auto scores = [&](const Buffers<D>& kt, f16v (&sc)[2]) {
+    const char* base = reinterpret_cast<const char*>(kt.t);
+    uint32_t at = k_at;
+    asm volatile("" : "+v"(at));
+#pragma unroll
+    for (int s = 0; s < QS; ++s) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const u4 kf = *reinterpret_cast<const u4*>(base + (at ^ (32 * s)) + 2 * D * 32 * x);
+        sc[x] = E::mfma32(kf, qf[s], s == 0 ? zero16() : sc[x]);
+      }
     }
   };
 
   f16v o[DB];
 #pragma unroll
   for (int i = 0; i < DB; ++i) o[i] = zero16();
-  float m = NEG_INF, l = 0.f;
+  const float scale = a.scale;
+  float m = NEG_INF, l = 0.f;  // m: the weights' reference, at most E::SLACK below the largest score
 
-  auto compute = [&](int u, int buf) {
-    const int kb = u * KB;
-    const bool masked = kb + KB > common;
-    uint64_t odd = 0;
-    if (masked) {
-      // A weight of 0 does not cancel a value that is infinite or NaN: find
-      // the keys that have one, clear it in LDS and add it further down for
-      // the rows that see it.
-      if (threadIdx.x < 2) flag[threadIdx.x] = 0;
-      __syncthreads();
-      // thread: a quarter of key threadIdx.x / 4's row
-      const int key = threadIdx.x >> 2;
-      u4* p = reinterpret_cast<u4*>(&vs[buf][key * D + (threadIdx.x & 3) * (D / 4)]);
-      uint32_t f = 0;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        u4 w = p[i];
-        uint32_t any = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t x = nonfinite<E>(w[j]);
-          any |= x;
-          w[j] &= ~((x - (x >> 15)) | x);
-        }
-        if (any) p[i] = w;
-        f |= any;
-      }
-      if (f) atomicOr(&flag[key >> 5], 1u << (key & 31));
-      __syncthreads();
-      odd = (uint64_t)__builtin_amdgcn_readfirstlane(flag[1]) << 32 | __builtin_amdgcn_readfirstlane(flag[0]);
-    }
-    if (!active) return;
-
-    f16v sc[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      sc[x] = zero16();
-      const int krow = 32 * x + c32;
-#pragma unroll
-      for (int s = 0; s < QS; ++s) {
-        const u4 kf = *reinterpret_cast<const u4*>(&ks[buf][krow * D + 8 * ((2 * s + half) ^ T::swz(krow))]);
-        sc[x] = E::mfma32(kf, qf[s], sc[x]);
-      }
-    }
-    if (masked) {
-      const uint64_t seen = sight.window(a, r, kb) >> (4 * half);
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sc[x][i] = seen >> (32 * x + 8 * (i / 4) + i % 4) & 1 ? sc[x][i] : NEG_INF;
-    }
-    float mx = NEG_INF;
+  // the tile's scores into weights, and O^T += V^T P^T; with `some` there may
+  // be unseen keys among them, at -inf (whose product with a scale of 0 is not)
+  auto weigh = [&](const Buffers<D>& vt, f16v (&sc)[2], auto some) {
+    float mx = sc[0][0];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[x][i]);
     mx = half_max(mx);
-    mx = mx == NEG_INF ? NEG_INF : mx * a.scale;
-    if (__any(mx > m)) {
+    mx = mx == NEG_INF ? NEG_INF : mx * scale;
+    if (__any(mx > m + E::SLACK)) {
       const float mn = fmaxf(m, mx), w = mn == NEG_INF ? 1.f : exp2_(m - mn);
       m = mn;
       l *= w;
@@ -204,82 +200,181 @@ __device__ __forceinline__ void run_segment(const AttnArgs& a, const Segment& g,
       for (int i = 0; i < DB; ++i) o[i] *= w;
     }
     const float base = m == NEG_INF ? 0.f : m - E::LIFT;
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float s = sc[x][i];
-        sc[x][i] = s == NEG_INF ? 0.f : exp2_(fmaf(s, a.scale, -base));
-        l += sc[x][i];
-      }
-    // lane in the 16-lane group of a transposing read: row i16 / 4 of the
-    // four, columns 4 (i16 % 4) .. of the group's 16
-    const int i16 = lane & 15, g2 = lane >> 4 & 1;
+    const char* vb = reinterpret_cast<const char*>(vt.t);
+    uint32_t at[2] = {v_at[0], v_at[1]};
+    asm volatile("" : "+v"(at[0]), "+v"(at[1]));
 #pragma unroll
     for (int k4 = 0; k4 < 4; ++k4) {
       const int x = k4 >> 1, e = 8 * (k4 & 1);
-      const u4 pf = u4{E::pack(sc[x][e], sc[x][e + 1]), E::pack(sc[x][e + 2], sc[x][e + 3]),
-                       E::pack(sc[x][e + 4], sc[x][e + 5]), E::pack(sc[x][e + 6], sc[x][e + 7])};
+      float p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = exp2_(fmaf(sc[x][e + i], scale, -base));
+        if constexpr (decltype(some)::value) p[i] = sc[x][e + i] == NEG_INF ? 0.f : p[i];
+        l += p[i];
+      }
+      const u4 pf = u4{E::pack(p[0], p[1]), E::pack(p[2], p[3]), E::pack(p[4], p[5]), E::pack(p[6], p[7])};
 #pragma unroll
       for (int db = 0; db < DB; ++db) {
         s4v v[2];
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int vrow = 16 * k4 + 8 * y + 4 * half + (i16 >> 2);
-          const int piece = (4 * db + 2 * g2 + (i16 >> 1 & 1)) ^ T::swz(vrow);
-          v[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)&vs[buf][vrow * D + 8 * piece + 4 * (i16 & 1)]);
-        }
+        for (int y = 0; y < 2; ++y)
+          v[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(vb + (at[y] ^ (64 * db)) + 2 * D * 16 * k4));
         const u2 lo = __builtin_bit_cast(u2, v[0]), hi = __builtin_bit_cast(u2, v[1]);
         o[db] = E::mfma32(u4{lo[0], lo[1], hi[0], hi[1]}, pf, o[db]);
       }
     }
-    if (odd) {
-      const uint64_t mine = sight.window(a, r, kb);
-      for (; odd; odd &= odd - 1) {
-        const int key = __builtin_ctzll(odd), at = min(kb + key, r.keys - 1);
-        int64_t tok;
-        if constexpr (PAGED) {
-          const int page = a.tables[(int64_t)g.b * a.max_pages + (at >> a.page_shift)];
-          tok = ((int64_t)((unsigned)page < (unsigned)a.pages ? page : 0) << a.page_shift) +
-                (at & ((1 << a.page_shift) - 1));
-        } else {
-          tok = (int64_t)r.k0 + at;
-        }
-        const uint16_t* v = vh + tok * a.v_token;
-        if (mine >> key & 1)
+  };
+
+  // A weight of 0 does not cancel a value that is infinite or NaN: in a tile
+  // with unseen keys, find the keys that have one and clear it in LDS; the
+  // whole workgroup, returns the keys.  Thread: a quarter of a key's row.
+  auto odd_keys = [&](Buffers<D>& vt) -> uint64_t {
+    if (threadIdx.x < 2) flag[threadIdx.x] = 0;
+    __syncthreads();
+    const int key = threadIdx.x >> 2;
+    u4* p = reinterpret_cast<u4*>(&vt.t[key * D + (threadIdx.x & 3) * (D / 4)]);
+    uint32_t f = 0;
 #pragma unroll
-          for (int db = 0; db < DB; ++db)
+    for (int i = 0; i < D / 32; ++i) {
+      u4 w = p[i];
+      uint32_t any = 0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint16_t y = v[32 * db + 8 * (i / 4) + 4 * half + i % 4];
-              if (nonfinite<E>(y) & 0x8000u) o[db][i] += E::value(y);
-            }
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t x = nonfinite<E>(w[j]);
+        any |= x;
+        w[j] &= ~((x - (x >> 15)) | x);
       }
+      if (any) p[i] = w;
+      f |= any;
+    }
+    if (f) atomicOr(&flag[key >> 5], 1u << (key & 31));
+    __syncthreads();
+    return (uint64_t)__builtin_amdgcn_readfirstlane(flag[1]) << 32 | __builtin_amdgcn_readfirstlane(flag[0]);
+  };
+  // ... and add them for the rows that see them
+  auto add_odd = [&](uint64_t odd, int kb) {
+    const AttnArgs a = args_again();
+    const uint16_t* vh = a.v + (int64_t)g.h * a.v_head;
+    const uint64_t mine = sight.window(a, r, kb);
+    for (; odd; odd &= odd - 1) {
+      const int key = __builtin_ctzll(odd), at = min(kb + key, r.keys - 1);
+      int64_t tok;
+      if constexpr (PAGED) {
+        const int page = a.tables[(int64_t)g.b * a.max_pages + (at >> a.page_shift)];
+        tok = ((int64_t)((unsigned)page < (unsigned)a.pages ? page : 0) << a.page_shift) +
+              (at & ((1 << a.page_shift) - 1));
+      } else {
+        tok = (int64_t)r.k0 + at;
+      }
+      const uint16_t* v = vh + tok * a.v_token;
+      if (mine >> key & 1)
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint16_t y = v[32 * db + 8 * (i / 4) + 4 * half + i % 4];
+            if (nonfinite<E>(y) & 0x8000u) o[db][i] += E::value(y);
+          }
     }
   };
 
-  // tile u from buffer (u - u0) % 2: its loads were issued one tile ago; the
-  // barrier after the wait also says that every wave is past the tile before,
-  // whose buffer the next loads overwrite
-  if (g.u0 < u1) load(g.u0, 0);
-  for (int u = g.u0; u < u1; u += 2) {
+  // Pipeline.  Step u: the scores of tile u + 1 (matrix cores), then the
+  // weights and output sums of tile u, whose scores the step before left.
+  // K of tile u + 1 and V of tile u were asked for one step ago; the barrier
+  // after the wait also says that every wave is past step u - 1, so K of tile
+  // u + 2 may go where tile u's was and V of tile u + 1 where tile u - 1's was.
+  auto arrived = [&]() {
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0
+    lds_barrier();
+  };
+  // any step
+  auto step = [&](int u, Buffers<D>& k_now, Buffers<D>& k_next, Buffers<D>& v_now, Buffers<D>& v_next,
+                  f16v (&cur)[2], f16v (&next)[2]) {
+    const AttnArgs a = args_again();
+    const uint16_t* kh = a.k + (int64_t)g.h * a.k_head;
+    const uint16_t* vh = a.v + (int64_t)g.h * a.v_head;
+    arrived();
+    if (u + 2 < u1) load(kh + tok_of(u + 2) * a.k_token, a.k_token, u + 2, k_now);
+    if (u + 1 < u1) load(vh + tok_of(u + 1) * a.v_token, a.v_token, u + 1, v_next);
+    const int kb = u * KB;
+    const bool masked = kb + KB > common;
+    uint64_t odd = 0;
+    if (masked) odd = odd_keys(v_now);
+    if (active) {
+      if (u + 1 < u1) scores(k_next, next);
+      if (masked) {
+        const AttnArgs a = args_again();
+        const uint64_t seen = sight.window(a, r, kb) >> (4 * half);
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      if (u + y < u1) {
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0
-        __syncthreads();
-        if (u + y + 1 < u1) load(u + y + 1, y ^ 1);
-        compute(u + y, y);
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) cur[x][i] = seen >> (32 * x + 8 * (i / 4) + i % 4) & 1 ? cur[x][i] : NEG_INF;
+      }
+      weigh(v_now, cur, std::true_type{});
+      if (odd) add_odd(odd, kb);
+    }
+  };
+
+  if (u0 < u1) {
+    f16v sa[2], sb[2];
+    const int64_t tok0 = tok_of(u0);
+    load(kh + tok0 * a.k_token, a.k_token, u0, k0);
+    if (u0 + 1 < u1) load(kh + tok_of(u0 + 1) * a.k_token, a.k_token, u0 + 1, k1);
+    load(vh + tok0 * a.v_token, a.v_token, u0, v0);
+    arrived();
+    if (active) scores(k0, sa);
+    // steps whose tile every row sees in full, and whose loads are of whole
+    // tiles: two at a time (the waves without rows compute along, on zeros)
+    int uf = min(min(common / KB, u1 - 2), r.keys / KB - 2);
+    uf = u0 + ((uf - u0) & ~1);
+    int u = u0;
+    if (u < uf) {
+      uint32_t ko[T::LOADS], vo[T::LOADS];
+#pragma unroll
+      for (int i = 0; i < T::LOADS; ++i) {
+        ko[i] = lane_off(i, a.k_token, 15);
+        vo[i] = lane_off(i, a.v_token, 15);
+      }
+      // (the tokens of the next loads are looked up a step ahead)
+      int64_t tok1 = tok_of(u + 1), tok2 = tok_of(u + 2);
+      auto fast = [&](Buffers<D>& k_now, Buffers<D>& k_next, Buffers<D>& v_now, Buffers<D>& v_next, f16v (&cur)[2],
+                      f16v (&next)[2]) {
+        arrived();
+        const uint16_t* kp = kh + tok2 * a.k_token;
+        const uint16_t* vp = vh + tok1 * a.v_token;
+#pragma unroll
+        for (int i = 0; i < T::LOADS; ++i) {
+          asm volatile("" : "+v"(ko[i]), "+v"(vo[i]));  // (kept as 32-bit offsets of a scalar base)
+          put(kp, ko[i], i, k_now);
+        }
+#pragma unroll
+        for (int i = 0; i < T::LOADS; ++i) put(vp, vo[i], i, v_next);
+        tok1 = tok2;
+        tok2 = tok_of(u + 3);
+        ++u;
+        scores(k_next, next);
+        weigh(v_now, cur, std::false_type{});
+      };
+      while (u < uf) {
+        fast(k0, k1, v0, v1, sa, sb);
+        fast(k1, k0, v1, v0, sb, sa);
       }
     }
+    for (; u < u1; u += 2) {
+      step(u, k0, k1, v0, v1, sa, sb);
+      if (u + 1 < u1) step(u + 1, k1, k0, v1, v0, sb, sa);
+    }
+    lds_barrier();  // the buffers are free for the next segment
   }
-  __syncthreads();  // the buffers are free for the next segment
 
   l = half_sum(l);
+  if (!live) return;
+  const AttnArgs e = args_again();
+  const int t_ = row / e.group, g_ = row - t_ * e.group;
   if (g.slot < 0) {
-    if (live) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      uint16_t* out = a.o + (int64_t)(r.q0 + t) * a.o_token + (int64_t)(g.h * a.group + gh) * a.o_head;
+      uint16_t* out = e.o + (int64_t)(r.q0 + t_) * e.o_token + (int64_t)(g.h * e.group + g_) * e.o_head;
 #pragma unroll
       for (int db = 0; db < DB; ++db)
 #pragma unroll
@@ -287,8 +382,8 @@ __device__ __forceinline__ void run_segment(const AttnArgs& a, const Segment& g,
           *reinterpret_cast<u2*>(out + 32 * db + 8 * i + 4 * half) =
               u2{E::pack(o[db][4 * i] * inv, o[db][4 * i + 1] * inv),
                  E::pack(o[db][4 * i + 2] * inv, o[db][4 * i + 3] * inv)};
-    }
-  } else if (live) {
+  } else {
+    const Partials<BM, D> parts(e.ws, slots);
     const int pr = 32 * wave + c32;
     float* po = parts.o_at(g.slot, pr);
 #pragma unroll
@@ -334,7 +429,7 @@ __device__ __forceinline__ void split_range(const AttnArgs& a, const Row& r, int
 
 template <typename E, int D>
 __global__ void __launch_bounds__(64 * WAVES, 2) attn_prompt_kernel(AttnArgs a, int tiles, int splits) {
-  __shared__ __attribute__((aligned(16))) uint16_t ks[2][KB * D], vs[2][KB * D];
+  __shared__ Buffers<D> k0, k1, v0, v1;
   __shared__ uint32_t flag[2];
   Segment g;
   // key head fastest: workgroups go to the XCDs round robin, so with 8 key
@@ -347,8 +442,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_prompt_kernel(AttnArgs a, 
   if (!find_tile(a, tile, g.r, g.b, g.tile)) return;
   split_range(a, g.r, g.tile, splits, s, g.u0, g.u1);
   g.slot = splits == 1 ? -1 : ((int64_t)tile * a.heads_kv + g.h) * splits + s;
-  const Partials<BM, D> parts(a.ws, (int64_t)tiles * a.heads_kv * splits);
-  run_segment<E, D, false>(a, g, parts, ks, vs, flag);
+  run_segment<E, D, false>(g, (int64_t)tiles * a.heads_kv * splits, k0, k1, v0, v1, flag);
 }
 
 // one wave: joins the parts of query token w / heads, head w % heads
@@ -378,12 +472,11 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(AttnArgs a, int t
 template <typename E, int D>
 __global__ void __launch_bounds__(64 * WAVES, 2) attn_tree_kernel(AttnArgs a, int workgroups, int least) {
   using U = Units<BM, KB, true>;
-  __shared__ __attribute__((aligned(16))) uint16_t ks[2][KB * D], vs[2][KB * D];
+  __shared__ Buffers<D> k0, k1, v0, v1;
   __shared__ uint32_t flag[2];
   const Split sp = U::split(a, workgroups, least);
   const int64_t u_begin = (int64_t)blockIdx.x * sp.per;
   const int64_t u_end = u_begin + sp.per < sp.total ? u_begin + sp.per : sp.total;
-  const Partials<BM, D> parts(a.ws, 2 * (int64_t)workgroups);
   for (int64_t u = u_begin; u < u_end;) {
     const Place at = U::place(a, u);
     Segment g;
@@ -399,7 +492,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_tree_kernel(AttnArgs a, in
     const int next = g.u1;
     g.slot = g.u0 == 0 && g.u1 == per_item ? -1 : 2 * (int64_t)blockIdx.x + (u != u_begin);
     u += next - g.u0;
-    run_segment<E, D, true>(a, g, parts, ks, vs, flag);
+    run_segment<E, D, true>(g, 2 * (int64_t)workgroups, k0, k1, v0, v1, flag);
   }
 }
 

@@ -69,7 +69,7 @@ typedef struct {
  *
  * Checks, in order: null, dtype / head_dim (UNSUPPORTED), shape (counts not
  * negative, heads % heads_kv, strides, tokens * heads < 2^31 and about
- * tokens * heads / 128 + batch * heads_kv < 2^24), alignment,
+ * tokens * heads / 128 + batch * heads_kv < 2^24, k's and v's token strides < 2^26), alignment,
  * o overlapping an input (VALUE), workspace.  o's elements must not overlap
  * each other (SHAPE).  tokens or batch of 0 does nothing.
  * ------------------------------------------------------------------------ */
