@@ -59,11 +59,15 @@ int check_counts(int tokens, int rows, int heads, int heads_kv) {
   return QGEMV_OK;
 }
 
-// workgroups of the wide prompt kernel (0 where it is not the one that runs)
-int64_t prompt_grid(int tokens, int tokens_k, int rows, int heads, int heads_kv) {
+// Whether the attention kernels' launches stay under 2^32 threads: a workgroup
+// per query token and head joins the narrow kernel's parts, one per tile and
+// key head runs the wide prompt kernel (8 of them join its parts, where there
+// are so few tiles that it splits them).
+bool launchable(int tokens, int rows, int heads, int heads_kv) {
+  if (!tokens || !rows) return true;
   const int group = heads / heads_kv;
-  if (!tokens || !rows || qg::narrow_tiles(tokens, rows, group)) return 0;
-  return (int64_t)qg::prompt_tiles(tokens, rows, group) * heads_kv * qg::prompt_splits(tokens, tokens_k, rows, heads_kv, group);
+  if (qg::narrow_tiles(tokens, rows, group)) return (int64_t)tokens * heads < 1 << 24;
+  return (int64_t)qg::prompt_tiles(tokens, rows, group) * heads_kv < 1 << 21 && heads_kv < 65536;
 }
 
 int check_scale(float scale) { return std::isfinite(scale) && scale >= 0.f ? QGEMV_OK : QGEMV_ERR_VALUE; }
@@ -151,7 +155,7 @@ int qgemv_attn_prompt(int dtype, int causal, int tokens, int tokens_k, int batch
   int rc = check_kind(dtype, head_dim);
   if (rc) return rc;
   if ((rc = check_counts(tokens, batch, heads, heads_kv))) return rc;
-  if (tokens_k < 0 || prompt_grid(tokens, tokens_k, batch, heads, heads_kv) >= 1 << 24) return QGEMV_ERR_SHAPE;
+  if (tokens_k < 0 || !launchable(tokens, batch, heads, heads_kv)) return QGEMV_ERR_SHAPE;
   if ((rc = check_heads(*q, tokens, heads, head_dim, false)) || (rc = check_heads(*k, tokens_k, heads_kv, head_dim, false)) ||
       (rc = check_heads(*v, tokens_k, heads_kv, head_dim, false)) || (rc = check_heads(*o, tokens, heads, head_dim, true)))
     return rc;
@@ -207,6 +211,7 @@ int qgemv_attn_tree(int dtype, const qgemv_kv_cache* c, int layer, int tokens, i
   if (rc) return rc;
   if ((rc = check_cache(c, false))) return rc;
   if ((rc = check_counts(tokens, c->rows, heads, c->heads_kv))) return rc;
+  if (!launchable(tokens, c->rows, heads, c->heads_kv)) return QGEMV_ERR_SHAPE;
   if (layer < 0 || layer >= c->layers || mask_words < 0 || mask_words > 1 << 20 || (mask != nullptr) != (mask_words > 0))
     return QGEMV_ERR_SHAPE;
   if ((rc = check_heads(*q, tokens, heads, c->head_dim, false)) || (rc = check_heads(*o, tokens, heads, c->head_dim, true)))

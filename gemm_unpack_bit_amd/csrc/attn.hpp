@@ -85,13 +85,6 @@ inline int prompt_splits(int tokens, int tokens_k, int rows, int heads_kv, int g
   return s < 1 ? 1 : (int)s;
 }
 
-// workgroups of the kernels that join partial results: a wave per query token
-// and head, in a loop beyond 2^20 workgroups
-inline unsigned join_blocks(const AttnArgs& a) {
-  const int64_t n = ((int64_t)a.tokens * a.heads + 3) / 4;
-  return (unsigned)(n < 1 << 20 ? n : 1 << 20);
-}
-
 hipError_t launch_attn_narrow(const AttnArgs& a, int rt, hipStream_t s);
 hipError_t launch_attn_wide(const AttnArgs& a, hipStream_t s);
 

@@ -119,6 +119,16 @@ __device__ __forceinline__ Row row_of(const AttnArgs& a, int b) {
   return r;
 }
 
+// The pool token (page * page_size + place) of position kb of row b, kb in the
+// row's table; a page number outside the pool counts as page 0.  b and kb are
+// the same in the whole wave, and tables do not change during the kernel, so
+// this is a scalar load.
+__device__ __forceinline__ int64_t pool_token(const AttnArgs& a, int b, int kb) {
+  typedef __attribute__((address_space(4))) const int32_t* table;
+  const int page = ((table)a.tables)[(int64_t)b * a.max_pages + (kb >> a.page_shift)];
+  return ((int64_t)((unsigned)page < (unsigned)a.pages ? page : 0) << a.page_shift) + (kb & ((1 << a.page_shift) - 1));
+}
+
 // What query token t of a row sees: every key below lim, and of the keys from
 // pos on those whose bit is set in its mask words.
 template <bool PAGED>
@@ -172,33 +182,96 @@ struct Partials {
   __device__ __forceinline__ float* o_at(int64_t slot, int row) const { return o + (slot * BM + row) * D; }
 };
 
-// Joins the partial results of one query row (one wave; lane l holds outputs
-// EPL * l ..): o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i over parts i,
-// slot(i) naming the part's slot.
-template <typename E, int BM, int D, typename F>
-__device__ __forceinline__ void join_row(const Partials<BM, D>& p, int row, int parts, F&& slot, uint16_t* out) {
-  constexpr int EPL = D / 64;
-  const int lane = threadIdx.x & 63;
-  float M = NEG_INF;
-  for (int i = lane; i < parts; i += 64) M = fmaxf(M, p.ml_at(slot(i), row)[0]);
-  M = quarter_max(M);
+// Joins partial results of one query row: 16 threads hold the row's columns
+// (DL each), PL lanes of parts take the parts i = pl, pl + PL, ... and are then
+// added in LDS in a fixed order:
+//     o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
+// Every thread loads its parts' statistics and sums without waiting for
+// anything but their slots.  All threads of the workgroup take part; `tid` is
+// the thread's number among the row's 16 PL threads, with the column fastest.
+template <int D, int PL>
+struct JoinBuffer {
+  float o[PL][D], m[PL], l[PL];
+};
+template <typename E, int PL, int BM, int D, typename F>
+__device__ __forceinline__ void join_row(const Partials<BM, D>& p, int row, int parts, F&& slot, uint16_t* out, bool live,
+                                         int tid, JoinBuffer<D, PL>* buf) {
+  constexpr int DL = D / 16;
+  typedef float fl __attribute__((ext_vector_type(DL)));
+  const int pl = tid >> 4, col = DL * (tid & 15);
+  float m = NEG_INF, l = 0.f;
+  fl acc;
 #pragma unroll
-  for (int d = 1; d < 16; d <<= 1) M = fmaxf(M, __shfl_xor(M, d));
-  const float base = M == NEG_INF ? 0.f : M;
-  float l = 0.f, acc[EPL] = {};
-#pragma unroll 4
-  for (int i = 0; i < parts; ++i) {
-    const int64_t s = slot(i);
-    const float* ml = p.ml_at(s, row);
-    const float w = exp2_(ml[0] - base), li = ml[1];
-    l += w * li;
-    const float* o = p.o_at(s, row) + EPL * lane;
+  for (int e = 0; e < DL; ++e) acc[e] = 0.f;
+  if (live) {
+    for (int i = pl; i < parts; i += 4 * PL) {
+      float mi[4], li[4];
+      fl oi[4];
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] += li == 0.f ? 0.f : w * o[e];
+      for (int x = 0; x < 4; ++x) {
+        const int at = i + x * PL;
+        const int64_t s = slot(at < parts ? at : i);
+        const float* ml = p.ml_at(s, row);
+        mi[x] = at < parts ? ml[0] : NEG_INF;
+        li[x] = at < parts ? ml[1] : 0.f;
+        oi[x] = *reinterpret_cast<const fl*>(p.o_at(s, row) + col);
+      }
+      float mn = m;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mn = fmaxf(mn, mi[x]);
+      const float base = mn == NEG_INF ? 0.f : mn, w = exp2_(m - base);
+      l *= w;
+      acc *= w;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float wx = exp2_(mi[x] - base);
+        l += wx * li[x];
+#pragma unroll
+        for (int e = 0; e < DL; ++e) acc[e] += li[x] == 0.f ? 0.f : wx * oi[x][e];  // (no weights: o may be anything)
+      }
+      m = mn;
+    }
   }
+  if constexpr (PL > 1) {
+    *reinterpret_cast<fl*>(&buf->o[pl][col]) = acc;
+    if ((tid & 15) == 0) buf->m[pl] = m, buf->l[pl] = l;
+    __syncthreads();
+    if (pl > 0) return;
+    float M = NEG_INF;
+#pragma unroll
+    for (int x = 0; x < PL; ++x) M = fmaxf(M, buf->m[x]);
+    const float base = M == NEG_INF ? 0.f : M;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < DL; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int x = 0; x < PL; ++x) {
+      const float w = exp2_(buf->m[x] - base);
+      l += w * buf->l[x];
+      acc += w * *reinterpret_cast<const fl*>(&buf->o[x][col]);
+    }
+  }
+  if (!live) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  if constexpr (EPL == 2) reinterpret_cast<uint32_t*>(out)[lane] = E::pack(acc[0] * inv, acc[1] * inv);
-  else out[lane] = (uint16_t)E::pack(acc[0] * inv, 0.f);
+  typedef uint32_t vw __attribute__((ext_vector_type(DL / 2)));
+  vw y;
+#pragma unroll
+  for (int e = 0; e < DL / 2; ++e) y[e] = E::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  *reinterpret_cast<vw*>(out + col) = y;
+}
+
+// inclusive sums over the wave's lanes of values < 2^24 (row shifts, then
+// broadcasts of the rows' last lanes)
+__device__ __forceinline__ uint32_t scan24(uint32_t v) {
+#define QG_SCAN(CTRL, ROWS) v += __builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false)
+  QG_SCAN(0x111, 0xF);  // row_shr:1
+  QG_SCAN(0x112, 0xF);
+  QG_SCAN(0x114, 0xF);
+  QG_SCAN(0x118, 0xF);
+  QG_SCAN(DPP_BCAST15, 0xA);
+  QG_SCAN(DPP_BCAST31, 0xC);
+#undef QG_SCAN
+  return v;
 }
 
 // The split of the key axis.  An item is a tile of BM query rows (row
@@ -212,83 +285,114 @@ __device__ __forceinline__ void join_row(const Partials<BM, D>& p, int row, int 
 // partial result (the part that starts with the workgroup's share in slot
 // 2 c, one that starts later in slot 2 c + 1), which a second kernel joins in
 // key order.
-struct Split {
-  int64_t per, total;
-};
-struct Place {  // of one unit
-  int b;
-  int64_t first;  // the row's first unit
-};
+//
+// A wave keeps 64 rows at a time, one per lane, with the running sum of their
+// units; up to 64 rows are read once.
 template <int BM, int KB, bool PAGED>
-struct Units {
+struct Walk {
+  int64_t total, per;
+  int b0;           // the first row held
+  Row mine;         // the lane's row
+  int64_t incl;     // units of the rows held up to and with the lane's
+  int64_t cost;     // units of the lane's row
+  int64_t before, all;  // units in front of the rows held, and of the rows held
+
   static __device__ __forceinline__ int tiles(const AttnArgs& a, const Row& r) { return (r.n * a.group + BM - 1) / BM; }
   // key units of an item; one without keys still has an output to write
   static __device__ __forceinline__ int units(const Row& r) { return r.keys ? (r.keys + KB - 1) / KB : 1; }
-  static __device__ __forceinline__ int64_t cost(const AttnArgs& a, int b) {
-    if (b >= a.rows) return 0;
-    const Row r = row_of<PAGED>(a, b);
-    return (int64_t)tiles(a, r) * a.heads_kv * units(r);
-  }
-  static __device__ __forceinline__ int64_t scan64(int64_t v) {  // inclusive, over the wave
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int64_t o = __shfl_up((long long)v, d);
-      if (lane >= d) v += o;
-    }
-    return v;
-  }
-  static __device__ __forceinline__ int64_t uniform64(int64_t v, int lane) {
+  static __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+  static __device__ __forceinline__ int64_t lane64(int64_t v, int lane) {
     const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane);
     const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)((uint64_t)v >> 32), lane);
     return (int64_t)((uint64_t)hi << 32 | lo);
   }
-  static __device__ __forceinline__ Split split(const AttnArgs& a, int workgroups, int least) {
-    Split s;
-    s.total = 0;
-    for (int b0 = 0; b0 < a.rows; b0 += 64) s.total += uniform64(scan64(cost(a, b0 + (threadIdx.x & 63))), 63);
-    const int64_t even = (s.total + workgroups - 1) / workgroups;
-    s.per = even > least ? even : least;
-    return s;
-  }
-  // the row that unit u (< total) belongs to
-  static __device__ __forceinline__ Place place(const AttnArgs& a, int64_t u) {
-    int64_t before = 0;
-    for (int b0 = 0; b0 < a.rows; b0 += 64) {
-      const int64_t c = cost(a, b0 + (threadIdx.x & 63)), s = scan64(c);
-      const int64_t all = uniform64(s, 63);
-      if (u < before + all) {
-        const int l = __builtin_ctzll(__ballot(u < before + s));
-        return Place{b0 + l, before + uniform64(s - c, l)};
-      }
-      before += all;
+  __device__ __forceinline__ void hold(const AttnArgs& a, int first, int64_t sum) {
+    b0 = first;
+    before = sum;
+    const int b = b0 + (threadIdx.x & 63);
+    mine = Row{0, 0, 0, 0, 0};
+    cost = 0;
+    if (b < a.rows) {
+      mine = row_of<PAGED>(a, b);
+      cost = (int64_t)tiles(a, mine) * a.heads_kv * units(mine);
     }
-    return Place{a.rows - 1, before};
+    incl = ((int64_t)scan24((uint32_t)(cost >> 24)) << 24) + scan24((uint32_t)cost & 0xFFFFFF);
+    all = lane64(incl, 63);
   }
-  // one wave: query token w / heads of head w % heads, where its item lay in
-  // several workgroups
-  template <typename E, int D>
-  static __device__ __forceinline__ void join(const AttnArgs& a, int w, int workgroups, int least) {
-    const int token = w / a.heads, head = w - token * a.heads, h = head / a.group;
-    const Split sp = split(a, workgroups, least);
-    const int b = find_row(a.rows, token, [&](int i) { return a.cu[i]; });
-    const Row r = row_of<PAGED>(a, b);
-    const int t = token - r.q0;
-    if (t < 0 || t >= r.n) return;
-    int64_t first = 0;
-    for (int b0 = 0; b0 < b; b0 += 64) {
-      const int x = b0 + (threadIdx.x & 63);
-      first += uniform64(scan64(x < b ? cost(a, x) : 0), 63);
+  __device__ __forceinline__ void init(const AttnArgs& a, int workgroups, int least) {
+    hold(a, 0, 0);
+    total = all;
+    for (int first = 64; first < a.rows; first += 64) {
+      hold(a, first, total);
+      total += all;
     }
-    const int qr = t * a.group + head - h * a.group;
-    const int tile = qr / BM;
-    const int64_t u0 = first + (int64_t)(tile * a.heads_kv + h) * units(r), u1 = u0 + units(r);
-    const int64_t c0 = u0 / sp.per, c1 = (u1 - 1) / sp.per;
-    if (c0 == c1) return;
-    const Partials<BM, D> parts(a.ws, 2 * (int64_t)workgroups);
-    const bool late = u0 != c0 * sp.per;
-    join_row<E>(parts, qr - tile * BM, (int)(c1 - c0 + 1), [&](int i) { return 2 * (c0 + i) + (i == 0 && late); },
-                a.o + (int64_t)token * a.o_token + (int64_t)head * a.o_head);
+    const int64_t even = (total + workgroups - 1) / workgroups;
+    per = even > least ? even : least;
+  }
+  __device__ __forceinline__ Row row(int lane) const {
+    Row r;
+    r.q0 = __builtin_amdgcn_readlane(mine.q0, lane);
+    r.n = __builtin_amdgcn_readlane(mine.n, lane);
+    r.pos = __builtin_amdgcn_readlane(mine.pos, lane);
+    r.k0 = __builtin_amdgcn_readlane(mine.k0, lane);
+    r.keys = __builtin_amdgcn_readlane(mine.keys, lane);
+    return r;
+  }
+  __device__ __forceinline__ int64_t first_of(int lane) const { return before + lane64(incl - cost, lane); }
+  // unit u (< total) and what follows it in its item, up to unit u_end: row b,
+  // key head h, tile, units [k0, k1) of the item's `of`
+  struct Piece {
+    Row r;
+    int b, h, tile, k0, k1, of;
+  };
+  __device__ __forceinline__ Piece seek(const AttnArgs& a, int64_t u, int64_t u_end) {
+    if (u < before) hold(a, 0, 0);
+    while (u >= before + all && b0 + 64 < a.rows) hold(a, b0 + 64, before + all);
+    const int lane = __builtin_ctzll(__ballot(u < before + incl) | 1ull << 63);
+    Piece p;
+    p.b = uniform(b0 + lane);
+    p.r = row(lane);
+    p.of = uniform(units(p.r));
+    const int64_t in = u - first_of(lane), item = in / p.of, left = u_end - u;
+    p.k0 = uniform((int)(in - item * p.of));
+    p.k1 = uniform((int)(p.k0 + left < p.of ? p.k0 + left : p.of));
+    p.h = uniform((int)(item % a.heads_kv));
+    p.tile = uniform((int)(item / a.heads_kv));
+    return p;
+  }
+  // row b, and its first unit
+  __device__ __forceinline__ void seek_row(const AttnArgs& a, int b, Row& r, int64_t& first) {
+    if (b < b0) hold(a, 0, 0);
+    while (b >= b0 + 64) hold(a, b0 + 64, before + all);
+    r = row(b - b0);
+    first = first_of(b - b0);
+  }
+  // the row of highest number whose key (ascending over rows, key(0) <= x) is
+  // at most x; held(row) gives the key of a row held, key(b) of any row
+  template <typename H, typename K>
+  __device__ __forceinline__ int find(const AttnArgs& a, int x, H&& held, K&& key) const {
+    if (a.rows <= 64) {
+      const int b = threadIdx.x & 63;
+      const uint64_t m = __ballot(b < a.rows && held(mine, b) <= x);
+      return m ? 63 - __builtin_clzll(m) : 0;
+    }
+    return find_row(a.rows, x, key);
+  }
+  // the parts of an item whose first unit is u0: how many (1: it lies in one
+  // workgroup), the first one's workgroup, and whether it is that workgroup's
+  // second slot
+  struct Parts {
+    int n;
+    int64_t c0;
+    bool late;
+    __device__ __forceinline__ int64_t slot(int i) const { return 2 * (c0 + i) + (i == 0 && late); }
+  };
+  __device__ __forceinline__ Parts parts(int64_t u0, const Row& r) const {
+    Parts p;
+    p.c0 = u0 / per;
+    p.n = (int)((u0 + units(r) - 1) / per - p.c0) + 1;
+    p.late = u0 != p.c0 * per;
+    return p;
   }
 };
 

@@ -41,27 +41,23 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
   constexpr int DW = DL / 2;  // ... in 32-bit words
   constexpr int PITCH = D + 4;
   typedef uint32_t vw __attribute__((ext_vector_type(DW)));
-  using U = Units<BM, KB, PAGED>;
+  using U = Walk<BM, KB, PAGED>;
   __shared__ __attribute__((aligned(16))) float o_s[WAVES][BM][PITCH];
   __shared__ float m_s[WAVES][BM], l_s[WAVES][BM];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n16 = lane & 15, quarter = lane >> 4;
-  const Split sp = U::split(a, workgroups, least);
-  int64_t u = (int64_t)blockIdx.x * sp.per;
-  const int64_t u_end = u + sp.per < sp.total ? u + sp.per : sp.total;
+  U walk;
+  walk.init(a, workgroups, least);
+  int64_t u = (int64_t)blockIdx.x * walk.per;
+  const int64_t u_end = u + walk.per < walk.total ? u + walk.per : walk.total;
   const int64_t u_begin = u;
   const Partials<BM, D> parts(a.ws, 2 * (int64_t)workgroups);
 
   while (u < u_end) {
-    const Place at = U::place(a, u);
-    const Row r = row_of<PAGED>(a, at.b);
-    const int per_item = U::units(r);
-    const int64_t item = (u - at.first) / per_item;
-    const int ku = (int)(u - at.first - item * per_item);  // first unit in the item
-    const int64_t left = u_end - u;
-    const int ku_end = (int)(ku + left < per_item ? ku + left : per_item);
-    const int h = (int)(item % a.heads_kv), tile = (int)(item / a.heads_kv);
+    const typename U::Piece piece = walk.seek(a, u, u_end);
+    const Row r = piece.r;
+    const int b = piece.b, h = piece.h, tile = piece.tile, ku = piece.k0, ku_end = piece.k1;
     const int rows = r.n * a.group;
 
     // the wave's query rows: lane column n16 of each 16-row tile
@@ -107,9 +103,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
       last = r.keys - 1 - kb;  // keys past it are read from its place
       int64_t tok;
       if constexpr (PAGED) {
-        const int page = a.tables[(int64_t)at.b * a.max_pages + (kb >> a.page_shift)];
-        const int ok = (unsigned)page < (unsigned)a.pages ? page : 0;
-        tok = ((int64_t)ok << a.page_shift) + (kb & ((1 << a.page_shift) - 1));
+        tok = pool_token(a, b, kb);
       } else {
         tok = (int64_t)r.k0 + kb;
       }
@@ -241,7 +235,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
       if (quarter == 0) m_s[wave][row] = m[i], l_s[wave][row] = sum;
     }
     __syncthreads();
-    const bool whole = ku == 0 && ku_end == per_item;
+    const bool whole = ku == 0 && ku_end == piece.of;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (u != u_begin);
     constexpr int TPR = 64 * WAVES / 16;  // 16 threads per row, DL columns each
     static_assert(TPR == 16, "a row's columns are DL per thread");
@@ -287,15 +281,27 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
   }
 }
 
-// One wave per query token and head: joins the parts of an item that lay in
-// several workgroups.
+// One workgroup per query token and head: joins the parts of an item that lay
+// in several workgroups, 16 parts at a time.
 template <typename E, int D, int RT, bool PAGED>
 __global__ void __launch_bounds__(256) attn_narrow_join_kernel(AttnArgs a, int workgroups, int least) {
-  constexpr int BM = 16 * RT;
-  using U = Units<BM, KB, PAGED>;
-  const int n = a.tokens * a.heads;
-  for (int64_t w = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6)); w < n; w += (int64_t)gridDim.x * 4)
-    U::template join<E, D>(a, (int)w, workgroups, least);
+  constexpr int BM = 16 * RT, PL = 16;
+  using U = Walk<BM, KB, PAGED>;
+  __shared__ __attribute__((aligned(16))) JoinBuffer<D, PL> buf;
+  U walk;
+  walk.init(a, workgroups, least);
+  const int token = blockIdx.x / a.heads, head = blockIdx.x - token * a.heads, h = head / a.group;
+  const int b = walk.find(a, token, [](const Row& r, int) { return r.q0; }, [&](int i) { return a.cu[i]; });
+  Row r;
+  int64_t first;
+  walk.seek_row(a, b, r, first);
+  const int t = token - r.q0;
+  if (t < 0 || t >= r.n) return;
+  const int qr = t * a.group + head - h * a.group, tile = qr / BM;
+  const typename U::Parts p = walk.parts(first + (int64_t)(tile * a.heads_kv + h) * U::units(r), r);
+  if (p.n == 1) return;
+  join_row<E, PL>(Partials<BM, D>(a.ws, 2 * (int64_t)workgroups), qr - tile * BM, p.n, [&](int i) { return p.slot(i); },
+                  a.o + (int64_t)token * a.o_token + (int64_t)head * a.o_head, true, threadIdx.x, &buf);
 }
 
 template <typename E, int D, int RT, bool PAGED>
@@ -303,7 +309,7 @@ hipError_t launch(const AttnArgs& a, hipStream_t s) {
   const int least = 1;
   hipLaunchKernelGGL((attn_narrow_kernel<E, D, RT, PAGED>), dim3(NARROW_WORKGROUPS), dim3(64 * WAVES), 0, s, a,
                      NARROW_WORKGROUPS, least);
-  hipLaunchKernelGGL((attn_narrow_join_kernel<E, D, RT, PAGED>), dim3(join_blocks(a)), dim3(256), 0, s, a,
+  hipLaunchKernelGGL((attn_narrow_join_kernel<E, D, RT, PAGED>), dim3((unsigned)(a.tokens * a.heads)), dim3(256), 0, s, a,
                      NARROW_WORKGROUPS, least);
   return hipGetLastError();
 }

@@ -122,9 +122,7 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
   auto tok_of = [&](int u) -> int64_t {  // pool or array token of the wave's first row
     const int kb = min(u * KB + 16 * wave, top);
     if constexpr (PAGED) {
-      const int page = a.tables[(int64_t)g.b * a.max_pages + (kb >> a.page_shift)];
-      const int ok = (unsigned)page < (unsigned)a.pages ? page : 0;
-      return ((int64_t)ok << a.page_shift) + (kb & ((1 << a.page_shift) - 1));
+      return pool_token(a, g.b, kb);
     } else {
       return (int64_t)r.k0 + kb;
     }
@@ -261,9 +259,7 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
       const int key = __builtin_ctzll(odd), at = min(kb + key, r.keys - 1);
       int64_t tok;
       if constexpr (PAGED) {
-        const int page = a.tables[(int64_t)g.b * a.max_pages + (at >> a.page_shift)];
-        tok = ((int64_t)((unsigned)page < (unsigned)a.pages ? page : 0) << a.page_shift) +
-              (at & ((1 << a.page_shift) - 1));
+        tok = pool_token(a, g.b, at);
       } else {
         tok = (int64_t)r.k0 + at;
       }
@@ -445,63 +441,67 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_prompt_kernel(AttnArgs a, 
   run_segment<E, D, false>(g, (int64_t)tiles * a.heads_kv * splits, k0, k1, v0, v1, flag);
 }
 
-// one wave: joins the parts of query token w / heads, head w % heads
+// One workgroup per 16 query rows of a tile and key head: joins their parts.
 template <typename E, int D>
-__device__ __forceinline__ void join_prompt(const AttnArgs& a, int w, int tiles, int splits) {
-  const int token = w / a.heads, head = w - token * a.heads, h = head / a.group;
-  const int b = find_row(a.rows, token, [&](int i) { return a.cu[i]; });
-  const Row r = row_of<false>(a, b);
-  const int t = token - r.q0;
-  if (t < 0 || t >= r.n) return;
-  const int qr = t * a.group + head - h * a.group;
-  const int64_t tile = first_tile(a, b) + qr / BM;
-  const Partials<BM, D> parts(a.ws, (int64_t)tiles * a.heads_kv * splits);
-  join_row<E>(parts, qr % BM, splits, [&](int i) { return (tile * a.heads_kv + h) * splits + i; },
-              a.o + (int64_t)token * a.o_token + (int64_t)head * a.o_head);
-}
-
-template <typename E, int D>
-__global__ void __launch_bounds__(256) attn_prompt_join_kernel(AttnArgs a, int tiles, int splits) {
-  const int n = a.tokens * a.heads;
-  for (int64_t w = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6)); w < n; w += (int64_t)gridDim.x * 4)
-    join_prompt<E, D>(a, (int)w, tiles, splits);
+__global__ void __launch_bounds__(256) attn_prompt_join_kernel(AttnArgs a, int splits) {
+  const int tile = blockIdx.x / (BM / 16), h = blockIdx.y;
+  Row r;
+  int b, in;
+  if (!find_tile(a, tile, r, b, in)) return;
+  const int row = 16 * (blockIdx.x % (BM / 16)) + (threadIdx.x >> 4), qr = in * BM + row;
+  const int t = qr / a.group, head = h * a.group + qr - t * a.group;
+  const Partials<BM, D> parts(a.ws, (int64_t)(gridDim.x / (BM / 16)) * a.heads_kv * splits);
+  join_row<E, 1>(parts, row, splits, [&](int i) { return ((int64_t)tile * a.heads_kv + h) * splits + i; },
+                 a.o + (int64_t)(r.q0 + t) * a.o_token + (int64_t)head * a.o_head, t < r.n, threadIdx.x & 15,
+                 (JoinBuffer<D, 1>*)nullptr);
 }
 
 // Trees over the paged cache: the units of all items shared out evenly
 // (Units), so rows of very different lengths keep every workgroup busy.
 template <typename E, int D>
 __global__ void __launch_bounds__(64 * WAVES, 2) attn_tree_kernel(AttnArgs a, int workgroups, int least) {
-  using U = Units<BM, KB, true>;
+  using U = Walk<BM, KB, true>;
   __shared__ Buffers<D> k0, k1, v0, v1;
   __shared__ uint32_t flag[2];
-  const Split sp = U::split(a, workgroups, least);
-  const int64_t u_begin = (int64_t)blockIdx.x * sp.per;
-  const int64_t u_end = u_begin + sp.per < sp.total ? u_begin + sp.per : sp.total;
-  for (int64_t u = u_begin; u < u_end;) {
-    const Place at = U::place(a, u);
-    Segment g;
-    g.b = at.b;
-    g.r = row_of<true>(a, at.b);
-    const int per_item = U::units(g.r);
-    const int64_t item = (u - at.first) / per_item;
-    const int64_t left = u_end - u;
-    g.u0 = (int)(u - at.first - item * per_item);
-    g.u1 = (int)(g.u0 + left < per_item ? g.u0 + left : per_item);
-    g.h = (int)(item % a.heads_kv);
-    g.tile = (int)(item / a.heads_kv);
-    const int next = g.u1;
-    g.slot = g.u0 == 0 && g.u1 == per_item ? -1 : 2 * (int64_t)blockIdx.x + (u != u_begin);
-    u += next - g.u0;
+  // (the rows are looked up again for every segment, of which there are few,
+  // so that they occupy no registers during one)
+  for (int64_t done = 0;;) {
+    U walk;
+    walk.init(a, workgroups, least);
+    const int64_t u_begin = (int64_t)blockIdx.x * walk.per, u = u_begin + done;
+    const int64_t u_end = u_begin + walk.per < walk.total ? u_begin + walk.per : walk.total;
+    if (u >= u_end) break;
+    const typename U::Piece p = walk.seek(a, u, u_end);
+    Segment g{p.r, p.b, p.h, p.tile, p.k0, p.k1, 0};
+    g.slot = g.u0 == 0 && g.u1 == p.of ? -1 : 2 * (int64_t)blockIdx.x + (done != 0);
+    done += g.u1 - g.u0;
     run_segment<E, D, true>(g, 2 * (int64_t)workgroups, k0, k1, v0, v1, flag);
   }
 }
 
+// One workgroup per 16 query rows of a tile and key head: joins the parts of
+// an item that lay in several workgroups.
 template <typename E, int D>
 __global__ void __launch_bounds__(256) attn_tree_join_kernel(AttnArgs a, int workgroups, int least) {
-  using U = Units<BM, KB, true>;
-  const int n = a.tokens * a.heads;
-  for (int64_t w = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6)); w < n; w += (int64_t)gridDim.x * 4)
-    U::template join<E, D>(a, (int)w, workgroups, least);
+  using U = Walk<BM, KB, true>;
+  U walk;
+  walk.init(a, workgroups, least);
+  const int tile = blockIdx.x / (BM / 16), h = blockIdx.y;
+  auto first_at = [&](int q0, int b) { return (int)((int64_t)q0 * a.group / BM) + b; };
+  const int b = walk.find(a, tile, [&](const Row& r, int i) { return first_at(r.q0, i); },
+                          [&](int i) { return first_at(a.cu[i], i); });
+  Row r;
+  int64_t first;
+  walk.seek_row(a, b, r, first);
+  const int in = tile - first_at(r.q0, b);
+  if (in < 0 || in >= U::tiles(a, r)) return;
+  const typename U::Parts p = walk.parts(first + (int64_t)(in * a.heads_kv + h) * U::units(r), r);
+  if (p.n == 1) return;
+  const int row = 16 * (blockIdx.x % (BM / 16)) + (threadIdx.x >> 4), qr = in * BM + row;
+  const int t = qr / a.group, head = h * a.group + qr - t * a.group;
+  join_row<E, 1>(Partials<BM, D>(a.ws, 2 * (int64_t)workgroups), row, p.n, [&](int i) { return p.slot(i); },
+                 a.o + (int64_t)(r.q0 + t) * a.o_token + (int64_t)head * a.o_head, t < r.n, threadIdx.x & 15,
+                 (JoinBuffer<D, 1>*)nullptr);
 }
 
 template <typename E, int D>
@@ -511,14 +511,17 @@ hipError_t prompt(const AttnArgs& a, hipStream_t s) {
   const int64_t grid = (int64_t)tiles * a.heads_kv * splits;
   hipLaunchKernelGGL((attn_prompt_kernel<E, D>), dim3((unsigned)grid), dim3(64 * WAVES), 0, s, a, tiles, splits);
   if (splits > 1)
-    hipLaunchKernelGGL((attn_prompt_join_kernel<E, D>), dim3(join_blocks(a)), dim3(256), 0, s, a, tiles, splits);
+    hipLaunchKernelGGL((attn_prompt_join_kernel<E, D>), dim3((unsigned)tiles * (BM / 16), (unsigned)a.heads_kv), dim3(256),
+                       0, s, a, splits);
   return hipGetLastError();
 }
 
 template <typename E, int D>
 hipError_t tree(const AttnArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((attn_tree_kernel<E, D>), dim3(WIDE_WORKGROUPS), dim3(64 * WAVES), 0, s, a, WIDE_WORKGROUPS, 1);
-  hipLaunchKernelGGL((attn_tree_join_kernel<E, D>), dim3(join_blocks(a)), dim3(256), 0, s, a, WIDE_WORKGROUPS, 1);
+  hipLaunchKernelGGL((attn_tree_join_kernel<E, D>),
+                     dim3((unsigned)prompt_tiles(a.tokens, a.rows, a.group) * (BM / 16), (unsigned)a.heads_kv), dim3(256), 0,
+                     s, a, WIDE_WORKGROUPS, 1);
   return hipGetLastError();
 }
 
