@@ -9,68 +9,71 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
 import gemm_unpack_bit_amd as _q
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+_pack = struct.Struct("Pqq").pack  # qgemv_heads: data, token, head
+_lib = _q.lib()
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-class _Heads(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
-
-
-class _Cache(ctypes.Structure):
+class _Cache(ctypes.Structure):  # qgemv_kv_cache
     _fields_ = [(n, ctypes.c_int) for n in ("layers", "pages", "page_size", "heads_kv", "head_dim", "rows", "max_pages")]
     _fields_ += [(n, ctypes.c_void_p) for n in ("k", "v", "tables", "lens", "refs", "status")]
 
 
-def _heads(t, name, dtype=None):
-    """[tokens, heads, head_dim] view with a contiguous last dimension -> qgemv_heads."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
-        raise TypeError(f"{name} must be {dtype or 'float16 or bfloat16'}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    token, head, one = t.stride()
-    if one != 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    return _Heads(t.data_ptr() or 16, token, head)  # (an empty tensor has no data)
+# These checks run on every call of a decode loop, so each is a handful of
+# attribute reads; a tensor's device number is -1 off the GPU.
+
+def _heads(t, name, dtype, dev):
+    """[tokens, heads, head_dim] view with a contiguous last dimension -> a packed qgemv_heads."""
+    if t.get_device() != dev or dev < 0:
+        raise TypeError(f"{name} must be a CUDA tensor on the same device as the others")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    stride = t.stride()
+    if len(stride) != 3 or stride[2] != 1:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] with a contiguous last dimension")
+    return _pack(t.data_ptr() or 16, stride[0], stride[1])  # (an empty tensor has no data)
 
 
-def _ints(t, name, n):
-    _q._need(t, torch.int32, name)
-    if t.numel() != n:
-        raise ValueError(f"{name} must hold {n} int32 values, got {t.numel()}")
-    return t.data_ptr()
+def _ints(t, name, n, dev):
+    if t.get_device() != dev:
+        raise TypeError(f"{name} must be a CUDA tensor on the same device as the others")
+    if t.dtype is not torch.int32:
+        raise TypeError(f"{name} must be {torch.int32}, got {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {n} contiguous int32 values")
+    return t.data_ptr() or 4
 
 
-def _same_device(ref, **others):
-    for name, t in others.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+def _ws(ws, dev):
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous CUDA tensor on the same device as the others")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _ws(ws, need, device):
-    if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    if not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("ws must be a contiguous CUDA tensor")
-    return ws
+def _kind(t, name):
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be a float16 or bfloat16 tensor")
+    return t.dtype
 
 
-def _bytes(ws):
-    return (0, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+def _done(fn, status):
+    if status:
+        raise _q.QgemvError(fn, status)
 
 
 def attn_prompt_workspace_bytes(tokens, tokens_k, batch, heads, heads_kv, head_dim):
-    return int(_q.lib().qgemv_attn_prompt_workspace_bytes(tokens, tokens_k, batch, heads, heads_kv, head_dim))
+    return int(_lib.qgemv_attn_prompt_workspace_bytes(tokens, tokens_k, batch, heads, heads_kv, head_dim))
 
 
 def attn_tree_workspace_bytes(tokens, rows, heads, heads_kv, head_dim):
-    return int(_q.lib().qgemv_attn_tree_workspace_bytes(tokens, rows, heads, heads_kv, head_dim))
+    return int(_lib.qgemv_attn_tree_workspace_bytes(tokens, rows, heads, heads_kv, head_dim))
 
 
 def attn_prompt(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None, ws=None):
@@ -83,34 +86,34 @@ def attn_prompt(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None, ws=
     i sees keys up to i + nk - nq.  scale: head_dim ** -0.5 by default.  ws:
     optional scratch of attn_prompt_workspace_bytes(...) bytes, reusable across
     calls on one stream.  Returns out [tokens, heads, head_dim]."""
-    hq, hk, hv = _heads(q, "q"), _heads(k, "k", q.dtype), _heads(v, "v", q.dtype)
+    dtype, dev = _kind(q, "q"), q.get_device()
+    hq, hk, hv = _heads(q, "q", dtype, dev), _heads(k, "k", dtype, dev), _heads(v, "v", dtype, dev)
     tokens, heads, dim = q.shape
-    tokens_k, heads_kv, _ = k.shape
-    if k.shape != v.shape or k.shape[2] != dim:
+    tokens_k, heads_kv, dim_k = k.shape
+    if v.shape != k.shape or dim_k != dim:
         raise ValueError("k and v must be [tokens_k, heads_kv, head_dim] with q's head_dim")
     batch = cu_q.numel() - 1
     if batch < 0:
         raise ValueError("cu_q must hold batch + 1 offsets")
-    if cu_k is None:
-        if tokens_k != tokens:
-            raise ValueError("cu_k is needed where queries and keys differ in number")
-        cu_k = cu_q
-    pq, pk = _ints(cu_q, "cu_q", batch + 1), _ints(cu_k, "cu_k", batch + 1)
+    pq = _ints(cu_q, "cu_q", batch + 1, dev)
+    if cu_k is not None:
+        pk = _ints(cu_k, "cu_k", batch + 1, dev)
+    elif tokens_k == tokens:
+        pk = pq
+    else:
+        raise ValueError("cu_k is needed where queries and keys differ in number")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty(q.shape, dtype=dtype, device=q.device)
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    ho = _heads(out, "out", q.dtype)
-    _same_device(q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, out=out, ws=ws)
     if ws is None:
-        ws = _ws(None, attn_prompt_workspace_bytes(tokens, tokens_k, batch, heads, heads_kv, dim), q.device)
-    else:
-        ws = _ws(ws, 0, q.device)
-    wp, wn = _bytes(ws)
-    _q._check("qgemv_attn_prompt", _q.lib().qgemv_attn_prompt(
-        _DTYPES[q.dtype], int(causal), tokens, tokens_k, batch, heads, heads_kv, dim,
-        1.0 / math.sqrt(dim) if scale is None else scale, ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv), pq, pk,
-        ctypes.byref(ho), wp, wn, _q._stream(q)))
+        ws = torch.empty(attn_prompt_workspace_bytes(tokens, tokens_k, batch, heads, heads_kv, dim), dtype=torch.uint8,
+                         device=q.device)
+    wp, wn = _ws(ws, dev)
+    _done("qgemv_attn_prompt", _lib.qgemv_attn_prompt(
+        _DTYPES[dtype], int(causal), tokens, tokens_k, batch, heads, heads_kv, dim,
+        1.0 / math.sqrt(dim) if scale is None else scale, hq, hk, hv, pq, pk, _heads(out, "out", dtype, dev), wp, wn,
+        _raw_stream(dev)))
     return out
 
 
@@ -123,11 +126,10 @@ class KvCache:
     stream, or must be ordered by the caller."""
 
     def __init__(self, k, v, tables, lens, refs, status=None, ws=None):
+        dtype, dev = _kind(k, "k"), k.get_device()
         for name, t in (("k", k), ("v", v)):
-            if not isinstance(t, torch.Tensor) or not t.is_cuda:
-                raise TypeError(f"{name} must be a CUDA tensor")
-            if t.dtype not in _DTYPES or t.dtype != k.dtype:
-                raise TypeError("k and v must be float16 or bfloat16, and alike")
+            if _kind(t, name) is not dtype or t.get_device() != dev or dev < 0:
+                raise TypeError("k and v must be CUDA tensors of one type and device")
             if t.dim() != 5 or not t.is_contiguous() or t.shape != k.shape:
                 raise ValueError("k and v must be contiguous [layers, pages, page_size, heads_kv, head_dim]")
         if tables.dim() != 2:
@@ -135,19 +137,20 @@ class KvCache:
         rows, max_pages = tables.shape
         if status is None:
             status = torch.zeros(1, dtype=torch.int32, device=k.device)
-        for name, t, n in (("tables", tables, rows * max_pages), ("lens", lens, rows), ("refs", refs, k.shape[1]),
-                           ("status", status, 1)):
-            _ints(t, name, n)
-        _same_device(k, v=v, tables=tables, lens=lens, refs=refs, status=status, ws=ws)
-        need = int(_q.lib().qgemv_kv_workspace_bytes(rows, k.shape[1]))
+        pointers = [_ints(t, name, n, dev) for name, t, n in (
+            ("tables", tables, rows * max_pages), ("lens", lens, rows), ("refs", refs, k.shape[1]), ("status", status, 1))]
+        need = int(_lib.qgemv_kv_workspace_bytes(rows, k.shape[1]))
         if ws is None:
             ws = torch.empty(max(need, 16), dtype=torch.uint8, device=k.device)
-        elif ws.numel() * ws.element_size() < need or not ws.is_contiguous():
-            raise ValueError(f"ws must be contiguous and hold {need} bytes")
+        self._ws = _ws(ws, dev)
+        if self._ws[1] < need:
+            raise ValueError(f"ws must hold {need} bytes")
         self.k, self.v, self.tables, self.lens, self.refs, self.status, self.ws = k, v, tables, lens, refs, status, ws
-        self._c = _Cache(*k.shape, rows, max_pages, k.data_ptr(), v.data_ptr(), tables.data_ptr() or 4,
-                         lens.data_ptr() or 4, refs.data_ptr(), status.data_ptr())
-        self._ref = ctypes.byref(self._c)
+        self.rows, self.max_pages = rows, max_pages
+        self.page_size, self.heads_kv, self.head_dim = k.shape[2:]
+        self.dtype, self._dev = dtype, dev
+        self._c = _Cache(*k.shape, rows, max_pages, k.data_ptr(), v.data_ptr(), *pointers)
+        self._ref = ctypes.addressof(self._c)
 
     @classmethod
     def empty(cls, layers, pages, page_size, heads_kv, head_dim, rows, max_pages, dtype=torch.float16, device="cuda"):
@@ -166,35 +169,29 @@ class KvCache:
                        torch.full((rows, self.max_pages), -1, dtype=torch.int32, device=self.k.device),
                        torch.zeros(rows, dtype=torch.int32, device=self.k.device), self.refs, self.status)
 
-    rows = property(lambda self: self.tables.shape[0])
-    max_pages = property(lambda self: self.tables.shape[1])
-    page_size = property(lambda self: self.k.shape[2])
-    heads_kv = property(lambda self: self.k.shape[3])
-    head_dim = property(lambda self: self.k.shape[4])
-
 
 def kv_reserve(cache, cu, out=None):
     """Grows row b by cu[b + 1] - cu[b] tokens, taking the pages it lacks.
     Returns pos int32 [rows]: where each row's new tokens start, or -1 for a row
     that could not grow (cache.status says why).  Once per step."""
-    rows = cache.rows
-    pos = torch.empty(rows, dtype=torch.int32, device=cache.k.device) if out is None else out
-    p, o = _ints(cu, "cu", rows + 1), _ints(pos, "out", rows)
-    _same_device(cache.k, cu=cu, out=pos)
-    _q._check("qgemv_kv_reserve", _q.lib().qgemv_kv_reserve(cache._ref, p, o or 4, *_bytes(cache.ws), _q._stream(cache.k)))
-    return pos
+    rows, dev = cache.rows, cache._dev
+    if out is None:
+        out = torch.empty(rows, dtype=torch.int32, device=cache.k.device)
+    _done("qgemv_kv_reserve", _lib.qgemv_kv_reserve(cache._ref, _ints(cu, "cu", rows + 1, dev), _ints(out, "out", rows, dev),
+                                                    *cache._ws, _raw_stream(dev)))
+    return out
 
 
 def kv_write(cache, layer, k, v, cu, pos):
     """Writes one layer's new keys and values [tokens, heads_kv, head_dim] to the
     positions that kv_reserve gave (token cu[b] + i of row b to pos[b] + i)."""
-    hk, hv = _heads(k, "k", cache.k.dtype), _heads(v, "v", cache.k.dtype)
-    if k.shape != v.shape or tuple(k.shape[1:]) != (cache.heads_kv, cache.head_dim):
+    rows, dev, dtype = cache.rows, cache._dev, cache.dtype
+    hk, hv = _heads(k, "k", dtype, dev), _heads(v, "v", dtype, dev)
+    tokens, heads_kv, dim = k.shape
+    if v.shape != k.shape or heads_kv != cache.heads_kv or dim != cache.head_dim:
         raise ValueError("k and v must be [tokens, heads_kv, head_dim] of the cache")
-    p, o = _ints(cu, "cu", cache.rows + 1), _ints(pos, "pos", cache.rows)
-    _same_device(cache.k, k=k, v=v, cu=cu, pos=pos)
-    _q._check("qgemv_kv_write", _q.lib().qgemv_kv_write(cache._ref, layer, k.shape[0], ctypes.byref(hk), ctypes.byref(hv),
-                                                        p, o or 4, _q._stream(cache.k)))
+    _done("qgemv_kv_write", _lib.qgemv_kv_write(cache._ref, layer, tokens, hk, hv, _ints(cu, "cu", rows + 1, dev),
+                                                _ints(pos, "pos", rows, dev), _raw_stream(dev)))
 
 
 def kv_fork(cache, parents, out=None):
@@ -206,10 +203,10 @@ def kv_fork(cache, parents, out=None):
     are stale afterwards.  Returns out."""
     if out is None:
         out = cache.empty_rows(parents.numel())
-    p = _ints(parents, "parents", out.rows)
-    _same_device(cache.k, parents=parents)
-    ws = cache.ws if cache.ws.numel() >= out.ws.numel() else out.ws
-    _q._check("qgemv_kv_fork", _q.lib().qgemv_kv_fork(cache._ref, p or 4, out._ref, *_bytes(ws), _q._stream(cache.k)))
+    dev = cache._dev
+    ws = cache._ws if cache._ws[1] >= out._ws[1] else out._ws
+    _done("qgemv_kv_fork", _lib.qgemv_kv_fork(cache._ref, _ints(parents, "parents", out.rows, dev), out._ref, *ws,
+                                              _raw_stream(dev)))
     return out
 
 
@@ -220,12 +217,10 @@ def kv_compact(cache, pos, keep, count):
     [rows, max_keep]; pos -1 leaves a row alone, pos 0 with count 0 frees it."""
     if keep.dim() != 2:
         raise ValueError("keep must be [rows, max_keep]")
-    max_keep = keep.shape[1]
-    a, b = _ints(pos, "pos", cache.rows), _ints(count, "count", cache.rows)
-    c = _ints(keep, "keep", cache.rows * max_keep)
-    _same_device(cache.k, pos=pos, keep=keep, count=count)
-    _q._check("qgemv_kv_compact", _q.lib().qgemv_kv_compact(cache._ref, a or 4, c or None, max_keep, b or 4,
-                                                            *_bytes(cache.ws), _q._stream(cache.k)))
+    rows, dev, max_keep = cache.rows, cache._dev, keep.shape[1]
+    _done("qgemv_kv_compact", _lib.qgemv_kv_compact(
+        cache._ref, _ints(pos, "pos", rows, dev), _ints(keep, "keep", rows * max_keep, dev), max_keep,
+        _ints(count, "count", rows, dev), *cache._ws, _raw_stream(dev)))
 
 
 def attn_tree(q, cache, layer, cu, pos, mask=None, scale=None, out=None, ws=None):
@@ -236,30 +231,28 @@ def attn_tree(q, cache, layer, cu, pos, mask=None, scale=None, out=None, ws=None
     drafted tree: its ancestors and itself).  mask None: the new tokens up to
     itself; with one token per row that is a decode step.  ws: optional scratch
     of attn_tree_workspace_bytes(...) bytes.  Returns out, like q."""
-    hq = _heads(q, "q", cache.k.dtype)
+    dtype, dev, rows = cache.dtype, cache._dev, cache.rows
+    hq = _heads(q, "q", dtype, dev)
     tokens, heads, dim = q.shape
     if dim != cache.head_dim:
         raise ValueError("q must have the cache's head_dim")
     words, pm = 0, None
     if mask is not None:
-        _q._need(mask, torch.int64, "mask")
-        if mask.dim() != 2 or mask.shape[0] != tokens or mask.shape[1] < 1:
-            raise ValueError("mask must be [tokens, words]")
+        if mask.get_device() != dev or mask.dtype is not torch.int64:
+            raise TypeError("mask must be an int64 CUDA tensor on the same device as the others")
+        if mask.dim() != 2 or mask.shape[0] != tokens or mask.shape[1] < 1 or not mask.is_contiguous():
+            raise ValueError("mask must be contiguous [tokens, words]")
         words, pm = mask.shape[1], mask.data_ptr() or 8
-    rows = cache.rows
-    pc, pp = _ints(cu, "cu", rows + 1), _ints(pos, "pos", rows)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty(q.shape, dtype=dtype, device=q.device)
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    ho = _heads(out, "out", q.dtype)
-    _same_device(q, cache=cache.k, cu=cu, pos=pos, mask=mask, out=out, ws=ws)
     if ws is None:
-        ws = _ws(None, attn_tree_workspace_bytes(tokens, rows, heads, cache.heads_kv, dim), q.device)
-    else:
-        ws = _ws(ws, 0, q.device)
-    wp, wn = _bytes(ws)
-    _q._check("qgemv_attn_tree", _q.lib().qgemv_attn_tree(
-        _DTYPES[q.dtype], cache._ref, layer, tokens, heads, 1.0 / math.sqrt(dim) if scale is None else scale,
-        ctypes.byref(hq), pc, pp or 4, pm, words, ctypes.byref(ho), wp, wn, _q._stream(q)))
+        ws = torch.empty(attn_tree_workspace_bytes(tokens, rows, heads, cache.heads_kv, dim), dtype=torch.uint8,
+                         device=q.device)
+    wp, wn = _ws(ws, dev)
+    _done("qgemv_attn_tree", _lib.qgemv_attn_tree(
+        _DTYPES[dtype], cache._ref, layer, tokens, heads, 1.0 / math.sqrt(dim) if scale is None else scale, hq,
+        _ints(cu, "cu", rows + 1, dev), _ints(pos, "pos", rows, dev), pm, words, _heads(out, "out", dtype, dev), wp, wn,
+        _raw_stream(dev)))
     return out
