@@ -64,7 +64,10 @@ struct AttnArgs {
 
 // The choice of kernel, its split of the keys, and so the workspace, depend on
 // the sizes that the host knows (not on lengths on the device).
-constexpr int NARROW_WORKGROUPS = 512;
+// narrow kernel: waves per SIMD, and workgroups (of one wave per SIMD) that fill
+// the 256 compute units
+constexpr int narrow_waves(int) { return 2; }
+constexpr int narrow_workgroups(int rt) { return 256 * narrow_waves(rt); }
 constexpr int WIDE_WORKGROUPS = 512;
 constexpr int WIDE_BM = 128;
 constexpr size_t partial_bytes(size_t slots, int bm, int d) { return slots * bm * (size_t)(d + 2) * 4; }

@@ -130,45 +130,44 @@ __device__ __forceinline__ int64_t pool_token(const AttnArgs& a, int b, int kb) 
 }
 
 // What query token t of a row sees: every key below lim, and of the keys from
-// pos on those whose bit is set in its mask words.
+// pos up to all those whose bit is set in its mask words.  A token that the row
+// does not have (t >= n) sees nothing.  No branch here depends on the lane
+// (selects do): around the kernels' many live registers, code that only some
+// lanes run is where a compiler is most easily led to keep a register for
+// those lanes alone.
 template <bool PAGED>
 struct Sight {
-  int lim;
-  const uint64_t* words;  // NULL: lim alone
+  int lim, all;
+  const uint64_t* words;  // (of some token of the row, also for a token that it does not have)
   __device__ __forceinline__ void init(const AttnArgs& a, const Row& r, int t) {
+    const bool live = t < r.n;
+    all = live ? r.keys : 0;
     words = nullptr;
-    if (t >= r.n) {
-      lim = 0;
-      return;
-    }
     if constexpr (PAGED) {
-      if (a.mask) {
-        lim = r.pos;
-        words = a.mask + (int64_t)(r.q0 + t) * a.mask_words;
-      } else {
-        lim = r.pos + t + 1;
-      }
+      words = a.mask + (int64_t)(r.q0 + (live ? t : 0)) * a.mask_words;
+      lim = a.mask ? r.pos : r.pos + t + 1;
     } else {
       lim = a.causal ? r.pos + t + 1 : r.keys;
     }
-    lim = lim < 0 ? 0 : lim > r.keys ? r.keys : lim;
+    lim = lim < 0 ? 0 : lim > all ? all : lim;
   }
   // bit i: key kb + i is seen, i < 64
   __device__ __forceinline__ uint64_t window(const AttnArgs& a, const Row& r, int kb) const {
     auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };
     uint64_t v = below(lim - kb);
-    if (PAGED && words) {
-      const int i0 = kb - r.pos;
-      uint64_t m = 0;
-      if (i0 >= 0) {
-        const int w = i0 >> 6, s = i0 & 63;
-        if (w < a.mask_words) m = words[w] >> s;
-        if (s && w + 1 < a.mask_words) m |= words[w + 1] << (64 - s);
-      } else if (i0 > -64) {
-        m = words[0] << -i0;
+    if constexpr (PAGED)
+      if (a.mask) {
+        const int i0 = kb - r.pos;
+        uint64_t m = 0;
+        if (i0 >= 0) {
+          const int w = i0 >> 6, s = i0 & 63;
+          if (w < a.mask_words) m = words[w] >> s;
+          if (s && w + 1 < a.mask_words) m |= words[w + 1] << (64 - s);
+        } else if (i0 > -64) {
+          m = words[0] << -i0;
+        }
+        v |= m & below(all - kb);
       }
-      v |= m & below(r.keys - kb);
-    }
     return v;
   }
 };

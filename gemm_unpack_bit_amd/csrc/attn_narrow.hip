@@ -24,6 +24,8 @@
 // The waves of a workgroup take the steps of its key range in turn, each with
 // its own m, l, O, joined in LDS at the end.  Few rows leave few tiles, so the
 // key axis is split over workgroups (Units).
+#include <type_traits>
+
 #include "attn_common.hpp"
 
 namespace qg {
@@ -34,7 +36,7 @@ constexpr int WAVES = 4;
 
 // RT: 16-row tiles of query rows held by a wave (BM = 16 RT rows)
 template <typename E, int D, int RT, bool PAGED>
-__global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, int workgroups, int least) {
+__global__ void __launch_bounds__(64 * WAVES, narrow_waves(RT)) attn_narrow_kernel(AttnArgs a, int workgroups, int least) {
   constexpr int BM = 16 * RT;
   constexpr int KS = D / 32;  // matrix steps along head_dim
   constexpr int DL = D / 16;  // output columns of a lane
@@ -72,8 +74,9 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
       const uint16_t* q = a.q + (live ? (int64_t)(r.q0 + t) * a.q_token + (int64_t)(h * a.group + g) * a.q_head : 0);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        qf[i][s] = u4{0, 0, 0, 0};
-        if (live) qf[i][s] = *reinterpret_cast<const u4*>(q + 32 * s + 8 * quarter);
+        const u4 x = *reinterpret_cast<const u4*>(q + 32 * s + 8 * quarter);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qf[i][s][e] = live ? x[e] : 0;
       }
     }
     // keys that every row of the tile sees
@@ -93,51 +96,108 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
       for (int j = 0; j < DL; ++j) o[i][j] = f4{0.f, 0.f, 0.f, 0.f};
     }
 
+    // Loads of a step: two tiles of 16 keys, each 16 rows of one page, by a
+    // scalar base and a lane's 32-bit offset.  A tile past the row's last key
+    // falls back on the last tile that has any, and a key past the last is read
+    // from the last one's place.
     const uint16_t* kh = a.k + (int64_t)h * a.k_head;
     const uint16_t* vh = a.v + (int64_t)h * a.v_head;
-    // where the 16 keys from key kb (a multiple of 16) on start; a tile past
-    // the row's last key falls back on the last one that has any
-    auto tile_at = [&](int kb, int64_t& ko, int64_t& vo, int& last) {
-      const int top = (r.keys - 1) & ~15;
+    const uint32_t k_row = 2u * (uint32_t)a.k_token, v_row = 2u * (uint32_t)a.v_token;  // bytes
+    const int top = (r.keys - 1) & ~15;
+    auto token_at = [&](int kb) -> int64_t {
       kb = kb < top ? kb : top;
-      last = r.keys - 1 - kb;  // keys past it are read from its place
-      int64_t tok;
-      if constexpr (PAGED) {
-        tok = pool_token(a, b, kb);
-      } else {
-        tok = (int64_t)r.k0 + kb;
-      }
-      ko = tok * a.k_token;
-      vo = tok * a.v_token;
+      if constexpr (PAGED) return pool_token(a, b, kb);
+      else return (int64_t)r.k0 + kb;
     };
-
-    const int k_end = ku_end * KB < r.keys ? ku_end * KB : r.keys;
-    for (int kb = ku * KB + 32 * wave; kb < k_end; kb += 32 * WAVES) {
-      int64_t ko[2], vo[2];
-      int last[2];
-      tile_at(kb, ko[0], vo[0], last[0]);
-      tile_at(kb + 16, ko[1], vo[1], last[1]);
-      u4 kf[2][KS];
-      vw vf[8];
+    u4 kf[2][KS];
+    vw vf[8];
+    // (a lane's offsets in a tile with all its keys)
+    const uint32_t k_off = (uint32_t)n16 * k_row + 16u * quarter, v_off = 4u * quarter * v_row + 2u * DL * n16;
+    auto last_of = [&](int k0) { return r.keys - 1 - (k0 < top ? k0 : top); };
+    auto load_k = [&](int kb, const int64_t (&tok)[2]) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const uint16_t* p = kh + ko[x] + (int64_t)min(n16, last[x]) * a.k_token + 8 * quarter;
+        const int k0 = kb + 16 * x;
+        const char* p = reinterpret_cast<const char*>(kh + tok[x] * a.k_token);
+        uint32_t off = k_off;
+        if (k0 + 16 > r.keys) off = (uint32_t)min(n16, last_of(k0)) * k_row + 16u * quarter;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) kf[x][s] = *reinterpret_cast<const u4*>(p + 32 * s);
+        for (int s = 0; s < KS; ++s) kf[x][s] = *reinterpret_cast<const u4*>(p + off + 64 * s);
       }
+    };
+    auto load_v = [&](int kb, const int64_t (&tok)[2]) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < 2; ++x) {
+        const int k0 = kb + 16 * x;
+        const char* p = reinterpret_cast<const char*>(vh + tok[x] * a.v_token);
+        uint32_t off[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          vf[4 * x + i] = *reinterpret_cast<const vw*>(vh + vo[x] + (int64_t)min(4 * quarter + i, last[x]) * a.v_token +
-                                                       DL * n16);
+        for (int i = 0; i < 4; ++i) off[i] = v_off + i * v_row;
+        if (k0 + 16 > r.keys)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) off[i] = (uint32_t)min(4 * quarter + i, last_of(k0)) * v_row + 2u * DL * n16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vf[4 * x + i] = __builtin_nontemporal_load(reinterpret_cast<const vw*>(p + off[i]));
+      }
+    };
+
+    // Pipeline: the next step's keys are asked for as soon as this one's are
+    // used up, and its values likewise, into the same registers: at any time
+    // one or the other is on its way.  (The scheduling barriers keep the loads
+    // where they stand.)
+    const int k_end = ku_end * KB < r.keys ? ku_end * KB : r.keys;
+    int kb = ku * KB + 32 * wave;
+    // The values taken out of masked steps, added up in the wave's part of o_s
+    // (a key at a time for the rows that see it, a column per lane; no
+    // rescaling: they are infinite or NaN)
+    bool odd_any = false;
+    auto add_odd = [&](uint64_t odd, int kb) {
+      const AttnArgs e = args_again();
+      float* sums = &o_s[wave][0][0];
+      if (!odd_any)
+        for (int x = lane; x < BM * PITCH; x += 64) sums[x] = 0.f;
+      odd_any = true;
+      for (; odd; odd &= odd - 1) {
+        const int key = __builtin_ctzll(odd), at = min(kb + key, r.keys - 1);
+        const uint16_t* v = e.v + (int64_t)h * e.v_head + (token_at(at & ~15) + (at & 15)) * e.v_token;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          uint32_t see = (uint32_t)__ballot(sight[i].window(e, r, kb) >> key & 1) & 0xFFFF;
+          for (; see; see &= see - 1)
+#pragma unroll
+            for (int d0 = 0; d0 < D; d0 += 64) {
+              const uint16_t y = v[d0 + lane];
+              sums[(16 * i + __builtin_ctz(see)) * PITCH + d0 + lane] += nonfinite<E>(y) & 0x8000u ? E::value(y) : 0.f;
+            }
+        }
+      }
+    };
+    int64_t tok1[2];  // the next step's
+    auto step = [&](auto more) {
+      f4 sc[RT][2];
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          sc[i][x] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < KS; ++s) sc[i][x] = E::mfma16(kf[x][s], qf[i][s], sc[i][x]);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (decltype(more)::value) load_k(kb + 32 * WAVES, tok1);
+      __builtin_amdgcn_sched_barrier(0);
 
       const bool masked = kb + 32 > common;
-      uint64_t seen[RT];
       uint64_t odd = 0;  // keys of the step with a value that is not finite (masked steps)
       if (masked) {
 #pragma unroll
-        for (int i = 0; i < RT; ++i) seen[i] = sight[i].window(a, r, kb) >> (4 * quarter);
+        for (int i = 0; i < RT; ++i) {
+          const uint64_t seen = sight[i].window(a, r, kb) >> (4 * quarter);
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[i][x][e] = seen >> (16 * x + e) & 1 ? sc[i][x][e] : NEG_INF;
+        }
         // a weight of 0 does not cancel a value that is infinite or NaN:
         // take those out and add them for the rows that see them
         uint32_t bad = 0;
@@ -151,7 +211,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
             // halves to clear: 0x8000 of a half becomes 0xFFFF
             vf[i][w] &= ~((x - (x >> 15)) | x);
           }
-          if (f) bad |= 1u << i;
+          bad |= f ? 1u << i : 0u;
         }
         if (__any(bad))
 #pragma unroll
@@ -163,24 +223,11 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
 
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        f4 sc[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          sc[x] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int s = 0; s < KS; ++s) sc[x] = E::mfma16(kf[x][s], qf[i][s], sc[x]);
-        }
-        if (masked) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[x][e] = seen[i] >> (16 * x + e) & 1 ? sc[x][e] : NEG_INF;
-        }
-        float mx = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
-                         fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
+        const f4 s0 = sc[i][0], s1 = sc[i][1];
+        float mx = fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])), fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3])));
         mx = quarter_max(mx);
         mx = mx == NEG_INF ? NEG_INF : mx * a.scale;
-        if (__any(mx > m[i])) {
+        if (__any(mx > m[i] + E::SLACK)) {
           const float mn = fmaxf(m[i], mx), w = mn == NEG_INF ? 1.f : exp2_(m[i] - mn);
           m[i] = mn;
           l[i] *= w;
@@ -191,7 +238,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
         float p[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float x = sc[e >> 2][e & 3];
+          const float x = e < 4 ? s0[e & 3] : s1[e & 3];
           p[e] = x == NEG_INF ? 0.f : exp2_(fmaf(x, a.scale, -base));
           l[i] += p[e];
         }
@@ -204,21 +251,25 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
             va[w] = __builtin_amdgcn_perm(vf[2 * w + 1][j / 2], vf[2 * w][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
           o[i][j] = E::mfma16(va, pf, o[i][j]);
         }
-        if (odd) {
-          const uint64_t mine = sight[i].window(a, r, kb);
-          for (uint64_t left_keys = odd; left_keys; left_keys &= left_keys - 1) {
-            const int key = __builtin_ctzll(left_keys), x = key >> 4;
-            const uint16_t* v = vh + vo[x] + (int64_t)min(key & 15, last[x]) * a.v_token;
-#pragma unroll
-            for (int j = 0; j < DL; ++j)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint16_t y = v[DL * (4 * quarter + e) + j];
-                if (mine >> key & 1 && nonfinite<E>(y) & 0x8000u) o[i][j][e] += E::value(y);
-              }
-          }
-        }
       }
+      if (odd) add_odd(odd, kb);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (decltype(more)::value) load_v(kb + 32 * WAVES, tok1);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if (kb < k_end) {
+      const int64_t tok0[2] = {token_at(kb), token_at(kb + 16)};
+      load_k(kb, tok0);
+      load_v(kb, tok0);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) tok1[x] = token_at(kb + 32 * WAVES + 16 * x);
+      for (; kb + 32 * WAVES < k_end; kb += 32 * WAVES) {
+        // (looked up a step ahead of the loads)
+        const int64_t tok2[2] = {token_at(kb + 64 * WAVES), token_at(kb + 64 * WAVES + 16)};
+        step(std::true_type{});
+        tok1[0] = tok2[0], tok1[1] = tok2[1];
+      }
+      step(std::false_type{});
     }
 
     // join the waves
@@ -228,9 +279,12 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int j = 0; j < DL; j += 4)
-          *reinterpret_cast<f4*>(&o_s[wave][row][DL * (4 * quarter + e) + j]) =
-              f4{o[i][j][e], o[i][j + 1][e], o[i][j + 2][e], o[i][j + 3][e]};
+        for (int j = 0; j < DL; j += 4) {
+          f4* at = reinterpret_cast<f4*>(&o_s[wave][row][DL * (4 * quarter + e) + j]);
+          f4 x = f4{o[i][j][e], o[i][j + 1][e], o[i][j + 2][e], o[i][j + 3][e]};
+          if (odd_any) x += *at;
+          *at = x;
+        }
       const float sum = quarter_sum(l[i]);
       if (quarter == 0) m_s[wave][row] = m[i], l_s[wave][row] = sum;
     }
@@ -307,10 +361,10 @@ __global__ void __launch_bounds__(256) attn_narrow_join_kernel(AttnArgs a, int w
 template <typename E, int D, int RT, bool PAGED>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
   const int least = 1;
-  hipLaunchKernelGGL((attn_narrow_kernel<E, D, RT, PAGED>), dim3(NARROW_WORKGROUPS), dim3(64 * WAVES), 0, s, a,
-                     NARROW_WORKGROUPS, least);
+  hipLaunchKernelGGL((attn_narrow_kernel<E, D, RT, PAGED>), dim3(narrow_workgroups(RT)), dim3(64 * WAVES), 0, s, a,
+                     narrow_workgroups(RT), least);
   hipLaunchKernelGGL((attn_narrow_join_kernel<E, D, RT, PAGED>), dim3((unsigned)(a.tokens * a.heads)), dim3(256), 0, s, a,
-                     NARROW_WORKGROUPS, least);
+                     narrow_workgroups(RT), least);
   return hipGetLastError();
 }
 

@@ -93,8 +93,9 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
       a.q + (live ? (int64_t)(r.q0 + t) * a.q_token + (int64_t)(g.h * a.group + gh) * a.q_head : 0);
 #pragma unroll
   for (int s = 0; s < QS; ++s) {
-    qf[s] = u4{0, 0, 0, 0};
-    if (live) qf[s] = *reinterpret_cast<const u4*>(q + 16 * s + 8 * half);
+    const u4 x = *reinterpret_cast<const u4*>(q + 16 * s + 8 * half);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) qf[s][e] = live ? x[e] : 0;
   }
   const bool active = g.tile * BM + 32 * wave < rows;  // (wave-uniform)
   // keys that every row of the tile sees, and the keys that any sees
@@ -243,7 +244,7 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
         any |= x;
         w[j] &= ~((x - (x >> 15)) | x);
       }
-      if (any) p[i] = w;
+      p[i] = w;
       f |= any;
     }
     if (f) atomicOr(&flag[key >> 5], 1u << (key & 31));
@@ -264,14 +265,14 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
         tok = (int64_t)r.k0 + at;
       }
       const uint16_t* v = vh + tok * a.v_token;
-      if (mine >> key & 1)
+      const uint32_t sees = mine >> key & 1 ? 0x8000u : 0u;
 #pragma unroll
-        for (int db = 0; db < DB; ++db)
+      for (int db = 0; db < DB; ++db)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint16_t y = v[32 * db + 8 * (i / 4) + 4 * half + i % 4];
-            if (nonfinite<E>(y) & 0x8000u) o[db][i] += E::value(y);
-          }
+        for (int i = 0; i < 16; ++i) {
+          const uint16_t y = v[32 * db + 8 * (i / 4) + 4 * half + i % 4];
+          o[db][i] += nonfinite<E>(y) & sees ? E::value(y) : 0.f;
+        }
     }
   };
 

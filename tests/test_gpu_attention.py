@@ -314,7 +314,7 @@ def test_tree_rows_without_keys_and_odd_values_of_unseen_nodes(dtype, n):
 
 
 @pytest.mark.parametrize("heads,kv,D,ns,pos", [
-    (8, 1, 128, [1], [40000]), (32, 8, 128, [1] * 5, [20000, 3, 700, 9000, 64]), (8, 2, 64, [50, 3], [17000, 200]),
+    (8, 1, 128, [1], [40000]), (64, 8, 128, [1] * 32, [(97 * i * i) % 4001 for i in range(32)]), (32, 8, 128, [1] * 5, [20000, 3, 700, 9000, 64]), (8, 2, 64, [50, 3], [17000, 200]),
 ])
 def test_tree_long_rows(heads, kv, D, ns, pos):
     """Rows of very different lengths: the split of long ones and the join of their parts."""
