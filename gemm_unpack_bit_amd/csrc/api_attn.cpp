@@ -141,8 +141,8 @@ size_t qgemv_attn_prompt_workspace_bytes(int tokens, int tokens_k, int batch, in
   if (check_counts(tokens, batch, heads, heads_kv) || tokens_k < 0 || !tokens || !batch) return 0;
   if (head_dim != 64 && head_dim != 128) return 0;
   const int group = heads / heads_kv, rt = qg::narrow_tiles(tokens, batch, group);
-  if (rt) return qg::partial_bytes(2 * (size_t)qg::narrow_workgroups(rt), 16 * rt, head_dim);
-  const int splits = qg::prompt_splits(tokens, tokens_k, batch, heads_kv, group);
+  if (rt) return qg::partial_bytes(2 * qg::NARROW_WORKGROUPS, 16 * rt, head_dim);
+  const int splits = qg::prompt_splits(tokens, tokens_k, batch, heads_kv, group, head_dim);
   if (splits == 1) return 0;
   return qg::partial_bytes((size_t)qg::prompt_tiles(tokens, batch, group) * heads_kv * splits, qg::WIDE_BM, head_dim);
 }
@@ -199,8 +199,8 @@ size_t qgemv_attn_tree_workspace_bytes(int tokens, int rows, int heads, int head
   if (check_counts(tokens, rows, heads, heads_kv) || !tokens || !rows) return 0;
   if (head_dim != 64 && head_dim != 128) return 0;
   const int rt = qg::narrow_tiles(tokens, rows, heads / heads_kv);
-  if (rt) return qg::partial_bytes(2 * (size_t)qg::narrow_workgroups(rt), 16 * rt, head_dim);
-  return qg::partial_bytes(2 * qg::WIDE_WORKGROUPS, qg::WIDE_BM, head_dim);
+  if (rt) return qg::partial_bytes(2 * qg::NARROW_WORKGROUPS, 16 * rt, head_dim);
+  return qg::partial_bytes(2 * (size_t)qg::wide_workgroups(head_dim), qg::WIDE_BM, head_dim);
 }
 
 int qgemv_attn_tree(int dtype, const qgemv_kv_cache* c, int layer, int tokens, int heads, float scale,

@@ -64,11 +64,12 @@ struct AttnArgs {
 
 // The choice of kernel, its split of the keys, and so the workspace, depend on
 // the sizes that the host knows (not on lengths on the device).
-// narrow kernel: waves per SIMD, and workgroups (of one wave per SIMD) that fill
-// the 256 compute units
-constexpr int narrow_waves(int) { return 2; }
-constexpr int narrow_workgroups(int rt) { return 256 * narrow_waves(rt); }
-constexpr int WIDE_WORKGROUPS = 512;
+// Waves per SIMD that the kernels' registers allow, and the workgroups (of one
+// wave per SIMD) that then fill the 256 compute units: the split of a tree's
+// keys is over that many.
+constexpr int NARROW_WORKGROUPS = 512;
+constexpr int wide_waves(int head_dim) { return head_dim == 64 ? 3 : 2; }
+constexpr int wide_workgroups(int head_dim) { return 256 * wide_waves(head_dim); }
 constexpr int WIDE_BM = 128;
 constexpr size_t partial_bytes(size_t slots, int bm, int d) { return slots * bm * (size_t)(d + 2) * 4; }
 
@@ -80,11 +81,11 @@ inline int narrow_tiles(int tokens, int rows, int group) {
 }
 inline int prompt_tiles(int tokens, int rows, int group) { return (int)((int64_t)tokens * group / WIDE_BM) + rows; }
 // parts of the keys of each tile, where whole tiles would leave compute units
-// idle: up to 512 workgroups, of at least 4 key tiles on average
-inline int prompt_splits(int tokens, int tokens_k, int rows, int heads_kv, int group) {
+// idle: as many workgroups as fit, of at least 4 key tiles on average
+inline int prompt_splits(int tokens, int tokens_k, int rows, int heads_kv, int group, int head_dim) {
   const int64_t items = (int64_t)prompt_tiles(tokens, rows, group) * heads_kv;
-  const int64_t most = tokens_k / rows / 256;
-  const int64_t s = 512 / items < most ? 512 / items : most;
+  const int64_t most = tokens_k / rows / 256, fit = wide_workgroups(head_dim) / items;
+  const int64_t s = fit < most ? fit : most;
   return s < 1 ? 1 : (int)s;
 }
 

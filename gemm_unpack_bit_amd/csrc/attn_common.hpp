@@ -276,7 +276,7 @@ __device__ __forceinline__ uint32_t scan24(uint32_t v) {
 // The split of the key axis.  An item is a tile of BM query rows (row
 // t * group + g: query token t, head g of the key head's group) of one row and
 // key head; its keys are cut into units of KB.  The units of all items, in the
-// order row, tile, key head, unit, are shared out evenly: workgroup c takes
+// order row, key head, tile, unit, are shared out evenly: workgroup c takes
 // units [c * per, (c + 1) * per), per = max(least, ceil(total / workgroups)).
 // So a long row is worked on by many workgroups and short ones share one,
 // whatever the mix, and no workgroup waits for another.  An item that lies in
@@ -285,8 +285,20 @@ __device__ __forceinline__ uint32_t scan24(uint32_t v) {
 // 2 c, one that starts later in slot 2 c + 1), which a second kernel joins in
 // key order.
 //
+// Neighbouring shares read the same keys (the tiles of a row and key head come
+// one after the other) at about the same time, so they belong on one XCD, where
+// the second one finds them in the cache: workgroups go to the XCDs round robin,
+// and share_of gives each XCD a run of shares.
+//
 // A wave keeps 64 rows at a time, one per lane, with the running sum of their
 // units; up to 64 rows are read once.
+constexpr int NXCD = 8;
+// (`shares` of them have work; a result past them means none)
+__device__ __forceinline__ int share_of(int workgroup, int shares) {
+  const int run = (shares + NXCD - 1) / NXCD, in = workgroup / NXCD;
+  return in < run ? (workgroup % NXCD) * run + in : shares;
+}
+
 template <int BM, int KB, bool PAGED>
 struct Walk {
   int64_t total, per;
@@ -328,6 +340,7 @@ struct Walk {
     const int64_t even = (total + workgroups - 1) / workgroups;
     per = even > least ? even : least;
   }
+  __device__ __forceinline__ int shares() const { return (int)((total + per - 1) / per); }
   __device__ __forceinline__ Row row(int lane) const {
     Row r;
     r.q0 = __builtin_amdgcn_readlane(mine.q0, lane);
@@ -355,8 +368,9 @@ struct Walk {
     const int64_t in = u - first_of(lane), item = in / p.of, left = u_end - u;
     p.k0 = uniform((int)(in - item * p.of));
     p.k1 = uniform((int)(p.k0 + left < p.of ? p.k0 + left : p.of));
-    p.h = uniform((int)(item % a.heads_kv));
-    p.tile = uniform((int)(item / a.heads_kv));
+    const int n = tiles(a, p.r);
+    p.h = uniform((int)(item / n));
+    p.tile = uniform((int)(item % n));
     return p;
   }
   // row b, and its first unit

@@ -36,7 +36,7 @@ constexpr int WAVES = 4;
 
 // RT: 16-row tiles of query rows held by a wave (BM = 16 RT rows)
 template <typename E, int D, int RT, bool PAGED>
-__global__ void __launch_bounds__(64 * WAVES, narrow_waves(RT)) attn_narrow_kernel(AttnArgs a, int workgroups, int least) {
+__global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, int workgroups, int least) {
   constexpr int BM = 16 * RT;
   constexpr int KS = D / 32;  // matrix steps along head_dim
   constexpr int DL = D / 16;  // output columns of a lane
@@ -51,7 +51,8 @@ __global__ void __launch_bounds__(64 * WAVES, narrow_waves(RT)) attn_narrow_kern
   const int n16 = lane & 15, quarter = lane >> 4;
   U walk;
   walk.init(a, workgroups, least);
-  int64_t u = (int64_t)blockIdx.x * walk.per;
+  const int c = share_of(blockIdx.x, walk.shares());
+  int64_t u = c * walk.per;
   const int64_t u_end = u + walk.per < walk.total ? u + walk.per : walk.total;
   const int64_t u_begin = u;
   const Partials<BM, D> parts(a.ws, 2 * (int64_t)workgroups);
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(64 * WAVES, narrow_waves(RT)) attn_narrow_kern
     }
     __syncthreads();
     const bool whole = ku == 0 && ku_end == piece.of;
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (u != u_begin);
+    const int64_t slot = 2 * (int64_t)c + (u != u_begin);
     constexpr int TPR = 64 * WAVES / 16;  // 16 threads per row, DL columns each
     static_assert(TPR == 16, "a row's columns are DL per thread");
 #pragma unroll
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(256) attn_narrow_join_kernel(AttnArgs a, int w
   const int t = token - r.q0;
   if (t < 0 || t >= r.n) return;
   const int qr = t * a.group + head - h * a.group, tile = qr / BM;
-  const typename U::Parts p = walk.parts(first + (int64_t)(tile * a.heads_kv + h) * U::units(r), r);
+  const typename U::Parts p = walk.parts(first + (int64_t)(h * U::tiles(a, r) + tile) * U::units(r), r);
   if (p.n == 1) return;
   join_row<E, PL>(Partials<BM, D>(a.ws, 2 * (int64_t)workgroups), qr - tile * BM, p.n, [&](int i) { return p.slot(i); },
                   a.o + (int64_t)token * a.o_token + (int64_t)head * a.o_head, true, threadIdx.x, &buf);
@@ -361,10 +362,10 @@ __global__ void __launch_bounds__(256) attn_narrow_join_kernel(AttnArgs a, int w
 template <typename E, int D, int RT, bool PAGED>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
   const int least = 1;
-  hipLaunchKernelGGL((attn_narrow_kernel<E, D, RT, PAGED>), dim3(narrow_workgroups(RT)), dim3(64 * WAVES), 0, s, a,
-                     narrow_workgroups(RT), least);
+  hipLaunchKernelGGL((attn_narrow_kernel<E, D, RT, PAGED>), dim3(NARROW_WORKGROUPS), dim3(64 * WAVES), 0, s, a,
+                     NARROW_WORKGROUPS, least);
   hipLaunchKernelGGL((attn_narrow_join_kernel<E, D, RT, PAGED>), dim3((unsigned)(a.tokens * a.heads)), dim3(256), 0, s, a,
-                     narrow_workgroups(RT), least);
+                     NARROW_WORKGROUPS, least);
   return hipGetLastError();
 }
 

@@ -425,7 +425,7 @@ __device__ __forceinline__ void split_range(const AttnArgs& a, const Row& r, int
 }
 
 template <typename E, int D>
-__global__ void __launch_bounds__(64 * WAVES, 2) attn_prompt_kernel(AttnArgs a, int tiles, int splits) {
+__global__ void __launch_bounds__(64 * WAVES, wide_waves(D)) attn_prompt_kernel(AttnArgs a, int tiles, int splits) {
   __shared__ Buffers<D> k0, k1, v0, v1;
   __shared__ uint32_t flag[2];
   Segment g;
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(AttnArgs a, int s
 // Trees over the paged cache: the units of all items shared out evenly
 // (Units), so rows of very different lengths keep every workgroup busy.
 template <typename E, int D>
-__global__ void __launch_bounds__(64 * WAVES, 2) attn_tree_kernel(AttnArgs a, int workgroups, int least) {
+__global__ void __launch_bounds__(64 * WAVES, wide_waves(D)) attn_tree_kernel(AttnArgs a, int workgroups, int least) {
   using U = Walk<BM, KB, true>;
   __shared__ Buffers<D> k0, k1, v0, v1;
   __shared__ uint32_t flag[2];
@@ -469,12 +469,13 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_tree_kernel(AttnArgs a, in
   for (int64_t done = 0;;) {
     U walk;
     walk.init(a, workgroups, least);
-    const int64_t u_begin = (int64_t)blockIdx.x * walk.per, u = u_begin + done;
+    const int c = share_of(blockIdx.x, walk.shares());
+    const int64_t u_begin = c * walk.per, u = u_begin + done;
     const int64_t u_end = u_begin + walk.per < walk.total ? u_begin + walk.per : walk.total;
     if (u >= u_end) break;
     const typename U::Piece p = walk.seek(a, u, u_end);
     Segment g{p.r, p.b, p.h, p.tile, p.k0, p.k1, 0};
-    g.slot = g.u0 == 0 && g.u1 == p.of ? -1 : 2 * (int64_t)blockIdx.x + (done != 0);
+    g.slot = g.u0 == 0 && g.u1 == p.of ? -1 : 2 * (int64_t)c + (done != 0);
     done += g.u1 - g.u0;
     run_segment<E, D, true>(g, 2 * (int64_t)workgroups, k0, k1, v0, v1, flag);
   }
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(AttnArgs a, int wor
   walk.seek_row(a, b, r, first);
   const int in = tile - first_at(r.q0, b);
   if (in < 0 || in >= U::tiles(a, r)) return;
-  const typename U::Parts p = walk.parts(first + (int64_t)(in * a.heads_kv + h) * U::units(r), r);
+  const typename U::Parts p = walk.parts(first + (int64_t)(h * U::tiles(a, r) + in) * U::units(r), r);
   if (p.n == 1) return;
   const int row = 16 * (blockIdx.x % (BM / 16)) + (threadIdx.x >> 4), qr = in * BM + row;
   const int t = qr / a.group, head = h * a.group + qr - t * a.group;
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(AttnArgs a, int wor
 template <typename E, int D>
 hipError_t prompt(const AttnArgs& a, hipStream_t s) {
   const int tiles = prompt_tiles(a.tokens, a.rows, a.group);
-  const int splits = prompt_splits(a.tokens, a.tokens_k, a.rows, a.heads_kv, a.group);
+  const int splits = prompt_splits(a.tokens, a.tokens_k, a.rows, a.heads_kv, a.group, D);
   const int64_t grid = (int64_t)tiles * a.heads_kv * splits;
   hipLaunchKernelGGL((attn_prompt_kernel<E, D>), dim3((unsigned)grid), dim3(64 * WAVES), 0, s, a, tiles, splits);
   if (splits > 1)
@@ -519,10 +520,10 @@ hipError_t prompt(const AttnArgs& a, hipStream_t s) {
 
 template <typename E, int D>
 hipError_t tree(const AttnArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((attn_tree_kernel<E, D>), dim3(WIDE_WORKGROUPS), dim3(64 * WAVES), 0, s, a, WIDE_WORKGROUPS, 1);
+  hipLaunchKernelGGL((attn_tree_kernel<E, D>), dim3(wide_workgroups(D)), dim3(64 * WAVES), 0, s, a, wide_workgroups(D), 1);
   hipLaunchKernelGGL((attn_tree_join_kernel<E, D>),
                      dim3((unsigned)prompt_tiles(a.tokens, a.rows, a.group) * (BM / 16), (unsigned)a.heads_kv), dim3(256), 0,
-                     s, a, WIDE_WORKGROUPS, 1);
+                     s, a, wide_workgroups(D), 1);
   return hipGetLastError();
 }
 

@@ -50,27 +50,43 @@ __device__ __forceinline__ int block_scan(int v, int& total, int* red) {
 
 // The lowest `want` free pages into list, in order; returns how many there are
 // (<= want).  All threads of the workgroup; ends with a barrier, so list can
-// be read by any of them.
-__device__ __forceinline__ int find_free(const int32_t* refs, int pages, int want, int32_t* list, int* red) {
+// be read by any of them.  A wave takes 512 neighbouring pages, 64 at a time,
+// and counts by ballots.
+template <typename L>
+__device__ __forceinline__ int find_free(const int32_t* refs, int pages, int want, L* list, int* red) {
+  constexpr int EACH = 8;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   int found = 0;
-  for (int p0 = 0; p0 < pages && found < want; p0 += 8 * SCAN) {
-    const int p = p0 + 8 * (int)threadIdx.x;
-    uint32_t free = 0;
+  for (int p0 = 0; p0 < pages && found < want; p0 += EACH * SCAN) {
+    const int p = p0 + w * 64 * EACH + lane;
+    int r[EACH];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (p + i < pages && refs[p + i] == 0) free |= 1u << i;
-    int total;
-    int at = found + block_scan(__builtin_popcount(free), total, red);
+    for (int i = 0; i < EACH; ++i) r[i] = p + 64 * i < pages ? refs[p + 64 * i] : 1;
+    uint64_t free[EACH];
+    int n = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (free >> i & 1) {
-        if (at < want) list[at] = p + i;
-        ++at;
-      }
+    for (int i = 0; i < EACH; ++i) {
+      free[i] = __ballot(r[i] == 0);
+      n += __builtin_popcountll(free[i]);
+    }
+    if (lane == 0) red[w] = n;
+    __syncthreads();
+    int at = found, total = 0;
+#pragma unroll
+    for (int i = 0; i < SCAN / 64; ++i) {
+      const int x = red[i];
+      at += i < w ? x : 0;
+      total += x;
+    }
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const int mine = at + __builtin_popcountll(free[i] & ((1ull << lane) - 1));
+      if (free[i] >> lane & 1 && mine < want) list[mine] = p + 64 * i;
+      at += __builtin_popcountll(free[i]);
+    }
     found += total;
+    __syncthreads();
   }
-  __threadfence_block();
-  __syncthreads();
   return found < want ? found : want;
 }
 
@@ -105,20 +121,25 @@ __global__ void __launch_bounds__(SCAN) kv_reserve_kernel(KvArgs c, const int32_
     }
     return r;
   };
-  int64_t want = 0;
-  for (int b0 = 0; b0 < c.rows; b0 += SCAN) {
-    int total;
-    block_scan(row(b0 + threadIdx.x).need, total, red);
-    want += total;
+  Row r = row(threadIdx.x);
+  int before, total;  // (the first 1024 rows are read and summed once)
+  before = block_scan(r.need, total, red);
+  int64_t want = total;
+  for (int b0 = SCAN; b0 < c.rows; b0 += SCAN) {
+    int more;
+    block_scan(row(b0 + threadIdx.x).need, more, red);
+    want += more;
   }
   const int got = want ? find_free(c.refs, c.pages, want < c.pages ? (int)want : c.pages, w.free_list, red) : 0;
   int64_t given = 0;
   int status = 0;
   for (int b0 = 0; b0 < c.rows; b0 += SCAN) {
     const int b = b0 + threadIdx.x;
-    const Row r = row(b);
-    int total;
-    const int64_t at = given + block_scan(r.need, total, red);
+    if (b0) {
+      r = row(b);
+      before = block_scan(r.need, total, red);
+    }
+    const int64_t at = given + before;
     given += total;
     const bool fits = r.need == 0 || at + r.need <= got;
     const bool ok = b < c.rows && !r.bad && fits;
@@ -271,6 +292,87 @@ __global__ void __launch_bounds__(SCAN) kv_fork_pages_kernel(KvArgs c, KvArgs ou
   if (threadIdx.x == 0 && got < want) atomicOr(c.status, KV_NO_PAGES);
 }
 
+// kv_fork_rows_kernel and kv_fork_pages_kernel in one workgroup, a thread per
+// table entry: for few entries, where the second launch costs more.
+constexpr int FORK_ROWS = 256;
+__global__ void __launch_bounds__(SCAN) kv_fork_small_kernel(KvArgs c, const int32_t* parents, KvArgs out, KvScratch w) {
+  __shared__ int red[SCAN / 64];
+  // of the old rows: children, length; of the new rows: parent, and whether an
+  // earlier new row has it too
+  __shared__ int kids[FORK_ROWS], lens[FORK_ROWS], par[FORK_ROWS], later[FORK_ROWS], list[FORK_ROWS];
+  const int page = 1 << c.page_shift, x = threadIdx.x;
+  if (x < FORK_ROWS) {
+    kids[x] = 0;
+    lens[x] = x < c.rows ? max(c.lens[x], 0) : 0;
+    const int p = x < out.rows ? parents[x] : -1;
+    par[x] = (unsigned)p < (unsigned)c.rows ? p : -1;
+    if (p != -1 && par[x] < 0) atomicOr(c.status, KV_BAD_INDEX);
+  }
+  __syncthreads();
+  if (x < out.rows && par[x] >= 0) {
+    atomicAdd(&kids[par[x]], 1);
+    int e = 0;
+    for (int i = 0; i < x; ++i) e |= par[i] == par[x];
+    later[x] = e;
+  }
+  __syncthreads();
+  auto full_of = [&](int len) { return min(len >> c.page_shift, c.max_pages); };
+  auto part_of = [&](int len) { return (len & (page - 1)) && full_of(len) < c.max_pages; };
+  int len = 0, src = -1;  // of new row x
+  if (x < out.rows && par[x] >= 0) {
+    len = lens[par[x]];
+    if (part_of(len) && later[x]) {
+      const int p = c.tables[(int64_t)par[x] * c.max_pages + full_of(len)];
+      src = (unsigned)p < (unsigned)c.pages ? p : -1;
+      if (src < 0) len = full_of(len) << c.page_shift;
+    }
+  }
+  const int rows = max(c.rows, out.rows), entries = rows * c.max_pages;
+  for (int e = x; e < entries; e += SCAN) {
+    const int b = e / c.max_pages, i = e - b * c.max_pages;
+    if (b < c.rows && kids[b] != 1) {
+      const int full = full_of(lens[b]);
+      if (i < full || (i == full && part_of(lens[b]) && kids[b] == 0)) {
+        const int p = c.tables[e];
+        if ((unsigned)p < (unsigned)c.pages) atomicAdd(&c.refs[p], kids[b] - 1);
+      }
+    }
+    if (b < out.rows && !(par[b] >= 0 && later[b] && i == full_of(lens[par[b]]))) {
+      int entry = -1;
+      if (par[b] >= 0) {
+        const int n = lens[par[b]], full = full_of(n);
+        if (i < full || (i == full && part_of(n))) entry = c.tables[(int64_t)par[b] * c.max_pages + i];
+      }
+      out.tables[e] = entry;
+    }
+  }
+  // the counts have to be in memory (this XCD's cache) before they are
+  // searched: every wave waits for its atomics, then all for one another
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0
+  int want;
+  const int at = block_scan(src >= 0, want, red);
+  const int got = want ? find_free(c.refs, c.pages, want, list, red) : 0;
+  // (a later child's entry for its partial page is written here alone)
+  if (x < out.rows) {
+    int fresh = -1;
+    if (src >= 0) {
+      if (at < got) {
+        fresh = list[at];
+        c.refs[fresh] = 1;
+        w.dst[x] = fresh;
+      } else {
+        src = -1;
+        len = full_of(len) << c.page_shift;
+      }
+    }
+    if (par[x] >= 0 && later[x] && full_of(lens[par[x]]) < out.max_pages)
+      out.tables[(int64_t)x * out.max_pages + full_of(lens[par[x]])] = fresh;
+    out.lens[x] = len;
+    w.src[x] = src;
+  }
+  if (x == 0 && got < want) atomicOr(c.status, KV_NO_PAGES);
+}
+
 // Copies the tokens of the pages that kv_fork_pages_kernel gave out: grid
 // (pieces of one token over all layers, keys and values; rows).  A thread
 // moves its 16-byte piece of every token, four at a time in flight.
@@ -300,81 +402,79 @@ __global__ void __launch_bounds__(256) kv_fork_copy_kernel(KvArgs c, KvArgs out,
 // compact
 // ---------------------------------------------------------------------------
 
-// Whether row b can be compacted, from the state before the call; every
-// thread of the workgroup gets the same answer and `bad` the reason.
-__device__ __forceinline__ bool compactable(const KvArgs& c, int b, int pos, int count, const int32_t* keep,
-                                            int max_keep, int& bad) {
-  bad = 0;
-  if (pos < 0) {
-    bad = pos < -1 ? KV_BAD_INDEX : 0;
-    return false;
-  }
-  const int len = c.lens[b];
-  if (count < 0 || count > max_keep || pos > len || pages_of(len, c.page_shift) > c.max_pages) {
-    bad = KV_BAD_INDEX;
-    return false;
-  }
-  int wrong = 0;
-  for (int j = threadIdx.x & 63; j < count; j += 64) {
-    const int s = keep[j], before = j ? keep[j - 1] : -1;
-    if (s <= before || s >= len - pos) wrong |= KV_BAD_INDEX;
+// Moves the kept tokens: grid (pieces of one token over all layers, keys and
+// values; rows).  Lane j of every wave looks up kept token j (64 at a time):
+// where it is and goes, and whether the row can be compacted at all, from the
+// state before the call, so every workgroup of a row comes to the same answer;
+// the first one leaves it for the next kernel.  Then a thread moves its 16-byte
+// piece of every token in order, eight at a time: keep is strictly ascending,
+// so the places that a batch writes (up to pos + j + 7) are never sources of a
+// later one (from pos + j + 8 on).
+__global__ void __launch_bounds__(256) kv_compact_move_kernel(KvArgs c, const int32_t* pos_, const int32_t* keep_,
+                                                              int max_keep, const int32_t* count_, KvScratch w, int n) {
+  const int b = blockIdx.y, lane = threadIdx.x & 63;
+  const int pos = pos_[b], count = count_[b], len = c.lens[b];
+  const int32_t* keep = keep_ + (int64_t)b * max_keep;
+  const int32_t* table = c.tables + (int64_t)b * c.max_pages;
+  const int inside = (1 << c.page_shift) - 1;
+  const bool sound = pos >= 0 && count >= 0 && count <= max_keep && pos <= len && pages_of(len, c.page_shift) <= c.max_pages;
+  // token t of the kept ones: its source and destination in the pool (in
+  // tokens), and what is wrong with it
+  int64_t from, to;
+  auto look = [&](int t) -> int {
+    from = to = 0;
+    if (!sound || t >= count) return 0;
+    const int s = keep[t], before = t ? keep[t - 1] : -1, p = pos + t;
+    const int dg = p >> c.page_shift;
+    const int dst = dg < c.max_pages ? table[dg] : -1;
+    if (s <= before || s >= len - pos) return KV_BAD_INDEX;
     // the page of a token that moves, or of the last one where the row ends
     // inside it, may not be another row's too
-    const int p = pos + j;
-    if (s != j || (j == count - 1 && (p + 1) & ((1 << c.page_shift) - 1))) {
-      const int g = p >> c.page_shift;
-      const int page = g < c.max_pages ? c.tables[(int64_t)b * c.max_pages + g] : -1;
-      if ((unsigned)page >= (unsigned)c.pages) wrong |= KV_BAD_INDEX;
-      else if (c.refs[page] > 1) wrong |= KV_SHARED;
-    }
-  }
-  if (count == 0 && pos & ((1 << c.page_shift) - 1)) {
-    const int page = c.tables[(int64_t)b * c.max_pages + (pos >> c.page_shift)];
+    const int src = s == t ? dst : table[(pos + s) >> c.page_shift];
+    const bool uses = s != t || (t == count - 1 && (p + 1) & inside);
+    if (uses && ((unsigned)dst >= (unsigned)c.pages || (unsigned)src >= (unsigned)c.pages)) return KV_BAD_INDEX;
+    if (uses && c.refs[dst] > 1) return KV_SHARED;
+    from = ((int64_t)src << c.page_shift) + ((pos + s) & inside);
+    to = ((int64_t)dst << c.page_shift) + (p & inside);
+    return 0;
+  };
+  int wrong = 0;
+  for (int t0 = 64; t0 < count && sound; t0 += 64) wrong |= look(t0 + lane);
+  wrong |= look(lane);  // (the first 64 stay looked up)
+  if (sound && count == 0 && pos & inside) {  // ends inside a page that stays
+    const int page = table[pos >> c.page_shift];
     if ((unsigned)page >= (unsigned)c.pages) wrong |= KV_BAD_INDEX;
     else if (c.refs[page] > 1) wrong |= KV_SHARED;
   }
-  bad = __ballot(wrong & KV_BAD_INDEX) ? KV_BAD_INDEX : __ballot(wrong & KV_SHARED) ? KV_SHARED : 0;
-  return !bad;
-}
-
-// Moves the kept tokens: grid (pieces of one token over all layers, keys and
-// values; rows).  A thread moves its 16-byte piece of every token in order,
-// eight at a time: keep is strictly ascending, so the places that a batch
-// writes (up to pos + j + 7) are never sources of a later one (from
-// pos + j + 8 on).  The first workgroup of a row leaves the decision for the
-// next kernel.
-__global__ void __launch_bounds__(256) kv_compact_move_kernel(KvArgs c, const int32_t* pos_, const int32_t* keep_,
-                                                              int max_keep, const int32_t* count_, KvScratch w, int n) {
-  const int b = blockIdx.y;
-  const int pos = pos_[b], count = count_[b];
-  const int32_t* keep = keep_ + (int64_t)b * max_keep;
-  int bad;
-  const bool ok = compactable(c, b, pos, count, keep, max_keep, bad);
+  int bad = __ballot(wrong & KV_BAD_INDEX) ? KV_BAD_INDEX : __ballot(wrong & KV_SHARED) ? KV_SHARED : 0;
+  if (!sound) bad = pos == -1 ? 0 : KV_BAD_INDEX;
+  const bool ok = sound && !bad;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     w.src[b] = ok;
     if (bad) atomicOr(c.status, bad);
   }
+  if (!ok) return;
   const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (!ok || j >= (int64_t)2 * c.layers * n) return;
+  const bool mine = j < (int64_t)2 * c.layers * n;
   const int layer = (int)(j / (2 * n)), r = (int)(j % (2 * n));
-  u4* pool = reinterpret_cast<u4*>(r < n ? c.k : c.v) + (((int64_t)layer * c.pages) << c.page_shift) * n + (r < n ? r : r - n);
-  const int32_t* table = c.tables + (int64_t)b * c.max_pages;
-  const int inside = (1 << c.page_shift) - 1;
-  for (int t0 = 0; t0 < count; t0 += 8) {
-    u4 x[8];
-    const int m = min(8, count - t0);
+  u4* pool = reinterpret_cast<u4*>(r < n ? c.k : c.v) + (((int64_t)(mine ? layer : 0) * c.pages) << c.page_shift) * n +
+             (r < n ? r : r - n);
+  for (int t0 = 0; t0 < count; t0 += 64) {
+    if (t0) look(t0 + lane);
+    const int m = min(64, count - t0);
+    for (int i0 = 0; i0 < m; i0 += 8) {
+      u4 x[8];
+      int64_t f[8], d[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < m && keep[t0 + i] != t0 + i) {
-        const int p = pos + keep[t0 + i], page = table[p >> c.page_shift];
-        if ((unsigned)page < (unsigned)c.pages) x[i] = pool[(((int64_t)page << c.page_shift) + (p & inside)) * n];
+      for (int i = 0; i < 8; ++i) {
+        f[i] = __shfl((long long)from, i0 + i);
+        d[i] = __shfl((long long)to, i0 + i);
+        if (mine && i0 + i < m && f[i] != d[i]) x[i] = pool[f[i] * n];
       }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < m && keep[t0 + i] != t0 + i) {
-        const int p = pos + t0 + i, page = table[p >> c.page_shift];
-        if ((unsigned)page < (unsigned)c.pages) pool[(((int64_t)page << c.page_shift) + (p & inside)) * n] = x[i];
-      }
+      for (int i = 0; i < 8; ++i)
+        if (mine && i0 + i < m && f[i] != d[i]) pool[d[i] * n] = x[i];
+    }
   }
 }
 
@@ -412,9 +512,12 @@ hipError_t launch_kv_write(const KvWriteArgs& a, hipStream_t s) {
 hipError_t launch_kv_fork(const KvArgs& c, const int32_t* parents, const KvArgs& out, const KvScratch& w,
                           hipStream_t s) {
   const int rows = c.rows > out.rows ? c.rows : out.rows;
-  hipLaunchKernelGGL(kv_fork_rows_kernel, dim3((unsigned)rows), dim3(256), 0, s, c, parents, out, w);
+  // (up to 16 entries a thread)
+  const bool small = rows <= FORK_ROWS && (int64_t)rows * c.max_pages <= 16 * SCAN;
+  if (small) hipLaunchKernelGGL(kv_fork_small_kernel, dim3(1), dim3(SCAN), 0, s, c, parents, out, w);
+  else hipLaunchKernelGGL(kv_fork_rows_kernel, dim3((unsigned)rows), dim3(256), 0, s, c, parents, out, w);
   if (out.rows) {
-    hipLaunchKernelGGL(kv_fork_pages_kernel, dim3(1), dim3(SCAN), 0, s, c, out, w);
+    if (!small) hipLaunchKernelGGL(kv_fork_pages_kernel, dim3(1), dim3(SCAN), 0, s, c, out, w);
     hipLaunchKernelGGL(kv_fork_copy_kernel, dim3(piece_blocks(c), (unsigned)out.rows), dim3(256), 0, s, c, out, w,
                        pieces(c));
   }

@@ -81,7 +81,8 @@ class Both:
 
 
 @pytest.mark.parametrize("page,kv,D,rows,dtype", [(16, 2, 64, 5, "float16"), (32, 1, 128, 9, "float16"),
-                                                  (128, 3, 64, 3, "float16"), (16, 8, 128, 70, "float16")])
+                                                  (128, 3, 64, 3, "float16"), (16, 8, 128, 70, "float16"),
+                                                  (16, 1, 64, 300, "float16")])
 def test_random_life(page, kv, D, rows, dtype):
     """Appends, trees with their compaction and forks in random order, from an empty pool to a full one."""
     t = torch()
@@ -179,6 +180,20 @@ def test_reserve_many_rows_and_bad_counts():
     before = c.lens.tolist()
     pos = q_.kv_reserve(c, cu)
     assert pos[4] == -1 and c.lens[4] == before[4] and int(c.status) & q_.KV_BAD_INDEX
+
+
+def test_keeping_more_tokens_than_a_wave_has_lanes():
+    """150 of 200 drafted tokens, and all of them; larger tables than a fork takes in one workgroup."""
+    t = torch()
+    say("kv long keeps")
+    rng = np.random.default_rng(1)
+    x = Both(2, 80, 16, 1, 64, 3, 6000, t.float16)
+    x.append([37, 0, 100])
+    pos = x.append([200, 200, 130])
+    keep = [sorted(rng.choice(200, 150, replace=False).tolist()), list(range(150)), [0, 5] + list(range(60, 130)) + [0] * 78]
+    x.compact(pos, keep, [150, 150, 72])
+    x.fork([2, 0, 0])
+    x.append([5, 30, 1])
 
 
 def test_more_rows_from_fewer_and_back():
