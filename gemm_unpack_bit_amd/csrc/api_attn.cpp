@@ -4,8 +4,11 @@
 
 #include <hip/hip_runtime.h>
 
+#include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdint>
+#include <random>
 
 #include "attn.hpp"
 #include "kernels.hpp"
@@ -59,15 +62,29 @@ int check_counts(int tokens, int rows, int heads, int heads_kv) {
   return QGEMV_OK;
 }
 
-// Whether the attention kernels' launches stay under 2^32 threads: a workgroup
-// per query token and head joins the narrow kernel's parts, one per tile and
-// key head runs the wide prompt kernel (8 of them join its parts, where there
-// are so few tiles that it splits them).
+// Whether the wide kernels' launches stay under 2^32 threads: up to 8 workgroups
+// of 256 threads per tile and key head.
 bool launchable(int tokens, int rows, int heads, int heads_kv) {
-  if (!tokens || !rows) return true;
   const int group = heads / heads_kv;
-  if (qg::narrow_tiles(tokens, rows, group)) return (int64_t)tokens * heads < 1 << 24;
+  if (!tokens || !rows || qg::narrow_tiles(tokens, rows, group)) return true;
   return (int64_t)qg::prompt_tiles(tokens, rows, group) * heads_kv < 1 << 21 && heads_kv < 65536;
+}
+
+size_t narrow_bytes(int rows, int heads_kv, int rt, int head_dim) {
+  const size_t n = (size_t)qg::narrow_workgroups(rows, heads_kv);
+  return qg::partial_bytes(2 * n, 16 * rt, head_dim) + 16 * n;  // (and two words per share for the tickets)
+}
+
+// A number of 48 bits for the tickets of one call's parts: counted up from a
+// random start, so that what an uninitialized workspace holds is not taken for
+// one; never 0.
+uint64_t next_nonce() {
+  static std::atomic<uint64_t> count{[] {
+    std::random_device r;
+    return (uint64_t)r() << 32 ^ r() ^ (uint64_t)std::chrono::steady_clock::now().time_since_epoch().count();
+  }()};
+  for (;;)
+    if (const uint64_t n = count.fetch_add(1) & 0xFFFFFFFFFFFFu) return n;
 }
 
 int check_scale(float scale) { return std::isfinite(scale) && scale >= 0.f ? QGEMV_OK : QGEMV_ERR_VALUE; }
@@ -141,7 +158,7 @@ size_t qgemv_attn_prompt_workspace_bytes(int tokens, int tokens_k, int batch, in
   if (check_counts(tokens, batch, heads, heads_kv) || tokens_k < 0 || !tokens || !batch) return 0;
   if (head_dim != 64 && head_dim != 128) return 0;
   const int group = heads / heads_kv, rt = qg::narrow_tiles(tokens, batch, group);
-  if (rt) return qg::partial_bytes(2 * qg::NARROW_WORKGROUPS, 16 * rt, head_dim);
+  if (rt) return narrow_bytes(batch, heads_kv, rt, head_dim);
   const int splits = qg::prompt_splits(tokens, tokens_k, batch, heads_kv, group, head_dim);
   if (splits == 1) return 0;
   return qg::partial_bytes((size_t)qg::prompt_tiles(tokens, batch, group) * heads_kv * splits, qg::WIDE_BM, head_dim);
@@ -191,6 +208,7 @@ int qgemv_attn_prompt(int dtype, int causal, int tokens, int tokens_k, int batch
   a.cu_k = cu_k;
   a.tokens_k = tokens_k;
   a.ws = reinterpret_cast<float*>(ws);
+  a.nonce = next_nonce();
   const int rt = qg::narrow_tiles(tokens, batch, a.group);
   return qg::hip_status(rt ? qg::launch_attn_narrow(a, rt, stream_of(stream)) : qg::launch_attn_wide(a, stream_of(stream)));
 }
@@ -199,7 +217,7 @@ size_t qgemv_attn_tree_workspace_bytes(int tokens, int rows, int heads, int head
   if (check_counts(tokens, rows, heads, heads_kv) || !tokens || !rows) return 0;
   if (head_dim != 64 && head_dim != 128) return 0;
   const int rt = qg::narrow_tiles(tokens, rows, heads / heads_kv);
-  if (rt) return qg::partial_bytes(2 * qg::NARROW_WORKGROUPS, 16 * rt, head_dim);
+  if (rt) return narrow_bytes(rows, heads_kv, rt, head_dim);
   return qg::partial_bytes(2 * (size_t)qg::wide_workgroups(head_dim), qg::WIDE_BM, head_dim);
 }
 
@@ -252,6 +270,7 @@ int qgemv_attn_tree(int dtype, const qgemv_kv_cache* c, int layer, int tokens, i
   a.mask = mask;
   a.mask_words = mask_words;
   a.ws = reinterpret_cast<float*>(ws);
+  a.nonce = next_nonce();
   const int rt = qg::narrow_tiles(tokens, a.rows, a.group);
   return qg::hip_status(rt ? qg::launch_attn_narrow(a, rt, stream_of(stream)) : qg::launch_attn_wide(a, stream_of(stream)));
 }

@@ -60,6 +60,7 @@ struct AttnArgs {
   const uint64_t* mask;
   int mask_words;
   float* ws;
+  uint64_t nonce;  // of the call (attn_narrow.hip, last_part): 48 bits, not 0
 };
 
 // The choice of kernel, its split of the keys, and so the workspace, depend on
@@ -67,7 +68,9 @@ struct AttnArgs {
 // Waves per SIMD that the kernels' registers allow, and the workgroups (of one
 // wave per SIMD) that then fill the 256 compute units: the split of a tree's
 // keys is over that many.
-constexpr int NARROW_WORKGROUPS = 512;
+// (The narrow kernel's parts of an item are joined by one workgroup: at most
+// 256 of them.)
+inline int narrow_workgroups(int rows, int heads_kv) { return (int64_t)rows * heads_kv < 2 ? 256 : 512; }
 constexpr int wide_waves(int head_dim) { return head_dim == 64 ? 3 : 2; }
 constexpr int wide_workgroups(int head_dim) { return 256 * wide_waves(head_dim); }
 constexpr int WIDE_BM = 128;

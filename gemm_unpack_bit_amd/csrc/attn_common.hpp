@@ -181,76 +181,44 @@ struct Partials {
   __device__ __forceinline__ float* o_at(int64_t slot, int row) const { return o + (slot * BM + row) * D; }
 };
 
-// Joins partial results of one query row: 16 threads hold the row's columns
-// (DL each), PL lanes of parts take the parts i = pl, pl + PL, ... and are then
-// added in LDS in a fixed order:
-//     o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
-// Every thread loads its parts' statistics and sums without waiting for
-// anything but their slots.  All threads of the workgroup take part; `tid` is
-// the thread's number among the row's 16 PL threads, with the column fastest.
-template <int D, int PL>
-struct JoinBuffer {
-  float o[PL][D], m[PL], l[PL];
-};
-template <typename E, int PL, int BM, int D, typename F>
-__device__ __forceinline__ void join_row(const Partials<BM, D>& p, int row, int parts, F&& slot, uint16_t* out, bool live,
-                                         int tid, JoinBuffer<D, PL>* buf) {
+// Joins partial results of one query row in the order of their slots, four
+// parts' loads at a time: o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
+// 16 threads (`thread` of them) hold the row's columns, D / 16 each.
+template <typename E, int BM, int D, typename F>
+__device__ __forceinline__ void join_row(const Partials<BM, D>& p, int row, int parts, F&& slot, uint16_t* out, int thread) {
   constexpr int DL = D / 16;
   typedef float fl __attribute__((ext_vector_type(DL)));
-  const int pl = tid >> 4, col = DL * (tid & 15);
+  const int col = DL * thread;
   float m = NEG_INF, l = 0.f;
   fl acc;
 #pragma unroll
   for (int e = 0; e < DL; ++e) acc[e] = 0.f;
-  if (live) {
-    for (int i = pl; i < parts; i += 4 * PL) {
-      float mi[4], li[4];
-      fl oi[4];
+  for (int i = 0; i < parts; i += 4) {
+    float mi[4], li[4];
+    fl oi[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int at = i + x * PL;
-        const int64_t s = slot(at < parts ? at : i);
-        const float* ml = p.ml_at(s, row);
-        mi[x] = at < parts ? ml[0] : NEG_INF;
-        li[x] = at < parts ? ml[1] : 0.f;
-        oi[x] = *reinterpret_cast<const fl*>(p.o_at(s, row) + col);
-      }
-      float mn = m;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) mn = fmaxf(mn, mi[x]);
-      const float base = mn == NEG_INF ? 0.f : mn, w = exp2_(m - base);
-      l *= w;
-      acc *= w;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float wx = exp2_(mi[x] - base);
-        l += wx * li[x];
-#pragma unroll
-        for (int e = 0; e < DL; ++e) acc[e] += li[x] == 0.f ? 0.f : wx * oi[x][e];  // (no weights: o may be anything)
-      }
-      m = mn;
+    for (int x = 0; x < 4; ++x) {
+      const int64_t s = slot(i + x < parts ? i + x : i);
+      const float* ml = p.ml_at(s, row);
+      mi[x] = i + x < parts ? ml[0] : NEG_INF;
+      li[x] = i + x < parts ? ml[1] : 0.f;
+      oi[x] = *reinterpret_cast<const fl*>(p.o_at(s, row) + col);
     }
-  }
-  if constexpr (PL > 1) {
-    *reinterpret_cast<fl*>(&buf->o[pl][col]) = acc;
-    if ((tid & 15) == 0) buf->m[pl] = m, buf->l[pl] = l;
-    __syncthreads();
-    if (pl > 0) return;
-    float M = NEG_INF;
+    float mn = m;
 #pragma unroll
-    for (int x = 0; x < PL; ++x) M = fmaxf(M, buf->m[x]);
-    const float base = M == NEG_INF ? 0.f : M;
-    l = 0.f;
+    for (int x = 0; x < 4; ++x) mn = fmaxf(mn, mi[x]);
+    const float base = mn == NEG_INF ? 0.f : mn, w = exp2_(m - base);
+    l *= w;
+    acc *= w;
 #pragma unroll
-    for (int e = 0; e < DL; ++e) acc[e] = 0.f;
+    for (int x = 0; x < 4; ++x) {
+      const float wx = exp2_(mi[x] - base);
+      l += wx * li[x];
 #pragma unroll
-    for (int x = 0; x < PL; ++x) {
-      const float w = exp2_(buf->m[x] - base);
-      l += w * buf->l[x];
-      acc += w * *reinterpret_cast<const fl*>(&buf->o[x][col]);
+      for (int e = 0; e < DL; ++e) acc[e] += li[x] == 0.f ? 0.f : wx * oi[x][e];  // (no weights: o may be anything)
     }
+    m = mn;
   }
-  if (!live) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   typedef uint32_t vw __attribute__((ext_vector_type(DL / 2)));
   vw y;
@@ -277,13 +245,12 @@ __device__ __forceinline__ uint32_t scan24(uint32_t v) {
 // t * group + g: query token t, head g of the key head's group) of one row and
 // key head; its keys are cut into units of KB.  The units of all items, in the
 // order row, key head, tile, unit, are shared out evenly: workgroup c takes
-// units [c * per, (c + 1) * per), per = max(least, ceil(total / workgroups)).
+// units [c * per, (c + 1) * per), per = ceil(total / workgroups).
 // So a long row is worked on by many workgroups and short ones share one,
 // whatever the mix, and no workgroup waits for another.  An item that lies in
 // one workgroup is finished there; of the others every workgroup leaves a
 // partial result (the part that starts with the workgroup's share in slot
-// 2 c, one that starts later in slot 2 c + 1), which a second kernel joins in
-// key order.
+// 2 c, one that starts later in slot 2 c + 1), and they are joined in key order.
 //
 // Neighbouring shares read the same keys (the tiles of a row and key head come
 // one after the other) at about the same time, so they belong on one XCD, where
@@ -330,15 +297,14 @@ struct Walk {
     incl = ((int64_t)scan24((uint32_t)(cost >> 24)) << 24) + scan24((uint32_t)cost & 0xFFFFFF);
     all = lane64(incl, 63);
   }
-  __device__ __forceinline__ void init(const AttnArgs& a, int workgroups, int least) {
+  __device__ __forceinline__ void init(const AttnArgs& a, int workgroups) {
     hold(a, 0, 0);
     total = all;
     for (int first = 64; first < a.rows; first += 64) {
       hold(a, first, total);
       total += all;
     }
-    const int64_t even = (total + workgroups - 1) / workgroups;
-    per = even > least ? even : least;
+    per = total ? (total + workgroups - 1) / workgroups : 1;
   }
   __device__ __forceinline__ int shares() const { return (int)((total + per - 1) / per); }
   __device__ __forceinline__ Row row(int lane) const {
@@ -400,10 +366,10 @@ struct Walk {
     bool late;
     __device__ __forceinline__ int64_t slot(int i) const { return 2 * (c0 + i) + (i == 0 && late); }
   };
-  __device__ __forceinline__ Parts parts(int64_t u0, const Row& r) const {
+  __device__ __forceinline__ Parts parts(int64_t u0, int of) const {
     Parts p;
     p.c0 = u0 / per;
-    p.n = (int)((u0 + units(r) - 1) / per - p.c0) + 1;
+    p.n = (int)((u0 + of - 1) / per - p.c0) + 1;
     p.late = u0 != p.c0 * per;
     return p;
   }

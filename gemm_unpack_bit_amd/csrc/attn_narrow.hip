@@ -34,9 +34,87 @@ namespace {
 constexpr int KB = 128;      // keys of a unit: 32 per wave
 constexpr int WAVES = 4;
 
+// Partial results in the workspace: [slots][BM] (max, sum); per slot BM * D
+// sums in 16-byte pieces, so that a wave's store or load of a piece per lane is
+// 1 KB; two words per share for the tickets.
+//
+// The workgroups that write and read a part sit on different XCDs, whose caches
+// do not see each other.  Fences would write back and drop whole caches (a
+// decode batch of 144k keys took 177 us instead of 108); instead every access
+// to a part goes past them (device scope, like the atomics on the tickets).
+// Joining here rather than in a second kernel saves that kernel's launch and
+// its look at all rows (8 us of 116 on the same batch).
+constexpr int CPOL_DEVICE = 16;
+template <int BM, int D>
+struct Parts {
+  rsrc_t r;
+  uint32_t sums;  // byte offset of the sums
+  unsigned long long* tickets;
+  __device__ __forceinline__ Parts(float* ws, int64_t slots)
+      : r(make_rsrc(ws, (uint32_t)(slots * BM * (D + 2) * 4))),
+        sums((uint32_t)(slots * BM * 8)),
+        tickets(reinterpret_cast<unsigned long long*>(ws + slots * BM * (D + 2))) {}
+  __device__ __forceinline__ void put_ml(int64_t slot, int row, float m, float l) const {
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, f2v{m, l}), r, (uint32_t)((slot * BM + row) * 8), 0,
+                                          CPOL_DEVICE);
+  }
+  __device__ __forceinline__ f2v ml(int64_t slot, int row) const {
+    return __builtin_bit_cast(
+        f2v, __builtin_amdgcn_raw_buffer_load_b64(r, (uint32_t)((slot * BM + row) * 8), 0, CPOL_DEVICE));
+  }
+  // piece x of thread t (of 16) of a row: four columns
+  __device__ __forceinline__ uint32_t at(int64_t slot, int row, int x, int t) const {
+    return sums + (uint32_t)(slot * (BM * D / 4) + ((row >> 4) * (D / 64) + x) * 256 + (row & 15) * 16 + t) * 16;
+  }
+  __device__ __forceinline__ void put(int64_t slot, int row, int x, int t, f4 v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v), r, at(slot, row, x, t), 0, CPOL_DEVICE);
+  }
+  __device__ __forceinline__ f4 get(int64_t slot, int row, int x, int t) const {
+    return __builtin_bit_cast(f4, bload16<CPOL_DEVICE>(r, at(slot, row, x, t)));
+  }
+};
+
+// Whether this workgroup's part of an item is the last of `parts` to be
+// written; the one for which it is joins them all, in key order, so the result
+// does not depend on which one that is, and no workgroup waits for another.
+// Called by the whole workgroup after its part's stores.
+//
+// The first word of a ticket is CLEAN plus the number of parts written so far,
+// and CLEAN again after the last.  The workspace comes without initial contents:
+// where the word is nothing of the kind (a workspace's first call), all parts of
+// the item see that, and count in the second word instead, under the call's
+// nonce (48 bits, another one for every call); what does not carry the nonce
+// there counts as 0.  (A stray value is taken for a count once in 2^48.)
+constexpr unsigned long long CLEAN = 0x9C3B5E2D71A60000ull;
+__device__ __forceinline__ bool last_part(unsigned long long* ticket, uint64_t nonce, int parts, uint32_t* shared) {
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0: this wave's stores have reached the device's memory
+  __syncthreads();                     // ... and every wave's
+  if (threadIdx.x == 0) {
+    bool last;
+    unsigned long long old = __hip_atomic_fetch_add(ticket, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (old - CLEAN < 0xFFFF) {
+      last = (int)(old - CLEAN) == parts - 1;
+    } else {
+      unsigned long long now;
+      old = __hip_atomic_load(ticket + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      do {
+        const int n = old >> 16 == nonce ? (int)(old & 0xFFFF) + 1 : 1;
+        last = n == parts;
+        now = nonce << 16 | (unsigned)n;
+      } while (!__hip_atomic_compare_exchange_strong(ticket + 1, &old, now, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
+                                                     __HIP_MEMORY_SCOPE_AGENT));
+      if (last) __hip_atomic_store(ticket + 1, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (last) __hip_atomic_store(ticket, CLEAN, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *shared = last;
+  }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(*shared) != 0;
+}
+
 // RT: 16-row tiles of query rows held by a wave (BM = 16 RT rows)
 template <typename E, int D, int RT, bool PAGED>
-__global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, int workgroups, int least) {
+__global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, int workgroups) {
   constexpr int BM = 16 * RT;
   constexpr int KS = D / 32;  // matrix steps along head_dim
   constexpr int DL = D / 16;  // output columns of a lane
@@ -46,16 +124,17 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
   using U = Walk<BM, KB, PAGED>;
   __shared__ __attribute__((aligned(16))) float o_s[WAVES][BM][PITCH];
   __shared__ float m_s[WAVES][BM], l_s[WAVES][BM];
+  __shared__ uint32_t last_s;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n16 = lane & 15, quarter = lane >> 4;
   U walk;
-  walk.init(a, workgroups, least);
+  walk.init(a, workgroups);
   const int c = share_of(blockIdx.x, walk.shares());
   int64_t u = c * walk.per;
   const int64_t u_end = u + walk.per < walk.total ? u + walk.per : walk.total;
   const int64_t u_begin = u;
-  const Partials<BM, D> parts(a.ws, 2 * (int64_t)workgroups);
+  const Parts<BM, D> parts(a.ws, 2 * (int64_t)workgroups);
 
   while (u < u_end) {
     const typename U::Piece piece = walk.seek(a, u, u_end);
@@ -320,14 +399,89 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
           *reinterpret_cast<vw*>(a.o + (int64_t)(r.q0 + t) * a.o_token + (int64_t)(h * a.group + g) * a.o_head + col) = y;
         }
       } else {
-        float* po = parts.o_at(slot, row) + col;
+        if (qr < rows) {
 #pragma unroll
-        for (int j = 0; j < DL; j += 4)
-          *reinterpret_cast<f4*>(po + j) = f4{acc[j], acc[j + 1], acc[j + 2], acc[j + 3]};
-        if ((threadIdx.x & 15) == 0) {
-          float* ml = parts.ml_at(slot, row);
-          ml[0] = M;
-          ml[1] = sum;
+          for (int j = 0; j < DL; j += 4)
+            parts.put(slot, row, j / 4, threadIdx.x & 15, f4{acc[j], acc[j + 1], acc[j + 2], acc[j + 3]});
+          if ((threadIdx.x & 15) == 0) parts.put_ml(slot, row, M, sum);
+        }
+      }
+    }
+    if (!whole) {
+      // (at most one item goes on from a share into the next: the share's number
+      // is its ticket's)
+      const typename U::Parts p = walk.parts(u - ku, piece.of);
+      if (last_part(parts.tickets + 2 * p.c0, a.nonce, p.n, &last_s)) {
+        // 16 threads hold a row's columns; with few rows, several such rows of
+        // threads take every PL-th part of one and are added up in LDS
+        const int live = min(BM, rows - tile * BM);
+        const int lg = live <= 1 ? 0 : live <= 2 ? 1 : live <= 4 ? 2 : live <= 8 ? 3 : 4;  // log2 of rows at a time
+        const int RP = 1 << lg, PL = 16 >> lg;
+        const int rl = threadIdx.x >> 4, pl = rl >> lg, col = DL * (threadIdx.x & 15);
+        typedef float fl __attribute__((ext_vector_type(DL)));
+        for (int row0 = 0; row0 < live; row0 += RP) {
+          const int row = row0 + (rl & (RP - 1));
+          float mj = NEG_INF, lj = 0.f;
+          fl acc;
+#pragma unroll
+          for (int j = 0; j < DL; ++j) acc[j] = 0.f;
+          if (row < live)
+            for (int i = pl; i < p.n; i += 4 * PL) {
+              float mi[4], li[4];
+              fl oi[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const int64_t at = p.slot(i + x * PL < p.n ? i + x * PL : i);
+                const f2v ml = parts.ml(at, row);
+                mi[x] = i + x * PL < p.n ? ml[0] : NEG_INF;
+                li[x] = i + x * PL < p.n ? ml[1] : 0.f;
+#pragma unroll
+                for (int j = 0; j < DL; j += 4) {
+                  const f4 y = parts.get(at, row, j / 4, threadIdx.x & 15);
+                  oi[x][j] = y[0], oi[x][j + 1] = y[1], oi[x][j + 2] = y[2], oi[x][j + 3] = y[3];
+                }
+              }
+              float mn = mj;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) mn = fmaxf(mn, mi[x]);
+              const float base = mn == NEG_INF ? 0.f : mn, w = exp2_(mj - base);
+              lj *= w;
+              acc *= w;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float wx = exp2_(mi[x] - base);
+                lj += wx * li[x];
+#pragma unroll
+                for (int j = 0; j < DL; ++j) acc[j] += i + x * PL < p.n ? wx * oi[x][j] : 0.f;
+              }
+              mj = mn;
+            }
+          float* sums = &o_s[0][0][0];
+          float* ms = &m_s[0][0];  // 16 of each: WAVES * BM are at least 64
+          float* ls = &l_s[0][0];
+          *reinterpret_cast<fl*>(sums + rl * D + col) = acc;
+          if (col == 0) ms[rl] = mj, ls[rl] = lj;
+          __syncthreads();
+          if (pl == 0 && row < live) {
+            float M = NEG_INF;
+            for (int x = 0; x < PL; ++x) M = fmaxf(M, ms[rl + x * RP]);
+            const float base = M == NEG_INF ? 0.f : M;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < DL; ++j) acc[j] = 0.f;
+            for (int x = 0; x < PL; ++x) {
+              const float w = exp2_(ms[rl + x * RP] - base);
+              sum += w * ls[rl + x * RP];
+              acc += w * *reinterpret_cast<const fl*>(sums + (rl + x * RP) * D + col);
+            }
+            const int qr = tile * BM + row, t = qr / a.group, g = qr - t * a.group;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            vw y;
+#pragma unroll
+            for (int j = 0; j < DW; ++j) y[j] = E::pack(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+            *reinterpret_cast<vw*>(a.o + (int64_t)(r.q0 + t) * a.o_token + (int64_t)(h * a.group + g) * a.o_head + col) = y;
+          }
+          __syncthreads();
         }
       }
     }
@@ -336,36 +490,10 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
   }
 }
 
-// One workgroup per query token and head: joins the parts of an item that lay
-// in several workgroups, 16 parts at a time.
-template <typename E, int D, int RT, bool PAGED>
-__global__ void __launch_bounds__(256) attn_narrow_join_kernel(AttnArgs a, int workgroups, int least) {
-  constexpr int BM = 16 * RT, PL = 16;
-  using U = Walk<BM, KB, PAGED>;
-  __shared__ __attribute__((aligned(16))) JoinBuffer<D, PL> buf;
-  U walk;
-  walk.init(a, workgroups, least);
-  const int token = blockIdx.x / a.heads, head = blockIdx.x - token * a.heads, h = head / a.group;
-  const int b = walk.find(a, token, [](const Row& r, int) { return r.q0; }, [&](int i) { return a.cu[i]; });
-  Row r;
-  int64_t first;
-  walk.seek_row(a, b, r, first);
-  const int t = token - r.q0;
-  if (t < 0 || t >= r.n) return;
-  const int qr = t * a.group + head - h * a.group, tile = qr / BM;
-  const typename U::Parts p = walk.parts(first + (int64_t)(h * U::tiles(a, r) + tile) * U::units(r), r);
-  if (p.n == 1) return;
-  join_row<E, PL>(Partials<BM, D>(a.ws, 2 * (int64_t)workgroups), qr - tile * BM, p.n, [&](int i) { return p.slot(i); },
-                  a.o + (int64_t)token * a.o_token + (int64_t)head * a.o_head, true, threadIdx.x, &buf);
-}
-
 template <typename E, int D, int RT, bool PAGED>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
-  const int least = 1;
-  hipLaunchKernelGGL((attn_narrow_kernel<E, D, RT, PAGED>), dim3(NARROW_WORKGROUPS), dim3(64 * WAVES), 0, s, a,
-                     NARROW_WORKGROUPS, least);
-  hipLaunchKernelGGL((attn_narrow_join_kernel<E, D, RT, PAGED>), dim3((unsigned)(a.tokens * a.heads)), dim3(256), 0, s, a,
-                     NARROW_WORKGROUPS, least);
+  const int workgroups = narrow_workgroups(a.rows, a.heads_kv);
+  hipLaunchKernelGGL((attn_narrow_kernel<E, D, RT, PAGED>), dim3(workgroups), dim3(64 * WAVES), 0, s, a, workgroups);
   return hipGetLastError();
 }
 

@@ -452,15 +452,15 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(AttnArgs a, int s
   const int row = 16 * (blockIdx.x % (BM / 16)) + (threadIdx.x >> 4), qr = in * BM + row;
   const int t = qr / a.group, head = h * a.group + qr - t * a.group;
   const Partials<BM, D> parts(a.ws, (int64_t)(gridDim.x / (BM / 16)) * a.heads_kv * splits);
-  join_row<E, 1>(parts, row, splits, [&](int i) { return ((int64_t)tile * a.heads_kv + h) * splits + i; },
-                 a.o + (int64_t)(r.q0 + t) * a.o_token + (int64_t)head * a.o_head, t < r.n, threadIdx.x & 15,
-                 (JoinBuffer<D, 1>*)nullptr);
+  if (t >= r.n) return;
+  join_row<E>(parts, row, splits, [&](int i) { return ((int64_t)tile * a.heads_kv + h) * splits + i; },
+                 a.o + (int64_t)(r.q0 + t) * a.o_token + (int64_t)head * a.o_head, threadIdx.x & 15);
 }
 
 // Trees over the paged cache: the units of all items shared out evenly
 // (Units), so rows of very different lengths keep every workgroup busy.
 template <typename E, int D>
-__global__ void __launch_bounds__(64 * WAVES, wide_waves(D)) attn_tree_kernel(AttnArgs a, int workgroups, int least) {
+__global__ void __launch_bounds__(64 * WAVES, wide_waves(D)) attn_tree_kernel(AttnArgs a, int workgroups) {
   using U = Walk<BM, KB, true>;
   __shared__ Buffers<D> k0, k1, v0, v1;
   __shared__ uint32_t flag[2];
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(64 * WAVES, wide_waves(D)) attn_tree_kernel(At
   // so that they occupy no registers during one)
   for (int64_t done = 0;;) {
     U walk;
-    walk.init(a, workgroups, least);
+    walk.init(a, workgroups);
     const int c = share_of(blockIdx.x, walk.shares());
     const int64_t u_begin = c * walk.per, u = u_begin + done;
     const int64_t u_end = u_begin + walk.per < walk.total ? u_begin + walk.per : walk.total;
@@ -484,10 +484,10 @@ __global__ void __launch_bounds__(64 * WAVES, wide_waves(D)) attn_tree_kernel(At
 // One workgroup per 16 query rows of a tile and key head: joins the parts of
 // an item that lay in several workgroups.
 template <typename E, int D>
-__global__ void __launch_bounds__(256) attn_tree_join_kernel(AttnArgs a, int workgroups, int least) {
+__global__ void __launch_bounds__(256) attn_tree_join_kernel(AttnArgs a, int workgroups) {
   using U = Walk<BM, KB, true>;
   U walk;
-  walk.init(a, workgroups, least);
+  walk.init(a, workgroups);
   const int tile = blockIdx.x / (BM / 16), h = blockIdx.y;
   auto first_at = [&](int q0, int b) { return (int)((int64_t)q0 * a.group / BM) + b; };
   const int b = walk.find(a, tile, [&](const Row& r, int i) { return first_at(r.q0, i); },
@@ -497,13 +497,13 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(AttnArgs a, int wor
   walk.seek_row(a, b, r, first);
   const int in = tile - first_at(r.q0, b);
   if (in < 0 || in >= U::tiles(a, r)) return;
-  const typename U::Parts p = walk.parts(first + (int64_t)(h * U::tiles(a, r) + in) * U::units(r), r);
+  const typename U::Parts p = walk.parts(first + (int64_t)(h * U::tiles(a, r) + in) * U::units(r), U::units(r));
   if (p.n == 1) return;
   const int row = 16 * (blockIdx.x % (BM / 16)) + (threadIdx.x >> 4), qr = in * BM + row;
   const int t = qr / a.group, head = h * a.group + qr - t * a.group;
-  join_row<E, 1>(Partials<BM, D>(a.ws, 2 * (int64_t)workgroups), row, p.n, [&](int i) { return p.slot(i); },
-                 a.o + (int64_t)(r.q0 + t) * a.o_token + (int64_t)head * a.o_head, t < r.n, threadIdx.x & 15,
-                 (JoinBuffer<D, 1>*)nullptr);
+  if (t >= r.n) return;
+  join_row<E>(Partials<BM, D>(a.ws, 2 * (int64_t)workgroups), row, p.n, [&](int i) { return p.slot(i); },
+                 a.o + (int64_t)(r.q0 + t) * a.o_token + (int64_t)head * a.o_head, threadIdx.x & 15);
 }
 
 template <typename E, int D>
@@ -520,10 +520,10 @@ hipError_t prompt(const AttnArgs& a, hipStream_t s) {
 
 template <typename E, int D>
 hipError_t tree(const AttnArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((attn_tree_kernel<E, D>), dim3(wide_workgroups(D)), dim3(64 * WAVES), 0, s, a, wide_workgroups(D), 1);
+  hipLaunchKernelGGL((attn_tree_kernel<E, D>), dim3(wide_workgroups(D)), dim3(64 * WAVES), 0, s, a, wide_workgroups(D));
   hipLaunchKernelGGL((attn_tree_join_kernel<E, D>),
                      dim3((unsigned)prompt_tiles(a.tokens, a.rows, a.group) * (BM / 16), (unsigned)a.heads_kv), dim3(256), 0,
-                     s, a, wide_workgroups(D), 1);
+                     s, a, wide_workgroups(D));
   return hipGetLastError();
 }
 

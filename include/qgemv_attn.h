@@ -68,9 +68,9 @@ typedef struct {
  *                      that is 0.
  *
  * Checks, in order: null, dtype / head_dim (UNSUPPORTED), shape (counts not
- * negative, heads % heads_kv, strides, k's and v's token strides < 2^26;
- * tokens * heads < 2^24, or where sequences have more than 32 query rows per
- * key head on average, tokens * heads / 128 + batch * heads_kv < 2^21), alignment,
+ * negative, heads % heads_kv, tokens * heads < 2^31 and about
+ * tokens * heads / 128 + batch * heads_kv < 2^21, strides, k's and v's token
+ * strides < 2^26), scale, alignment,
  * o overlapping an input (VALUE), workspace.  o's elements must not overlap
  * each other (SHAPE).  tokens or batch of 0 does nothing.
  * ------------------------------------------------------------------------ */

@@ -343,6 +343,32 @@ def test_tree_many_rows():
     _check_prompt(out, q, q[:, :2], q[:, 2:], ns, ns, True, 64 ** -0.5, "f16", "many prompts")
 
 
+@pytest.mark.parametrize("heads,kv,n", [(8, 2, 1), (32, 1, 1), (8, 2, 40)])
+def test_what_a_workspace_holds_does_not_matter(heads, kv, n):
+    """Parts are joined alike whatever the workspace held: anything on its first use, other shapes' parts later."""
+    t = torch()
+    say("attn_tree workspace", heads, kv, n)
+    dt, pos = _dt("f16"), [9000, 4, 700]
+    cache, tables = _cache(21, dt, [p + n for p in pos], 32, kv, 128)
+    q, p = _rand(_gen(21), 3 * n, heads, 128, dtype=dt), t.tensor(pos, dtype=t.int32, device="cuda")
+    need = q_.attn_tree_workspace_bytes(3 * n, 3, heads, kv, 128)
+    ws = t.zeros(need, dtype=t.uint8, device="cuda")
+    first = q_.attn_tree(q, cache, 0, _cu([n] * 3), p, ws=ws)
+    _check_tree(first, q, cache, 0, tables, [n] * 3, pos, None, 128 ** -0.5, "f16", "workspace", most=4)
+    small = _cache(22, dt, [300], 16, kv, 128)[0]
+    for fill in (0, 1, 255, "random", "small", "other"):
+        if fill == "random":
+            ws = t.randint(0, 256, (need,), dtype=t.uint8, device="cuda")
+        elif fill == "small":
+            ws = t.randint(0, 9, (need // 8,), dtype=t.int64, device="cuda").view(t.uint8)
+        elif fill == "other":
+            q_.attn_tree(q[:1], small, 0, _cu([1]), p[2:] - 500, ws=ws)
+        else:
+            ws.fill_(fill)
+        for _ in range(3):
+            assert t.equal(first, q_.attn_tree(q, cache, 0, _cu([n] * 3), p, ws=ws)), fill
+
+
 def test_offsets_past_32_bits():
     """A pool of more than 2^32 elements, and packed keys more than 2^31 elements apart."""
     t = torch()
