@@ -63,11 +63,11 @@ int check_counts(int tokens, int rows, int heads, int heads_kv) {
 }
 
 // Whether the wide kernels' launches stay under 2^32 threads: up to 8 workgroups
-// of 256 threads per tile and key head.
+// of 256 threads per 128 query rows and key head.
 bool launchable(int tokens, int rows, int heads, int heads_kv) {
   const int group = heads / heads_kv;
   if (!tokens || !rows || qg::narrow_tiles(tokens, rows, group)) return true;
-  return (int64_t)qg::prompt_tiles(tokens, rows, group) * heads_kv < 1 << 21 && heads_kv < 65536;
+  return (int64_t)qg::wide_tiles(tokens, rows, group, 4) * heads_kv < 1 << 21 && heads_kv < 65536;
 }
 
 size_t narrow_bytes(int rows, int heads_kv, int rt, int head_dim) {
@@ -159,9 +159,9 @@ size_t qgemv_attn_prompt_workspace_bytes(int tokens, int tokens_k, int batch, in
   if (head_dim != 64 && head_dim != 128) return 0;
   const int group = heads / heads_kv, rt = qg::narrow_tiles(tokens, batch, group);
   if (rt) return narrow_bytes(batch, heads_kv, rt, head_dim);
-  const int splits = qg::prompt_splits(tokens, tokens_k, batch, heads_kv, group, head_dim);
+  const int waves = qg::PROMPT_WAVES, splits = qg::prompt_splits(tokens, tokens_k, batch, heads_kv, group, head_dim, waves);
   if (splits == 1) return 0;
-  return qg::partial_bytes((size_t)qg::prompt_tiles(tokens, batch, group) * heads_kv * splits, qg::WIDE_BM, head_dim);
+  return qg::partial_bytes((size_t)qg::wide_tiles(tokens, batch, group, waves) * heads_kv * splits, 32 * waves, head_dim);
 }
 
 int qgemv_attn_prompt(int dtype, int causal, int tokens, int tokens_k, int batch, int heads, int heads_kv,
@@ -218,7 +218,8 @@ size_t qgemv_attn_tree_workspace_bytes(int tokens, int rows, int heads, int head
   if (head_dim != 64 && head_dim != 128) return 0;
   const int rt = qg::narrow_tiles(tokens, rows, heads / heads_kv);
   if (rt) return narrow_bytes(rows, heads_kv, rt, head_dim);
-  return qg::partial_bytes(2 * (size_t)qg::wide_workgroups(head_dim), qg::WIDE_BM, head_dim);
+  const int waves = qg::tree_waves(tokens, rows, heads / heads_kv);
+  return qg::partial_bytes(2 * (size_t)qg::wide_workgroups(head_dim, waves), 32 * waves, head_dim);
 }
 
 int qgemv_attn_tree(int dtype, const qgemv_kv_cache* c, int layer, int tokens, int heads, float scale,

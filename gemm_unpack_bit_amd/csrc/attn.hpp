@@ -71,9 +71,10 @@ struct AttnArgs {
 // (The narrow kernel's parts of an item are joined by one workgroup: at most
 // 256 of them.)
 inline int narrow_workgroups(int rows, int heads_kv) { return (int64_t)rows * heads_kv < 2 ? 256 : 512; }
-constexpr int wide_waves(int head_dim) { return head_dim == 64 ? 3 : 2; }
-constexpr int wide_workgroups(int head_dim) { return 256 * wide_waves(head_dim); }
-constexpr int WIDE_BM = 128;
+// (waves: per workgroup, 4 or 8; of 8, one workgroup fits a compute unit)
+constexpr int wide_waves(int head_dim, int waves) { return head_dim == 64 && waves == 4 ? 3 : 2; }
+constexpr int wide_workgroups(int head_dim, int waves) { return 256 * wide_waves(head_dim, waves) * 4 / waves; }
+constexpr int PROMPT_WAVES = 4;
 constexpr size_t partial_bytes(size_t slots, int bm, int d) { return slots * bm * (size_t)(d + 2) * 4; }
 
 // 16-row tiles a wave of the narrow kernel holds (1 or 2) for the average
@@ -82,12 +83,20 @@ inline int narrow_tiles(int tokens, int rows, int group) {
   const int64_t avg = ((int64_t)tokens + rows - 1) / rows * group;
   return avg <= 16 ? 1 : avg <= 32 ? 2 : 0;
 }
-inline int prompt_tiles(int tokens, int rows, int group) { return (int)((int64_t)tokens * group / WIDE_BM) + rows; }
+// Waves of a workgroup of the wide kernel over a paged cache (32 query rows
+// each).  With 8, more than 128 rows of a row and key head share one read of
+// its keys.
+inline int tree_waves(int tokens, int rows, int group) {
+  return ((int64_t)tokens + rows - 1) / rows * group > 128 ? 8 : 4;
+}
+inline int wide_tiles(int tokens, int rows, int group, int waves) {
+  return (int)((int64_t)tokens * group / (32 * waves)) + rows;
+}
 // parts of the keys of each tile, where whole tiles would leave compute units
-// idle: as many workgroups as fit, of at least 4 key tiles on average
-inline int prompt_splits(int tokens, int tokens_k, int rows, int heads_kv, int group, int head_dim) {
-  const int64_t items = (int64_t)prompt_tiles(tokens, rows, group) * heads_kv;
-  const int64_t most = tokens_k / rows / 256, fit = wide_workgroups(head_dim) / items;
+// idle: as many workgroups as fit, of at least 1024 keys on average
+inline int prompt_splits(int tokens, int tokens_k, int rows, int heads_kv, int group, int head_dim, int waves) {
+  const int64_t items = (int64_t)wide_tiles(tokens, rows, group, waves) * heads_kv;
+  const int64_t most = tokens_k / rows / 1024, fit = wide_workgroups(head_dim, waves) / items;
   const int64_t s = fit < most ? fit : most;
   return s < 1 ? 1 : (int)s;
 }

@@ -32,8 +32,7 @@ namespace qg {
 namespace {
 
 constexpr int KB = 64;   // keys of a tile
-constexpr int WAVES = 4;
-constexpr int BM = 32 * WAVES;
+constexpr int rows_of(int waves) { return 32 * waves; }  // query rows of a workgroup's tile (BM)
 
 __device__ __forceinline__ f16v zero16() {
   f16v z;
@@ -53,11 +52,12 @@ struct Segment {
   int64_t slot;
 };
 
-template <int D>
+template <int D, int WAVES>
 struct Tiles {
   static constexpr int PC = D / 8;                // 16-byte pieces of a row
   static constexpr int RPL = 64 / PC;             // rows of one wave-wide load
-  static constexpr int LOADS = KB / WAVES / RPL;  // loads per wave for one tile of K or V
+  static constexpr int RW = KB / WAVES;           // rows of a tile that a wave loads
+  static constexpr int LOADS = RW / RPL;          // ... for one tile of K or V
   static __device__ __forceinline__ int swz(int row) {
     return D == 128 ? ((row & 3) << 2 | (row >> 2 & 3)) : ((row & 1) << 2 | (row >> 1 & 3));
   }
@@ -70,11 +70,12 @@ struct __attribute__((aligned(16))) Buffers {
   uint16_t t[KB * D];
 };
 
-template <typename E, int D, bool PAGED>
+template <typename E, int D, bool PAGED, int WAVES>
 __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buffers<D>& k0, Buffers<D>& k1, Buffers<D>& v0,
                                             Buffers<D>& v1, uint32_t* flag) {
   const AttnArgs a = args_again();
-  using T = Tiles<D>;
+  using T = Tiles<D, WAVES>;
+  constexpr int BM = rows_of(WAVES);
   constexpr int QS = D / 16;  // matrix steps along head_dim
   constexpr int DB = D / 32;  // output blocks of 32 columns
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -113,15 +114,14 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
   most = min(most, r.keys);
   const int u0 = g.u0, u1 = min(g.u1, (most + KB - 1) / KB);
 
-  // Loads of a tile: wave w brings rows 16 w .. 16 w + 15 of it, 16 rows of
-  // one page.  A lane's place in them is a 32-bit offset, the same for every
+  // Loads of a tile: wave w brings RW rows of it (16 or 8), from one page.  A lane's place in them is a 32-bit offset, the same for every
   // tile but one that reaches past the row's last key, whose missing rows are
   // read from the last key's place.
   const uint16_t* kh = a.k + (int64_t)g.h * a.k_head;
   const uint16_t* vh = a.v + (int64_t)g.h * a.v_head;
-  const int top = (r.keys - 1) & ~15;
+  const int top = (r.keys - 1) & ~(T::RW - 1);
   auto tok_of = [&](int u) -> int64_t {  // pool or array token of the wave's first row
-    const int kb = min(u * KB + 16 * wave, top);
+    const int kb = min(u * KB + T::RW * wave, top);
     if constexpr (PAGED) {
       return pool_token(a, g.b, kb);
     } else {
@@ -131,15 +131,15 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
   typedef __attribute__((address_space(1))) const void* gp;
   typedef __attribute__((address_space(3))) void* lp;
   auto lane_off = [&](int i, int64_t token, int last) -> uint32_t {  // bytes
-    const int in = T::RPL * i + lane / T::PC;  // row in the wave's 16
-    return 2u * ((uint32_t)min(in, last) * (uint32_t)token + 8u * (uint32_t)((lane % T::PC) ^ T::swz(in)));
+    const int in = T::RPL * i + lane / T::PC;  // row in the wave's
+    return 2u * ((uint32_t)min(in, last) * (uint32_t)token + 8u * (uint32_t)((lane % T::PC) ^ T::swz(T::RW * wave + in)));
   };
   auto put = [&](const uint16_t* base, uint32_t off, int i, Buffers<D>& buf) {
     __builtin_amdgcn_global_load_lds((gp)(reinterpret_cast<const char*>(base) + off),
-                                     (lp)&buf.t[(16 * wave + T::RPL * i) * D], 16, 0, 0);
+                                     (lp)&buf.t[(T::RW * wave + T::RPL * i) * D], 16, 0, 0);
   };
   auto load = [&](const uint16_t* base, int64_t token, int u, Buffers<D>& buf) {
-    const int last = (u + 1) * KB <= r.keys ? 15 : r.keys - 1 - min(u * KB + 16 * wave, top);
+    const int last = (u + 1) * KB <= r.keys ? T::RW - 1 : r.keys - 1 - min(u * KB + T::RW * wave, top);
 #pragma unroll
     for (int i = 0; i < T::LOADS; ++i) put(base, lane_off(i, token, last), i, buf);
   };
@@ -227,15 +227,15 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
 
   // A weight of 0 does not cancel a value that is infinite or NaN: in a tile
   // with unseen keys, find the keys that have one and clear it in LDS; the
-  // whole workgroup, returns the keys.  Thread: a quarter of a key's row.
+  // whole workgroup, returns the keys.  Thread: WAVES to a key's row.
   auto odd_keys = [&](Buffers<D>& vt) -> uint64_t {
     if (threadIdx.x < 2) flag[threadIdx.x] = 0;
     __syncthreads();
-    const int key = threadIdx.x >> 2;
-    u4* p = reinterpret_cast<u4*>(&vt.t[key * D + (threadIdx.x & 3) * (D / 4)]);
+    const int key = threadIdx.x / WAVES;
+    u4* p = reinterpret_cast<u4*>(&vt.t[key * D + threadIdx.x % WAVES * (D / WAVES)]);
     uint32_t f = 0;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
+    for (int i = 0; i < D / WAVES / 8; ++i) {
       u4 w = p[i];
       uint32_t any = 0;
 #pragma unroll
@@ -330,8 +330,8 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
       uint32_t ko[T::LOADS], vo[T::LOADS];
 #pragma unroll
       for (int i = 0; i < T::LOADS; ++i) {
-        ko[i] = lane_off(i, a.k_token, 15);
-        vo[i] = lane_off(i, a.v_token, 15);
+        ko[i] = lane_off(i, a.k_token, T::RW - 1);
+        vo[i] = lane_off(i, a.v_token, T::RW - 1);
       }
       // (the tokens of the next loads are looked up a step ahead)
       int64_t tok1 = tok_of(u + 1), tok2 = tok_of(u + 2);
@@ -399,21 +399,24 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
 
 // Packed prompts: one item (128-row tile and key head) per workgroup, or one
 // of `splits` parts of its keys.  The tiles of sequence b have the numbers from
-// rows_before(b) / 128 + b on, which is at least as many as it needs and can be
+// rows_before(b) / BM + b on, which is at least as many as it needs and can be
 // looked up without a sum over the sequences.
+template <int BM>
 __device__ __forceinline__ int first_tile(const AttnArgs& a, int b) {
   return (int)((int64_t)a.cu[b] * a.group / BM) + b;
 }
 
 // tile number -> sequence and tile in it; false: no such tile
+template <int BM>
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, Row& r, int& b, int& in) {
-  b = find_row(a.rows, tile, [&](int i) { return first_tile(a, i); });
+  b = find_row(a.rows, tile, [&](int i) { return first_tile<BM>(a, i); });
   r = row_of<false>(a, b);
-  in = tile - first_tile(a, b);
+  in = tile - first_tile<BM>(a, b);
   return in >= 0 && (int64_t)in * BM < (int64_t)r.n * a.group;
 }
 
 // the part [u0, u1) of a tile's key tiles that split s takes
+template <int BM>
 __device__ __forceinline__ void split_range(const AttnArgs& a, const Row& r, int in, int splits, int s, int& u0,
                                             int& u1) {
   const int t1 = min((in * BM + BM - 1) / a.group, r.n - 1);
@@ -424,8 +427,9 @@ __device__ __forceinline__ void split_range(const AttnArgs& a, const Row& r, int
   u1 = (int)((int64_t)units * (s + 1) / splits);
 }
 
-template <typename E, int D>
-__global__ void __launch_bounds__(64 * WAVES, wide_waves(D)) attn_prompt_kernel(AttnArgs a, int tiles, int splits) {
+template <typename E, int D, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, wide_waves(D, WAVES)) attn_prompt_kernel(AttnArgs a, int tiles, int splits) {
+  constexpr int BM = rows_of(WAVES);
   __shared__ Buffers<D> k0, k1, v0, v1;
   __shared__ uint32_t flag[2];
   Segment g;
@@ -436,19 +440,20 @@ __global__ void __launch_bounds__(64 * WAVES, wide_waves(D)) attn_prompt_kernel(
   g.h = id % a.heads_kv;
   const int s = id / a.heads_kv % splits;
   const int tile = tiles - 1 - id / a.heads_kv / splits;
-  if (!find_tile(a, tile, g.r, g.b, g.tile)) return;
-  split_range(a, g.r, g.tile, splits, s, g.u0, g.u1);
+  if (!find_tile<BM>(a, tile, g.r, g.b, g.tile)) return;
+  split_range<BM>(a, g.r, g.tile, splits, s, g.u0, g.u1);
   g.slot = splits == 1 ? -1 : ((int64_t)tile * a.heads_kv + g.h) * splits + s;
-  run_segment<E, D, false>(g, (int64_t)tiles * a.heads_kv * splits, k0, k1, v0, v1, flag);
+  run_segment<E, D, false, WAVES>(g, (int64_t)tiles * a.heads_kv * splits, k0, k1, v0, v1, flag);
 }
 
 // One workgroup per 16 query rows of a tile and key head: joins their parts.
-template <typename E, int D>
+template <typename E, int D, int WAVES>
 __global__ void __launch_bounds__(256) attn_prompt_join_kernel(AttnArgs a, int splits) {
+  constexpr int BM = rows_of(WAVES);
   const int tile = blockIdx.x / (BM / 16), h = blockIdx.y;
   Row r;
   int b, in;
-  if (!find_tile(a, tile, r, b, in)) return;
+  if (!find_tile<BM>(a, tile, r, b, in)) return;
   const int row = 16 * (blockIdx.x % (BM / 16)) + (threadIdx.x >> 4), qr = in * BM + row;
   const int t = qr / a.group, head = h * a.group + qr - t * a.group;
   const Partials<BM, D> parts(a.ws, (int64_t)(gridDim.x / (BM / 16)) * a.heads_kv * splits);
@@ -459,8 +464,9 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(AttnArgs a, int s
 
 // Trees over the paged cache: the units of all items shared out evenly
 // (Units), so rows of very different lengths keep every workgroup busy.
-template <typename E, int D>
-__global__ void __launch_bounds__(64 * WAVES, wide_waves(D)) attn_tree_kernel(AttnArgs a, int workgroups) {
+template <typename E, int D, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, wide_waves(D, WAVES)) attn_tree_kernel(AttnArgs a, int workgroups) {
+  constexpr int BM = rows_of(WAVES);
   using U = Walk<BM, KB, true>;
   __shared__ Buffers<D> k0, k1, v0, v1;
   __shared__ uint32_t flag[2];
@@ -477,14 +483,15 @@ __global__ void __launch_bounds__(64 * WAVES, wide_waves(D)) attn_tree_kernel(At
     Segment g{p.r, p.b, p.h, p.tile, p.k0, p.k1, 0};
     g.slot = g.u0 == 0 && g.u1 == p.of ? -1 : 2 * (int64_t)c + (done != 0);
     done += g.u1 - g.u0;
-    run_segment<E, D, true>(g, 2 * (int64_t)workgroups, k0, k1, v0, v1, flag);
+    run_segment<E, D, true, WAVES>(g, 2 * (int64_t)workgroups, k0, k1, v0, v1, flag);
   }
 }
 
 // One workgroup per 16 query rows of a tile and key head: joins the parts of
 // an item that lay in several workgroups.
-template <typename E, int D>
+template <typename E, int D, int WAVES>
 __global__ void __launch_bounds__(256) attn_tree_join_kernel(AttnArgs a, int workgroups) {
+  constexpr int BM = rows_of(WAVES);
   using U = Walk<BM, KB, true>;
   U walk;
   walk.init(a, workgroups);
@@ -506,36 +513,41 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(AttnArgs a, int wor
                  a.o + (int64_t)(r.q0 + t) * a.o_token + (int64_t)head * a.o_head, threadIdx.x & 15);
 }
 
-template <typename E, int D>
+template <typename E, int D, int WAVES>
 hipError_t prompt(const AttnArgs& a, hipStream_t s) {
-  const int tiles = prompt_tiles(a.tokens, a.rows, a.group);
-  const int splits = prompt_splits(a.tokens, a.tokens_k, a.rows, a.heads_kv, a.group, D);
+  constexpr int BM = rows_of(WAVES);
+  const int tiles = wide_tiles(a.tokens, a.rows, a.group, WAVES);
+  const int splits = prompt_splits(a.tokens, a.tokens_k, a.rows, a.heads_kv, a.group, D, WAVES);
   const int64_t grid = (int64_t)tiles * a.heads_kv * splits;
-  hipLaunchKernelGGL((attn_prompt_kernel<E, D>), dim3((unsigned)grid), dim3(64 * WAVES), 0, s, a, tiles, splits);
+  hipLaunchKernelGGL((attn_prompt_kernel<E, D, WAVES>), dim3((unsigned)grid), dim3(64 * WAVES), 0, s, a, tiles, splits);
   if (splits > 1)
-    hipLaunchKernelGGL((attn_prompt_join_kernel<E, D>), dim3((unsigned)tiles * (BM / 16), (unsigned)a.heads_kv), dim3(256),
-                       0, s, a, splits);
+    hipLaunchKernelGGL((attn_prompt_join_kernel<E, D, WAVES>), dim3((unsigned)tiles * (BM / 16), (unsigned)a.heads_kv),
+                       dim3(256), 0, s, a, splits);
+  return hipGetLastError();
+}
+
+template <typename E, int D, int WAVES>
+hipError_t tree(const AttnArgs& a, hipStream_t s) {
+  constexpr int BM = rows_of(WAVES);
+  const int workgroups = wide_workgroups(D, WAVES);
+  hipLaunchKernelGGL((attn_tree_kernel<E, D, WAVES>), dim3(workgroups), dim3(64 * WAVES), 0, s, a, workgroups);
+  hipLaunchKernelGGL((attn_tree_join_kernel<E, D, WAVES>),
+                     dim3((unsigned)wide_tiles(a.tokens, a.rows, a.group, WAVES) * (BM / 16), (unsigned)a.heads_kv),
+                     dim3(256), 0, s, a, workgroups);
   return hipGetLastError();
 }
 
 template <typename E, int D>
-hipError_t tree(const AttnArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((attn_tree_kernel<E, D>), dim3(wide_workgroups(D)), dim3(64 * WAVES), 0, s, a, wide_workgroups(D));
-  hipLaunchKernelGGL((attn_tree_join_kernel<E, D>),
-                     dim3((unsigned)prompt_tiles(a.tokens, a.rows, a.group) * (BM / 16), (unsigned)a.heads_kv), dim3(256), 0,
-                     s, a, wide_workgroups(D));
-  return hipGetLastError();
+hipError_t launch(const AttnArgs& a, hipStream_t s) {
+  if (a.tables) return tree_waves(a.tokens, a.rows, a.group) == 8 ? tree<E, D, 8>(a, s) : tree<E, D, 4>(a, s);
+  return prompt<E, D, PROMPT_WAVES>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_attn_wide(const AttnArgs& a, hipStream_t s) {
-  if (a.tables) {
-    if (a.head_dim == 128) return a.bf16 ? tree<BF16, 128>(a, s) : tree<F16, 128>(a, s);
-    return a.bf16 ? tree<BF16, 64>(a, s) : tree<F16, 64>(a, s);
-  }
-  if (a.head_dim == 128) return a.bf16 ? prompt<BF16, 128>(a, s) : prompt<F16, 128>(a, s);
-  return a.bf16 ? prompt<BF16, 64>(a, s) : prompt<F16, 64>(a, s);
+  if (a.head_dim == 128) return a.bf16 ? launch<BF16, 128>(a, s) : launch<F16, 128>(a, s);
+  return a.bf16 ? launch<BF16, 64>(a, s) : launch<F16, 64>(a, s);
 }
 
 }  // namespace qg
