@@ -172,59 +172,68 @@ struct Sight {
   }
 };
 
-// partial results: [slots][BM] (max, sum), then [slots][BM][D] sums
+// Partial results: [slots][BM] (max, sum), then per slot the sums in groups of
+// four columns, each group's 32 rows side by side (a wave's store of its 32
+// rows is contiguous): [BM / 32][D / 4][32][4].
 template <int BM, int D>
 struct Partials {
   float *ml, *o;
   __device__ __forceinline__ Partials(float* ws, int64_t slots) : ml(ws), o(ws + slots * BM * 2) {}
   __device__ __forceinline__ float* ml_at(int64_t slot, int row) const { return ml + (slot * BM + row) * 2; }
-  __device__ __forceinline__ float* o_at(int64_t slot, int row) const { return o + (slot * BM + row) * D; }
+  // columns 4 c .. 4 c + 3 of a row
+  __device__ __forceinline__ f4* o_at(int64_t slot, int row, int c) const {
+    return reinterpret_cast<f4*>(o + slot * BM * D) + ((row >> 5) * (D / 4) + c) * 32 + (row & 31);
+  }
 };
 
-// Joins partial results of one query row in the order of their slots, four
-// parts' loads at a time: o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
-// 16 threads (`thread` of them) hold the row's columns, D / 16 each.
-template <typename E, int BM, int D, typename F>
-__device__ __forceinline__ void join_row(const Partials<BM, D>& p, int row, int parts, F&& slot, uint16_t* out, int thread) {
-  constexpr int DL = D / 16;
-  typedef float fl __attribute__((ext_vector_type(DL)));
-  const int col = DL * thread;
+// Joins the partial results of 32 query rows (row0 .. row0 + 31 of the tile) in
+// the order of their slots: o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  A
+// workgroup of 256 threads: a thread has one row and every eighth group of four
+// columns of it, so a wave's load is two runs of 512 bytes.
+// out(row) is where the row's result goes, NULL if nowhere.
+template <typename E, int BM, int D, typename F, typename O>
+__device__ __forceinline__ void join_rows(const Partials<BM, D>& p, int row0, int parts, F&& slot, O&& out) {
+  constexpr int G = D / 32;  // column groups of a thread
+  const int row = row0 + (threadIdx.x & 31), c0 = threadIdx.x >> 5;
+  uint16_t* to = out(row);
+  if (!to) return;
   float m = NEG_INF, l = 0.f;
-  fl acc;
+  f4 acc[G];
 #pragma unroll
-  for (int e = 0; e < DL; ++e) acc[e] = 0.f;
-  for (int i = 0; i < parts; i += 4) {
-    float mi[4], li[4];
-    fl oi[4];
+  for (int e = 0; e < G; ++e) acc[e] = f4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < parts; i += 2) {
+    float mi[2], li[2];
+    f4 oi[2][G];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < 2; ++x) {
       const int64_t s = slot(i + x < parts ? i + x : i);
       const float* ml = p.ml_at(s, row);
       mi[x] = i + x < parts ? ml[0] : NEG_INF;
       li[x] = i + x < parts ? ml[1] : 0.f;
-      oi[x] = *reinterpret_cast<const fl*>(p.o_at(s, row) + col);
-    }
-    float mn = m;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) mn = fmaxf(mn, mi[x]);
+      for (int e = 0; e < G; ++e) oi[x][e] = *p.o_at(s, row, c0 + 8 * e);
+    }
+    const float mn = fmaxf(m, fmaxf(mi[0], mi[1]));
     const float base = mn == NEG_INF ? 0.f : mn, w = exp2_(m - base);
     l *= w;
-    acc *= w;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int e = 0; e < G; ++e) acc[e] *= w;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
       const float wx = exp2_(mi[x] - base);
       l += wx * li[x];
 #pragma unroll
-      for (int e = 0; e < DL; ++e) acc[e] += li[x] == 0.f ? 0.f : wx * oi[x][e];  // (no weights: o may be anything)
+      for (int e = 0; e < G; ++e)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) acc[e][y] += li[x] == 0.f ? 0.f : wx * oi[x][e][y];  // (no weights: o may be anything)
     }
     m = mn;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  typedef uint32_t vw __attribute__((ext_vector_type(DL / 2)));
-  vw y;
 #pragma unroll
-  for (int e = 0; e < DL / 2; ++e) y[e] = E::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  *reinterpret_cast<vw*>(out + col) = y;
+  for (int e = 0; e < G; ++e)
+    *reinterpret_cast<u2*>(to + 4 * (c0 + 8 * e)) =
+        u2{E::pack(acc[e][0] * inv, acc[e][1] * inv), E::pack(acc[e][2] * inv, acc[e][3] * inv)};
 }
 
 // inclusive sums over the wave's lanes of values < 2^24 (row shifts, then

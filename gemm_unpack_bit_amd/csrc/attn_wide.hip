@@ -321,9 +321,12 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
     load(vh + tok0 * a.v_token, a.v_token, u0, v0);
     arrived();
     if (active) scores(k0, sa);
-    // steps whose tile every row sees in full, and whose loads are of whole
-    // tiles: two at a time (the waves without rows compute along, on zeros)
-    int uf = min(min(common / KB, u1 - 2), r.keys / KB - 2);
+    // steps whose tile every row sees in full, two at a time (the waves without
+    // rows compute along, on zeros).  Their loads are of whole tiles: in a page
+    // the places behind the last key are there too, packed keys need all 64.
+    // (The last ones bring tiles, and compute scores, that nothing uses.)
+    int uf = min(common / KB, u1);
+    if constexpr (!PAGED) uf = min(uf, r.keys / KB - 2);
     uf = u0 + ((uf - u0) & ~1);
     int u = u0;
     if (u < uf) {
@@ -362,7 +365,7 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
       step(u, k0, k1, v0, v1, sa, sb);
       if (u + 1 < u1) step(u + 1, k1, k0, v1, v0, sb, sa);
     }
-    lds_barrier();  // the buffers are free for the next segment
+    arrived();  // the buffers are free for the next segment
   }
 
   l = half_sum(l);
@@ -382,12 +385,11 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
   } else {
     const Partials<BM, D> parts(e.ws, slots);
     const int pr = 32 * wave + c32;
-    float* po = parts.o_at(g.slot, pr);
 #pragma unroll
     for (int db = 0; db < DB; ++db)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<f4*>(po + 32 * db + 8 * i + 4 * half) =
+        *parts.o_at(g.slot, pr, 8 * db + 2 * i + half) =
             f4{o[db][4 * i], o[db][4 * i + 1], o[db][4 * i + 2], o[db][4 * i + 3]};
     if (half == 0) {
       float* ml = parts.ml_at(g.slot, pr);
@@ -413,6 +415,12 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, Row& r, i
   r = row_of<false>(a, b);
   in = tile - first_tile<BM>(a, b);
   return in >= 0 && (int64_t)in * BM < (int64_t)r.n * a.group;
+}
+
+// where query row qr (t * group + g) of key head h has its output; NULL past the last
+__device__ __forceinline__ uint16_t* output_row(const AttnArgs& a, const Row& r, int h, int qr) {
+  const int t = qr / a.group, g = qr - t * a.group;
+  return t < r.n ? a.o + (int64_t)(r.q0 + t) * a.o_token + (int64_t)(h * a.group + g) * a.o_head : nullptr;
 }
 
 // the part [u0, u1) of a tile's key tiles that split s takes
@@ -446,20 +454,17 @@ __global__ void __launch_bounds__(64 * WAVES, wide_waves(D, WAVES)) attn_prompt_
   run_segment<E, D, false, WAVES>(g, (int64_t)tiles * a.heads_kv * splits, k0, k1, v0, v1, flag);
 }
 
-// One workgroup per 16 query rows of a tile and key head: joins their parts.
+// One workgroup per 32 query rows of a tile and key head: joins their parts.
 template <typename E, int D, int WAVES>
 __global__ void __launch_bounds__(256) attn_prompt_join_kernel(AttnArgs a, int splits) {
   constexpr int BM = rows_of(WAVES);
-  const int tile = blockIdx.x / (BM / 16), h = blockIdx.y;
+  const int tile = blockIdx.x / (BM / 32), h = blockIdx.y;
   Row r;
   int b, in;
   if (!find_tile<BM>(a, tile, r, b, in)) return;
-  const int row = 16 * (blockIdx.x % (BM / 16)) + (threadIdx.x >> 4), qr = in * BM + row;
-  const int t = qr / a.group, head = h * a.group + qr - t * a.group;
-  const Partials<BM, D> parts(a.ws, (int64_t)(gridDim.x / (BM / 16)) * a.heads_kv * splits);
-  if (t >= r.n) return;
-  join_row<E>(parts, row, splits, [&](int i) { return ((int64_t)tile * a.heads_kv + h) * splits + i; },
-                 a.o + (int64_t)(r.q0 + t) * a.o_token + (int64_t)head * a.o_head, threadIdx.x & 15);
+  const Partials<BM, D> parts(a.ws, (int64_t)(gridDim.x / (BM / 32)) * a.heads_kv * splits);
+  join_rows<E>(parts, 32 * (blockIdx.x % (BM / 32)), splits, [&](int i) { return ((int64_t)tile * a.heads_kv + h) * splits + i; },
+               [&](int row) { return output_row(a, r, h, in * BM + row); });
 }
 
 // Trees over the paged cache: the units of all items shared out evenly
@@ -487,7 +492,7 @@ __global__ void __launch_bounds__(64 * WAVES, wide_waves(D, WAVES)) attn_tree_ke
   }
 }
 
-// One workgroup per 16 query rows of a tile and key head: joins the parts of
+// One workgroup per 32 query rows of a tile and key head: joins the parts of
 // an item that lay in several workgroups.
 template <typename E, int D, int WAVES>
 __global__ void __launch_bounds__(256) attn_tree_join_kernel(AttnArgs a, int workgroups) {
@@ -495,7 +500,7 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(AttnArgs a, int wor
   using U = Walk<BM, KB, true>;
   U walk;
   walk.init(a, workgroups);
-  const int tile = blockIdx.x / (BM / 16), h = blockIdx.y;
+  const int tile = blockIdx.x / (BM / 32), h = blockIdx.y;
   auto first_at = [&](int q0, int b) { return (int)((int64_t)q0 * a.group / BM) + b; };
   const int b = walk.find(a, tile, [&](const Row& r, int i) { return first_at(r.q0, i); },
                           [&](int i) { return first_at(a.cu[i], i); });
@@ -506,11 +511,8 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(AttnArgs a, int wor
   if (in < 0 || in >= U::tiles(a, r)) return;
   const typename U::Parts p = walk.parts(first + (int64_t)(h * U::tiles(a, r) + in) * U::units(r), U::units(r));
   if (p.n == 1) return;
-  const int row = 16 * (blockIdx.x % (BM / 16)) + (threadIdx.x >> 4), qr = in * BM + row;
-  const int t = qr / a.group, head = h * a.group + qr - t * a.group;
-  if (t >= r.n) return;
-  join_row<E>(Partials<BM, D>(a.ws, 2 * (int64_t)workgroups), row, p.n, [&](int i) { return p.slot(i); },
-                 a.o + (int64_t)(r.q0 + t) * a.o_token + (int64_t)head * a.o_head, threadIdx.x & 15);
+  join_rows<E>(Partials<BM, D>(a.ws, 2 * (int64_t)workgroups), 32 * (blockIdx.x % (BM / 32)), p.n,
+               [&](int i) { return p.slot(i); }, [&](int row) { return output_row(a, r, h, in * BM + row); });
 }
 
 template <typename E, int D, int WAVES>
@@ -521,7 +523,7 @@ hipError_t prompt(const AttnArgs& a, hipStream_t s) {
   const int64_t grid = (int64_t)tiles * a.heads_kv * splits;
   hipLaunchKernelGGL((attn_prompt_kernel<E, D, WAVES>), dim3((unsigned)grid), dim3(64 * WAVES), 0, s, a, tiles, splits);
   if (splits > 1)
-    hipLaunchKernelGGL((attn_prompt_join_kernel<E, D, WAVES>), dim3((unsigned)tiles * (BM / 16), (unsigned)a.heads_kv),
+    hipLaunchKernelGGL((attn_prompt_join_kernel<E, D, WAVES>), dim3((unsigned)tiles * (BM / 32), (unsigned)a.heads_kv),
                        dim3(256), 0, s, a, splits);
   return hipGetLastError();
 }
@@ -532,7 +534,7 @@ hipError_t tree(const AttnArgs& a, hipStream_t s) {
   const int workgroups = wide_workgroups(D, WAVES);
   hipLaunchKernelGGL((attn_tree_kernel<E, D, WAVES>), dim3(workgroups), dim3(64 * WAVES), 0, s, a, workgroups);
   hipLaunchKernelGGL((attn_tree_join_kernel<E, D, WAVES>),
-                     dim3((unsigned)wide_tiles(a.tokens, a.rows, a.group, WAVES) * (BM / 16), (unsigned)a.heads_kv),
+                     dim3((unsigned)wide_tiles(a.tokens, a.rows, a.group, WAVES) * (BM / 32), (unsigned)a.heads_kv),
                      dim3(256), 0, s, a, workgroups);
   return hipGetLastError();
 }
