@@ -161,7 +161,8 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
   }
 
   // S^T of a tile
-  auto scores = [&](const Buffers<D>& kt, f16v (&sc)[2]) {
+  f16v sc[2];
+  auto scores = [&](const Buffers<D>& kt) {
     const char* base = reinterpret_cast<const char*>(kt.t);
     uint32_t at = k_at;
     asm volatile("" : "+v"(at));
@@ -181,9 +182,11 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
   const float scale = a.scale;
   float m = NEG_INF, l = 0.f;  // m: the weights' reference, at most E::SLACK below the largest score
 
-  // the tile's scores into weights, and O^T += V^T P^T; with `some` there may
-  // be unseen keys among them, at -inf (whose product with a scale of 0 is not)
-  auto weigh = [&](const Buffers<D>& vt, f16v (&sc)[2], auto some) {
+  // the tile's scores into weights (P^T, 16 keys a piece); with `some` there
+  // may be unseen keys among them, at -inf (whose product with a scale of 0 is
+  // not)
+  u4 pf[4];
+  auto weigh = [&](auto some) {
     float mx = sc[0][0];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
@@ -199,9 +202,6 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
       for (int i = 0; i < DB; ++i) o[i] *= w;
     }
     const float base = m == NEG_INF ? 0.f : m - E::LIFT;
-    const char* vb = reinterpret_cast<const char*>(vt.t);
-    uint32_t at[2] = {v_at[0], v_at[1]};
-    asm volatile("" : "+v"(at[0]), "+v"(at[1]));
 #pragma unroll
     for (int k4 = 0; k4 < 4; ++k4) {
       const int x = k4 >> 1, e = 8 * (k4 & 1);
@@ -212,7 +212,17 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
         if constexpr (decltype(some)::value) p[i] = sc[x][e + i] == NEG_INF ? 0.f : p[i];
         l += p[i];
       }
-      const u4 pf = u4{E::pack(p[0], p[1]), E::pack(p[2], p[3]), E::pack(p[4], p[5]), E::pack(p[6], p[7])};
+      pf[k4] = u4{E::pack(p[0], p[1]), E::pack(p[2], p[3]), E::pack(p[4], p[5]), E::pack(p[6], p[7])};
+    }
+  };
+
+  // O^T += V^T P^T
+  auto gather = [&](const Buffers<D>& vt) {
+    const char* vb = reinterpret_cast<const char*>(vt.t);
+    uint32_t at[2] = {v_at[0], v_at[1]};
+    asm volatile("" : "+v"(at[0]), "+v"(at[1]));
+#pragma unroll
+    for (int k4 = 0; k4 < 4; ++k4)
 #pragma unroll
       for (int db = 0; db < DB; ++db) {
         s4v v[2];
@@ -220,9 +230,8 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
         for (int y = 0; y < 2; ++y)
           v[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(vb + (at[y] ^ (64 * db)) + 2 * D * 16 * k4));
         const u2 lo = __builtin_bit_cast(u2, v[0]), hi = __builtin_bit_cast(u2, v[1]);
-        o[db] = E::mfma32(u4{lo[0], lo[1], hi[0], hi[1]}, pf, o[db]);
+        o[db] = E::mfma32(u4{lo[0], lo[1], hi[0], hi[1]}, pf[k4], o[db]);
       }
-    }
   };
 
   // A weight of 0 does not cancel a value that is infinite or NaN: in a tile
@@ -276,18 +285,18 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
     }
   };
 
-  // Pipeline.  Step u: the scores of tile u + 1 (matrix cores), then the
-  // weights and output sums of tile u, whose scores the step before left.
-  // K of tile u + 1 and V of tile u were asked for one step ago; the barrier
-  // after the wait also says that every wave is past step u - 1, so K of tile
-  // u + 2 may go where tile u's was and V of tile u + 1 where tile u - 1's was.
+  // Pipeline.  Step u: the weights of tile u, whose scores the step before
+  // left (vector units), then its output sums and the scores of tile u + 1
+  // (matrix cores); the two waves of a SIMD take turns at these.  K of tile
+  // u + 1 and V of tile u were asked for one step ago; the barrier after the
+  // wait also says that every wave is past step u - 1, so K of tile u + 2 may
+  // go where tile u's was and V of tile u + 1 where tile u - 1's was.
   auto arrived = [&]() {
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0
     lds_barrier();
   };
   // any step
-  auto step = [&](int u, Buffers<D>& k_now, Buffers<D>& k_next, Buffers<D>& v_now, Buffers<D>& v_next,
-                  f16v (&cur)[2], f16v (&next)[2]) {
+  auto step = [&](int u, Buffers<D>& k_now, Buffers<D>& k_next, Buffers<D>& v_now, Buffers<D>& v_next) {
     const AttnArgs a = args_again();
     const uint16_t* kh = a.k + (int64_t)g.h * a.k_head;
     const uint16_t* vh = a.v + (int64_t)g.h * a.v_head;
@@ -299,28 +308,28 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
     uint64_t odd = 0;
     if (masked) odd = odd_keys(v_now);
     if (active) {
-      if (u + 1 < u1) scores(k_next, next);
       if (masked) {
         const AttnArgs a = args_again();
         const uint64_t seen = sight.window(a, r, kb) >> (4 * half);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) cur[x][i] = seen >> (32 * x + 8 * (i / 4) + i % 4) & 1 ? cur[x][i] : NEG_INF;
+          for (int i = 0; i < 16; ++i) sc[x][i] = seen >> (32 * x + 8 * (i / 4) + i % 4) & 1 ? sc[x][i] : NEG_INF;
       }
-      weigh(v_now, cur, std::true_type{});
+      weigh(std::true_type{});
+      gather(v_now);
       if (odd) add_odd(odd, kb);
+      if (u + 1 < u1) scores(k_next);
     }
   };
 
   if (u0 < u1) {
-    f16v sa[2], sb[2];
     const int64_t tok0 = tok_of(u0);
     load(kh + tok0 * a.k_token, a.k_token, u0, k0);
     if (u0 + 1 < u1) load(kh + tok_of(u0 + 1) * a.k_token, a.k_token, u0 + 1, k1);
     load(vh + tok0 * a.v_token, a.v_token, u0, v0);
     arrived();
-    if (active) scores(k0, sa);
+    if (active) scores(k0);
     // steps whose tile every row sees in full, two at a time (the waves without
     // rows compute along, on zeros).  Their loads are of whole tiles: in a page
     // the places behind the last key are there too, packed keys need all 64.
@@ -338,8 +347,7 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
       }
       // (the tokens of the next loads are looked up a step ahead)
       int64_t tok1 = tok_of(u + 1), tok2 = tok_of(u + 2);
-      auto fast = [&](Buffers<D>& k_now, Buffers<D>& k_next, Buffers<D>& v_now, Buffers<D>& v_next, f16v (&cur)[2],
-                      f16v (&next)[2]) {
+      auto fast = [&](Buffers<D>& k_now, Buffers<D>& k_next, Buffers<D>& v_now, Buffers<D>& v_next) {
         arrived();
         const uint16_t* kp = kh + tok2 * a.k_token;
         const uint16_t* vp = vh + tok1 * a.v_token;
@@ -353,17 +361,18 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
         tok1 = tok2;
         tok2 = tok_of(u + 3);
         ++u;
-        scores(k_next, next);
-        weigh(v_now, cur, std::false_type{});
+        weigh(std::false_type{});
+        gather(v_now);
+        scores(k_next);
       };
       while (u < uf) {
-        fast(k0, k1, v0, v1, sa, sb);
-        fast(k1, k0, v1, v0, sb, sa);
+        fast(k0, k1, v0, v1);
+        fast(k1, k0, v1, v0);
       }
     }
     for (; u < u1; u += 2) {
-      step(u, k0, k1, v0, v1, sa, sb);
-      if (u + 1 < u1) step(u + 1, k1, k0, v1, v0, sb, sa);
+      step(u, k0, k1, v0, v1);
+      if (u + 1 < u1) step(u + 1, k1, k0, v1, v0);
     }
     arrived();  // the buffers are free for the next segment
   }
