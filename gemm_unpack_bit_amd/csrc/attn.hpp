@@ -60,6 +60,7 @@ struct AttnArgs {
   const uint64_t* mask;
   int mask_words;
   float* ws;
+  float join_cost;  // of one part in units of keys, over the call's items (narrow kernel, Walk::init)
   uint64_t nonce;  // of the call (attn_narrow.hip, last_part): 48 bits, not 0
 };
 

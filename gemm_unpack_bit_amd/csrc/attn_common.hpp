@@ -275,7 +275,10 @@ __device__ __forceinline__ int share_of(int workgroup, int shares) {
   return in < run ? (workgroup % NXCD) * run + in : shares;
 }
 
-template <int BM, int KB, bool PAGED>
+// Where one workgroup joins an item's parts, a part costs it some of a unit's
+// time, and an item of n units is done soonest in parts of sqrt(n * that): per
+// is at least so much, up to LEAST (1: a join that is itself shared out).
+template <int BM, int KB, bool PAGED, int LEAST>
 struct Walk {
   int64_t total, per;
   int b0;           // the first row held
@@ -313,7 +316,13 @@ struct Walk {
       hold(a, first, total);
       total += all;
     }
-    per = total ? (total + workgroups - 1) / workgroups : 1;
+    per = (total + workgroups - 1) / workgroups;
+    if (LEAST > 1 && per < LEAST) {
+      const float joined = __builtin_amdgcn_sqrtf((float)(uint32_t)min(total, (int64_t)UINT32_MAX) * a.join_cost);
+      const int least = uniform((int)fminf(joined, (float)LEAST));
+      if (per < least) per = least;
+    }
+    if (per < 1) per = 1;
   }
   __device__ __forceinline__ int shares() const { return (int)((total + per - 1) / per); }
   __device__ __forceinline__ Row row(int lane) const {

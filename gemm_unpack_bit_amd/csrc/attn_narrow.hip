@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
   constexpr int DW = DL / 2;  // ... in 32-bit words
   constexpr int PITCH = D + 4;
   typedef uint32_t vw __attribute__((ext_vector_type(DW)));
-  using U = Walk<BM, KB, PAGED>;
+  using U = Walk<BM, KB, PAGED, 16>;
   __shared__ __attribute__((aligned(16))) float o_s[WAVES][BM][PITCH];
   __shared__ float m_s[WAVES][BM], l_s[WAVES][BM];
   __shared__ uint32_t last_s;
@@ -419,6 +419,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
         const int RP = 1 << lg, PL = 16 >> lg;
         const int rl = threadIdx.x >> 4, pl = rl >> lg, col = DL * (threadIdx.x & 15);
         typedef float fl __attribute__((ext_vector_type(DL)));
+        constexpr int AT_ONCE = 4;  // parts on their way
         for (int row0 = 0; row0 < live; row0 += RP) {
           const int row = row0 + (rl & (RP - 1));
           float mj = NEG_INF, lj = 0.f;
@@ -426,11 +427,11 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
 #pragma unroll
           for (int j = 0; j < DL; ++j) acc[j] = 0.f;
           if (row < live)
-            for (int i = pl; i < p.n; i += 4 * PL) {
-              float mi[4], li[4];
-              fl oi[4];
+            for (int i = pl; i < p.n; i += AT_ONCE * PL) {
+              float mi[AT_ONCE], li[AT_ONCE];
+              fl oi[AT_ONCE];
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
+              for (int x = 0; x < AT_ONCE; ++x) {
                 const int64_t at = p.slot(i + x * PL < p.n ? i + x * PL : i);
                 const f2v ml = parts.ml(at, row);
                 mi[x] = i + x * PL < p.n ? ml[0] : NEG_INF;
@@ -443,12 +444,12 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
               }
               float mn = mj;
 #pragma unroll
-              for (int x = 0; x < 4; ++x) mn = fmaxf(mn, mi[x]);
+              for (int x = 0; x < AT_ONCE; ++x) mn = fmaxf(mn, mi[x]);
               const float base = mn == NEG_INF ? 0.f : mn, w = exp2_(mj - base);
               lj *= w;
               acc *= w;
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
+              for (int x = 0; x < AT_ONCE; ++x) {
                 const float wx = exp2_(mi[x] - base);
                 lj += wx * li[x];
 #pragma unroll
@@ -508,7 +509,17 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_attn_narrow(const AttnArgs& a, int rt, hipStream_t s) {
+// Joining a part with R queries takes about R / 64 of the time of a unit of keys:
+// 16 rows of them at once and 4 parts in flight.  Over an average item's n units
+// the least time is at sqrt(n * R / 64) units a part.  Measured against parts as
+// small as the workgroups allow: 8 tokens on 16000 keys 63 -> 35 us, 8-token
+// trees on 4000 keys 31 -> 22 us, one key head with 8 heads on 131072 keys
+// 43 -> 35 us; single tokens of 4 heads a key head stay as they were.
+hipError_t launch_attn_narrow(const AttnArgs& args, int rt, hipStream_t s) {
+  AttnArgs a = args;
+  const float items = (float)a.rows * (float)a.heads_kv;
+  const float queries = (float)a.tokens * (float)a.group / (float)a.rows;
+  a.join_cost = (queries < 16.f * rt ? queries : 16.f * rt) / (64.f * items);
   if (a.tables) return rt == 1 ? launch_d<1, true>(a, s) : launch_d<2, true>(a, s);
   return rt == 1 ? launch_d<1, false>(a, s) : launch_d<2, false>(a, s);
 }

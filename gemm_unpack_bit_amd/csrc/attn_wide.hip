@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(AttnArgs a, int s
 template <typename E, int D, int WAVES>
 __global__ void __launch_bounds__(64 * WAVES, wide_waves(D, WAVES)) attn_tree_kernel(AttnArgs a, int workgroups) {
   constexpr int BM = rows_of(WAVES);
-  using U = Walk<BM, KB, true>;
+  using U = Walk<BM, KB, true, 1>;
   __shared__ Buffers<D> k0, k1, v0, v1;
   __shared__ uint32_t flag[2];
   // (the rows are looked up again for every segment, of which there are few,
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(64 * WAVES, wide_waves(D, WAVES)) attn_tree_ke
 template <typename E, int D, int WAVES>
 __global__ void __launch_bounds__(256) attn_tree_join_kernel(AttnArgs a, int workgroups) {
   constexpr int BM = rows_of(WAVES);
-  using U = Walk<BM, KB, true>;
+  using U = Walk<BM, KB, true, 1>;
   U walk;
   walk.init(a, workgroups);
   const int tile = blockIdx.x / (BM / 32), h = blockIdx.y;
