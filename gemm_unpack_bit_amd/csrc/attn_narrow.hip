@@ -23,7 +23,12 @@
 //   four lane quarters by two swaps, the sum only once at the end.
 // The waves of a workgroup take the steps of its key range in turn, each with
 // its own m, l, O, joined in LDS at the end.  Few rows leave few tiles, so the
-// key axis is split over workgroups (Units).
+// key axis is split over workgroups (Walk).
+//
+// Measured (fp16, head_dim 128, pages of 16): one token of 64 heads over 8 key
+// heads for 32 rows of 18000 cached tokens, 399 us, 5.9 TB/s (a streaming read
+// of memory reaches 7.1); one row of 777 tokens, 32 heads over 8, 7.9 us, most
+// of it a launch and three trips to memory one behind the other.
 #include <type_traits>
 
 #include "attn_common.hpp"
