@@ -25,27 +25,33 @@ namespace {
 
 constexpr int SCAN = 1024;  // threads of the one-workgroup kernels
 
-// Exclusive prefix sum over the workgroup's SCAN threads; total in all.
-__device__ __forceinline__ int block_scan(int v, int& total, int* red) {
+// Exclusive prefix sum over the workgroup's SCAN threads; total in all.  Sums
+// end at 2^32 - 1: rows with offsets that go up and down can need more pages
+// together than 32 bits count, and whatever does not fit a pool is too many.
+// (The additions saturate by themselves; with sums of 64 bits an append of one
+// token to 48 rows takes 11.7 us for 11.3.)
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t& total, uint32_t* red) {
+  auto add = [](uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); };
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  int s = v;
+  uint32_t s = v;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(s, d);
-    if (lane >= d) s += o;
+    const uint32_t o = __shfl_up(s, d);
+    if (lane >= d) s = add(s, o);
   }
   if (lane == 63) red[w] = s;
   __syncthreads();
-  int before = 0, all = 0;
+  uint32_t before = 0, all = 0;
 #pragma unroll
   for (int i = 0; i < SCAN / 64; ++i) {
-    const int x = red[i];
-    before += i < w ? x : 0;
-    all += x;
+    const uint32_t x = red[i];
+    before = add(before, i < w ? x : 0);
+    all = add(all, x);
   }
   __syncthreads();
   total = all;
-  return before + s - v;
+  s = add(before, s);
+  return s == UINT32_MAX ? s : s - v;
 }
 
 // The lowest `want` free pages into list, in order; returns how many there are
@@ -101,6 +107,7 @@ __device__ __forceinline__ int pages_of(int tokens, int shift) { return (int)(((
 // whatever the pool holds (bad count, table too short) is 0 pages, ok false.
 __global__ void __launch_bounds__(SCAN) kv_reserve_kernel(KvArgs c, const int32_t* cu, int32_t* pos, KvScratch w) {
   __shared__ int red[SCAN / 64];
+  __shared__ uint32_t sums[SCAN / 64];
   __shared__ int at_s[SCAN], need_s[SCAN], have_s[SCAN];
   struct Row {
     int len, n, have, need, bad;
@@ -122,12 +129,12 @@ __global__ void __launch_bounds__(SCAN) kv_reserve_kernel(KvArgs c, const int32_
     return r;
   };
   Row r = row(threadIdx.x);
-  int before, total;  // (the first 1024 rows are read and summed once)
-  before = block_scan(r.need, total, red);
+  uint32_t before, total;  // (the first 1024 rows are read and summed once)
+  before = block_scan(r.need, total, sums);
   int64_t want = total;
   for (int b0 = SCAN; b0 < c.rows; b0 += SCAN) {
-    int more;
-    block_scan(row(b0 + threadIdx.x).need, more, red);
+    uint32_t more;
+    block_scan(row(b0 + threadIdx.x).need, more, sums);
     want += more;
   }
   const int got = want ? find_free(c.refs, c.pages, want < c.pages ? (int)want : c.pages, w.free_list, red) : 0;
@@ -137,13 +144,13 @@ __global__ void __launch_bounds__(SCAN) kv_reserve_kernel(KvArgs c, const int32_
     const int b = b0 + threadIdx.x;
     if (b0) {
       r = row(b);
-      before = block_scan(r.need, total, red);
+      before = block_scan(r.need, total, sums);
     }
     const int64_t at = given + before;
     given += total;
     const bool fits = r.need == 0 || at + r.need <= got;
     const bool ok = b < c.rows && !r.bad && fits;
-    at_s[threadIdx.x] = (int)at;
+    at_s[threadIdx.x] = (int)at;  // (used where the row fits: at most got)
     need_s[threadIdx.x] = ok ? r.need : 0;
     have_s[threadIdx.x] = r.have;
     if (b < c.rows) {
@@ -260,11 +267,12 @@ __global__ void __launch_bounds__(256) kv_fork_rows_kernel(KvArgs c, const int32
 // One workgroup: a fresh page for every row that copies, in row order.
 __global__ void __launch_bounds__(SCAN) kv_fork_pages_kernel(KvArgs c, KvArgs out, KvScratch w) {
   __shared__ int red[SCAN / 64];
+  __shared__ uint32_t sums[SCAN / 64];
   int want = 0;
   for (int b0 = 0; b0 < out.rows; b0 += SCAN) {
     const int b = b0 + threadIdx.x;
-    int total;
-    block_scan(b < out.rows && w.src[b] >= 0, total, red);
+    uint32_t total;
+    block_scan(b < out.rows && w.src[b] >= 0, total, sums);
     want += total;
   }
   if (!want) return;
@@ -273,8 +281,8 @@ __global__ void __launch_bounds__(SCAN) kv_fork_pages_kernel(KvArgs c, KvArgs ou
   for (int b0 = 0; b0 < out.rows; b0 += SCAN) {
     const int b = b0 + threadIdx.x;
     const bool copy = b < out.rows && w.src[b] >= 0;
-    int total;
-    const int at = given + block_scan(copy, total, red);
+    uint32_t total;
+    const int at = given + (int)block_scan(copy, total, sums);
     given += total;
     if (copy) {
       const int full = out.lens[b] >> c.page_shift;
@@ -297,6 +305,7 @@ __global__ void __launch_bounds__(SCAN) kv_fork_pages_kernel(KvArgs c, KvArgs ou
 constexpr int FORK_ROWS = 256;
 __global__ void __launch_bounds__(SCAN) kv_fork_small_kernel(KvArgs c, const int32_t* parents, KvArgs out, KvScratch w) {
   __shared__ int red[SCAN / 64];
+  __shared__ uint32_t sums[SCAN / 64];
   // of the old rows: children, length; of the new rows: parent, and whether an
   // earlier new row has it too
   __shared__ int kids[FORK_ROWS], lens[FORK_ROWS], par[FORK_ROWS], later[FORK_ROWS], list[FORK_ROWS];
@@ -349,8 +358,8 @@ __global__ void __launch_bounds__(SCAN) kv_fork_small_kernel(KvArgs c, const int
   // the counts have to be in memory (this XCD's cache) before they are
   // searched: every wave waits for its atomics, then all for one another
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0
-  int want;
-  const int at = block_scan(src >= 0, want, red);
+  uint32_t copies;
+  const int at = (int)block_scan(src >= 0, copies, sums), want = (int)copies;
   const int got = want ? find_free(c.refs, c.pages, want, list, red) : 0;
   // (a later child's entry for its partial page is written here alone)
   if (x < out.rows) {
