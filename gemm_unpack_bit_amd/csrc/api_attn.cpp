@@ -32,6 +32,7 @@ Span span(const qgemv_heads& x, int tokens, int heads, int dim) {
 }
 
 constexpr int64_t STRIDE_MAX = (int64_t)1 << 40;  // (products with 32-bit counts stay in 64 bits once checked)
+constexpr int64_t KEYS_MAX = ((int64_t)1 << 31) - 1024;  // (the kernels look a few steps past a row's last key, in 32 bits)
 constexpr int64_t KEY_STRIDE_MAX = (int64_t)1 << 26;  // 16 keys of a tile lie within 32-bit offsets of one another
 
 // strides in range and, for an output, no element shared
@@ -98,7 +99,7 @@ int check_cache(const qgemv_kv_cache* c, bool state) {
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return QGEMV_ERR_UNSUPPORTED;
   if (c->layers < 1 || c->pages < 1 || c->heads_kv < 1 || c->rows < 0 || c->rows > 65535 || c->max_pages < 1)
     return QGEMV_ERR_SHAPE;
-  if ((int64_t)c->max_pages * c->page_size >= (int64_t)1 << 31 || (int64_t)c->heads_kv * c->head_dim >= KEY_STRIDE_MAX || c->layers > 65536 ||
+  if ((int64_t)c->max_pages * c->page_size > KEYS_MAX || (int64_t)c->heads_kv * c->head_dim >= KEY_STRIDE_MAX || c->layers > 65536 ||
       (double)c->layers * c->pages * c->page_size * c->heads_kv * c->head_dim >= 1e15 ||
       (int64_t)c->layers * c->heads_kv * c->head_dim >= (int64_t)1 << 32)  // (a launch's threads: a thread per 16 bytes)
     return QGEMV_ERR_SHAPE;
@@ -155,7 +156,7 @@ hipStream_t stream_of(qgemv_stream_t s) { return reinterpret_cast<hipStream_t>(s
 extern "C" {
 
 size_t qgemv_attn_prompt_workspace_bytes(int tokens, int tokens_k, int batch, int heads, int heads_kv, int head_dim) {
-  if (check_counts(tokens, batch, heads, heads_kv) || tokens_k < 0 || !tokens || !batch) return 0;
+  if (check_counts(tokens, batch, heads, heads_kv) || tokens_k < 0 || tokens_k > KEYS_MAX || !tokens || !batch) return 0;
   if (head_dim != 64 && head_dim != 128) return 0;
   const int group = heads / heads_kv, rt = qg::narrow_tiles(tokens, batch, group);
   if (rt) return narrow_bytes(batch, heads_kv, rt, head_dim);
@@ -172,7 +173,7 @@ int qgemv_attn_prompt(int dtype, int causal, int tokens, int tokens_k, int batch
   int rc = check_kind(dtype, head_dim);
   if (rc) return rc;
   if ((rc = check_counts(tokens, batch, heads, heads_kv))) return rc;
-  if (tokens_k < 0 || !launchable(tokens, batch, heads, heads_kv)) return QGEMV_ERR_SHAPE;
+  if (tokens_k < 0 || tokens_k > KEYS_MAX || !launchable(tokens, batch, heads, heads_kv)) return QGEMV_ERR_SHAPE;
   if ((rc = check_heads(*q, tokens, heads, head_dim, false)) || (rc = check_heads(*k, tokens_k, heads_kv, head_dim, false)) ||
       (rc = check_heads(*v, tokens_k, heads_kv, head_dim, false)) || (rc = check_heads(*o, tokens, heads, head_dim, true)))
     return rc;

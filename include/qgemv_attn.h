@@ -69,8 +69,8 @@ typedef struct {
  *
  * Checks, in order: null, dtype / head_dim (UNSUPPORTED), shape (counts not
  * negative, heads % heads_kv, tokens * heads < 2^31 and about
- * tokens * heads / 128 + batch * heads_kv < 2^21, strides, k's and v's token
- * strides < 2^26), scale, alignment,
+ * tokens * heads / 128 + batch * heads_kv < 2^21, tokens_k at most 2^31 - 1024,
+ * strides, k's and v's token strides < 2^26), scale, alignment,
  * o overlapping an input (VALUE), workspace.  o's elements must not overlap
  * each other (SHAPE).  tokens or batch of 0 does nothing.
  * ------------------------------------------------------------------------ */
@@ -89,7 +89,8 @@ int qgemv_attn_prompt(int dtype, int causal, int tokens, int tokens_k, int batch
  *     refs   [dev] int32 [pages] rows that hold the page; 0 = free
  *     status [dev] int32 [1]     QGEMV_KV_* bits that calls OR into it; the
  *                                caller clears and reads it when it likes
- * page_size is 16, 32, 64, 128 or 256 (UNSUPPORTED otherwise).  A new cache
+ * page_size is 16, 32, 64, 128 or 256 (UNSUPPORTED otherwise), and a row holds
+ * at most max_pages * page_size <= 2^31 - 1024 tokens (SHAPE).  A new cache
  * has tables -1 and lens, refs and status 0.  Pages are taken lowest number
  * first and counted on the device, so a decode loop needs no host in between.
  * Invariant kept by the calls below: a row's last page is shared with another
