@@ -71,6 +71,19 @@ bool launchable(int tokens, int rows, int heads, int heads_kv) {
   return (int64_t)qg::wide_tiles(tokens, rows, group, 4) * heads_kv < 1 << 21 && heads_kv < 65536;
 }
 
+// Whether the units of work that the device shares out (Walk) stay within its
+// sums, whatever the offsets say (each row may seem to have all tokens and all
+// keys): those of 64 rows in two sums of 32 bits (over units / 2^24), those of
+// all rows in 63.  Packed prompts in the wide kernel are not shared out so.
+bool countable(int tokens, int rows, int heads, int heads_kv, int64_t keys, bool paged) {
+  if (!tokens || !rows) return true;
+  const int rt = qg::narrow_tiles(tokens, rows, heads / heads_kv);
+  if (!rt && !paged) return true;
+  const double tiles = (double)tokens * heads / (rt ? 16 * rt : 128) + heads_kv;
+  const double units = tiles * ((double)keys / (rt ? 128 : 64) + 1);
+  return units < 0x1p50 && units * rows < 0x1p62;
+}
+
 size_t narrow_bytes(int rows, int heads_kv, int rt, int head_dim) {
   const size_t n = (size_t)qg::narrow_workgroups(rows, heads_kv);
   return qg::partial_bytes(2 * n, 16 * rt, head_dim) + 16 * n;  // (and two words per share for the tickets)
@@ -173,7 +186,9 @@ int qgemv_attn_prompt(int dtype, int causal, int tokens, int tokens_k, int batch
   int rc = check_kind(dtype, head_dim);
   if (rc) return rc;
   if ((rc = check_counts(tokens, batch, heads, heads_kv))) return rc;
-  if (tokens_k < 0 || tokens_k > KEYS_MAX || !launchable(tokens, batch, heads, heads_kv)) return QGEMV_ERR_SHAPE;
+  if (tokens_k < 0 || tokens_k > KEYS_MAX || !launchable(tokens, batch, heads, heads_kv) ||
+      !countable(tokens, batch, heads, heads_kv, tokens_k, false))
+    return QGEMV_ERR_SHAPE;
   if ((rc = check_heads(*q, tokens, heads, head_dim, false)) || (rc = check_heads(*k, tokens_k, heads_kv, head_dim, false)) ||
       (rc = check_heads(*v, tokens_k, heads_kv, head_dim, false)) || (rc = check_heads(*o, tokens, heads, head_dim, true)))
     return rc;
@@ -231,7 +246,9 @@ int qgemv_attn_tree(int dtype, const qgemv_kv_cache* c, int layer, int tokens, i
   if (rc) return rc;
   if ((rc = check_cache(c, false))) return rc;
   if ((rc = check_counts(tokens, c->rows, heads, c->heads_kv))) return rc;
-  if (!launchable(tokens, c->rows, heads, c->heads_kv)) return QGEMV_ERR_SHAPE;
+  if (!launchable(tokens, c->rows, heads, c->heads_kv) ||
+      !countable(tokens, c->rows, heads, c->heads_kv, (int64_t)c->max_pages * c->page_size, true))
+    return QGEMV_ERR_SHAPE;
   if (layer < 0 || layer >= c->layers || mask_words < 0 || mask_words > 1 << 20 || (mask != nullptr) != (mask_words > 0))
     return QGEMV_ERR_SHAPE;
   if ((rc = check_heads(*q, tokens, heads, c->head_dim, false)) || (rc = check_heads(*o, tokens, heads, c->head_dim, true)))

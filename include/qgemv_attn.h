@@ -70,6 +70,7 @@ typedef struct {
  * Checks, in order: null, dtype / head_dim (UNSUPPORTED), shape (counts not
  * negative, heads % heads_kv, tokens * heads < 2^31 and about
  * tokens * heads / 128 + batch * heads_kv < 2^21, tokens_k at most 2^31 - 1024,
+ * tokens * heads * tokens_k under about 2^61 and, times batch, 2^73,
  * strides, k's and v's token strides < 2^26), scale, alignment,
  * o overlapping an input (VALUE), workspace.  o's elements must not overlap
  * each other (SHAPE).  tokens or batch of 0 does nothing.
@@ -160,7 +161,8 @@ int qgemv_kv_compact(const qgemv_kv_cache *c, const int32_t *pos, const int32_t 
  *
  * A row with pos[b] < 0 has output 0.  Every position that a row sees must
  * have a page (kv_reserve sees to that; a missing one reads some other page of
- * the pool).  scale, tokens, o, ws as in qgemv_attn_prompt.
+ * the pool).  scale, tokens, o, ws and the checks as in qgemv_attn_prompt, with
+ * max_pages * page_size for tokens_k.
  * ------------------------------------------------------------------------ */
 size_t qgemv_attn_tree_workspace_bytes(int tokens, int rows, int heads, int heads_kv, int head_dim);
 int qgemv_attn_tree(int dtype, const qgemv_kv_cache *c, int layer, int tokens, int heads, float scale,
