@@ -3,12 +3,12 @@
 #include "qgemv_attn.h"
 
 #include <hip/hip_runtime.h>
+#include <unistd.h>
 
 #include <atomic>
 #include <chrono>
 #include <cmath>
 #include <cstdint>
-#include <random>
 
 #include "attn.hpp"
 #include "kernels.hpp"
@@ -91,11 +91,15 @@ size_t narrow_bytes(int rows, int heads_kv, int rt, int head_dim) {
 
 // A number of 48 bits for the tickets of one call's parts: counted up from a
 // random start, so that what an uninitialized workspace holds is not taken for
-// one; never 0.
+// one; never 0.  (getentropy reports an error where std::random_device throws;
+// then the clock and a stack address have to do.)
 uint64_t next_nonce() {
   static std::atomic<uint64_t> count{[] {
-    std::random_device r;
-    return (uint64_t)r() << 32 ^ r() ^ (uint64_t)std::chrono::steady_clock::now().time_since_epoch().count();
+    uint64_t r = 0;
+    if (getentropy(&r, sizeof r))
+      r = (uint64_t)std::chrono::steady_clock::now().time_since_epoch().count() * 0x9E3779B97F4A7C15u ^
+          reinterpret_cast<uintptr_t>(&r);
+    return r;
   }()};
   for (;;)
     if (const uint64_t n = count.fetch_add(1) & 0xFFFFFFFFFFFFu) return n;

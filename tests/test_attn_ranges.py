@@ -47,3 +47,15 @@ def test_work_that_64_bits_do_not_count(L):  # noqa: F811
                                   hk=heads(0, 0, 64, far(1)), hv=heads(0, 0, 64, far(2)))
     assert prompt_(KEYS_MAX) == q.ERR_SHAPE
     assert prompt_(1 << 20) == q.ERR_WORKSPACE
+
+
+def test_no_call_depends_on_a_source_of_randomness_that_throws(L):  # noqa: F811
+    """std::random_device throws where the system has no random numbers to give; nothing may leave a C entry that way."""
+    import shutil
+    import subprocess
+
+    nm = shutil.which("nm")
+    if nm is None:
+        pytest.skip("needs nm")
+    names = subprocess.run([nm, "-D", "--undefined-only", q.LIB_PATH], stdout=subprocess.PIPE, check=True, text=True).stdout
+    assert "random_device" not in names
