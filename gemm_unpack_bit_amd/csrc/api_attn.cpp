@@ -9,6 +9,7 @@
 #include <chrono>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "attn.hpp"
 #include "kernels.hpp"
@@ -21,7 +22,9 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 struct Span {
   uintptr_t begin, end;
 };
-bool overlap(const Span& a, const Span& b) { return a.begin < b.end && b.begin < a.end; }
+bool overlap(const Span& a, const Span& b) {
+  return a.begin < a.end && b.begin < b.end && a.begin < b.end && b.begin < a.end;
+}
 Span span(const void* p, int64_t bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(p);
   return {x, x + (bytes > 0 ? (uintptr_t)bytes : 0)};
@@ -147,6 +150,28 @@ qg::KvArgs cache_args(const qgemv_kv_cache& c) {
   return a;
 }
 
+Span pool_k(const qgemv_kv_cache& c) { return span(c.k, pool_bytes(c)); }
+Span pool_v(const qgemv_kv_cache& c) { return span(c.v, pool_bytes(c)); }
+Span tables_of(const qgemv_kv_cache& c) { return span(c.tables, (int64_t)4 * c.rows * c.max_pages); }
+Span lens_of(const qgemv_kv_cache& c) { return span(c.lens, c.lens ? (int64_t)4 * c.rows : 0); }
+Span refs_of(const qgemv_kv_cache& c) { return span(c.refs, c.refs ? (int64_t)4 * c.pages : 0); }
+Span status_of(const qgemv_kv_cache& c) { return span(c.status, c.status ? 4 : 0); }
+Span kv_scratch(int rows, int pages, const void* ws) {
+  return span(ws, ws ? (int64_t)qgemv_kv_workspace_bytes(rows, pages) : 0);
+}
+
+// cache calls: what one writes lies apart from all else that it writes, and
+// from what it reads
+bool apart(std::initializer_list<Span> writes, std::initializer_list<Span> reads) {
+  for (auto w = writes.begin(); w != writes.end(); ++w) {
+    for (auto x = writes.begin(); x != w; ++x)
+      if (overlap(*w, *x)) return false;
+    for (const Span& r : reads)
+      if (overlap(*w, r)) return false;
+  }
+  return true;
+}
+
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
 int scratch(int rows, int pages, void* ws, size_t ws_bytes, qg::KvScratch* w) {
@@ -159,7 +184,7 @@ int scratch(int rows, int pages, void* ws, size_t ws_bytes, qg::KvScratch* w) {
   return QGEMV_OK;
 }
 
-// attention: o against what the call reads and its workspace
+// attention: o against what the call reads (or the cache keeps) and its workspace
 bool writes_input(const Span& o, const Span& ws, const Span* in, int n) {
   for (int i = 0; i < n; ++i)
     if (overlap(o, in[i]) || overlap(ws, in[i])) return true;
@@ -262,10 +287,10 @@ int qgemv_attn_tree(int dtype, const qgemv_kv_cache* c, int layer, int tokens, i
     return QGEMV_ERR_ALIGN;
   const size_t need = qgemv_attn_tree_workspace_bytes(tokens, c->rows, heads, c->heads_kv, c->head_dim);
   const Span so = span(*o, tokens, heads, c->head_dim), sw = span(ws, need && ws ? (int64_t)need : 0);
-  const Span in[] = {span(*q, tokens, heads, c->head_dim), span(c->k, pool_bytes(*c)), span(c->v, pool_bytes(*c)),
-                     span(c->tables, (int64_t)4 * c->rows * c->max_pages), span(cu, 4 * ((int64_t)c->rows + 1)),
-                     span(pos, (int64_t)4 * c->rows), span(mask, (int64_t)8 * tokens * mask_words)};
-  if (writes_input(so, sw, in, 7)) return QGEMV_ERR_VALUE;
+  const Span in[] = {span(*q, tokens, heads, c->head_dim), pool_k(*c), pool_v(*c), tables_of(*c), lens_of(*c),
+                     refs_of(*c), status_of(*c), span(cu, 4 * ((int64_t)c->rows + 1)), span(pos, (int64_t)4 * c->rows),
+                     span(mask, (int64_t)8 * tokens * mask_words)};
+  if (writes_input(so, sw, in, 10)) return QGEMV_ERR_VALUE;
   if (need && (!ws || ws_bytes < need)) return QGEMV_ERR_WORKSPACE;
   if (need && !aligned(ws, 16)) return QGEMV_ERR_ALIGN;
   if (!tokens || !c->rows) return QGEMV_OK;
@@ -309,6 +334,10 @@ int qgemv_kv_reserve(const qgemv_kv_cache* c, const int32_t* cu, int32_t* pos, v
   if (rc) return rc;
   if (!cu || !pos) return QGEMV_ERR_NULL;
   if (!aligned(cu, 4) || !aligned(pos, 4)) return QGEMV_ERR_ALIGN;
+  if (!apart({span(pos, (int64_t)4 * c->rows), kv_scratch(c->rows, c->pages, ws), tables_of(*c), lens_of(*c), refs_of(*c),
+              status_of(*c)},
+             {span(cu, (int64_t)4 * (c->rows + 1)), pool_k(*c), pool_v(*c)}))
+    return QGEMV_ERR_VALUE;
   qg::KvScratch w;
   if ((rc = scratch(c->rows, c->pages, ws, ws_bytes, &w))) return rc;
   if (!c->rows) return QGEMV_OK;
@@ -325,9 +354,10 @@ int qgemv_kv_write(const qgemv_kv_cache* c, int layer, int tokens, const qgemv_h
       (rc = check_heads(*v, tokens, c->heads_kv, c->head_dim, false)))
     return rc;
   if (!aligned_heads(*k) || !aligned_heads(*v) || !aligned(cu, 4) || !aligned(pos, 4)) return QGEMV_ERR_ALIGN;
-  const Span pk = span(c->k, pool_bytes(*c)), pv = span(c->v, pool_bytes(*c));
-  const Span ik = span(*k, tokens, c->heads_kv, c->head_dim), iv = span(*v, tokens, c->heads_kv, c->head_dim);
-  if (overlap(pk, ik) || overlap(pk, iv) || overlap(pv, ik) || overlap(pv, iv)) return QGEMV_ERR_VALUE;
+  const Span in[] = {span(*k, tokens, c->heads_kv, c->head_dim), span(*v, tokens, c->heads_kv, c->head_dim), tables_of(*c),
+                     span(cu, 4 * ((int64_t)c->rows + 1)), span(pos, (int64_t)4 * c->rows)};
+  for (const Span& r : in)
+    if (overlap(pool_k(*c), r) || overlap(pool_v(*c), r)) return QGEMV_ERR_VALUE;
   if (!tokens || !c->rows) return QGEMV_OK;
   qg::KvWriteArgs a{cache_args(*c), layer, tokens, k->data, v->data, k->token, k->head, v->token, v->head, cu, pos};
   return qg::hip_status(qg::launch_kv_write(a, stream_of(stream)));
@@ -343,13 +373,14 @@ int qgemv_kv_fork(const qgemv_kv_cache* c, const int32_t* parents, const qgemv_k
       out->heads_kv != c->heads_kv || out->head_dim != c->head_dim || out->max_pages != c->max_pages)
     return QGEMV_ERR_SHAPE;
   if (!aligned(parents, 4)) return QGEMV_ERR_ALIGN;
-  const Span ct = span(c->tables, (int64_t)4 * c->rows * c->max_pages), cl = span(c->lens, (int64_t)4 * c->rows);
-  const Span ot = span(out->tables, (int64_t)4 * out->rows * out->max_pages), ol = span(out->lens, (int64_t)4 * out->rows);
-  if (out->k != c->k || out->v != c->v || out->refs != c->refs || out->status != c->status || overlap(ct, ot) ||
-      overlap(ct, ol) || overlap(cl, ot) || overlap(cl, ol))
+  const int rows = c->rows > out->rows ? c->rows : out->rows;
+  const Span sp = span(parents, (int64_t)4 * out->rows);
+  if (out->k != c->k || out->v != c->v || out->refs != c->refs || out->status != c->status ||
+      !apart({tables_of(*out), lens_of(*out), kv_scratch(rows, c->pages, ws), refs_of(*c), status_of(*c)},
+             {sp, tables_of(*c), lens_of(*c), pool_k(*c), pool_v(*c)}) ||
+      !apart({pool_k(*c)}, {sp, tables_of(*c), lens_of(*c)}) || !apart({pool_v(*c)}, {sp, tables_of(*c), lens_of(*c)}))
     return QGEMV_ERR_VALUE;
   qg::KvScratch w;
-  const int rows = c->rows > out->rows ? c->rows : out->rows;
   if ((rc = scratch(rows, c->pages, ws, ws_bytes, &w))) return rc;
   if (!rows) return QGEMV_OK;
   return qg::hip_status(qg::launch_kv_fork(cache_args(*c), parents, cache_args(*out), w, stream_of(stream)));
@@ -362,6 +393,12 @@ int qgemv_kv_compact(const qgemv_kv_cache* c, const int32_t* pos, const int32_t*
   if (!pos || !count || (max_keep > 0 && !keep)) return QGEMV_ERR_NULL;
   if (max_keep < 0) return QGEMV_ERR_SHAPE;
   if (!aligned(pos, 4) || !aligned(keep, 4) || !aligned(count, 4)) return QGEMV_ERR_ALIGN;
+  const Span sp = span(pos, (int64_t)4 * c->rows), sk = span(keep, (int64_t)4 * c->rows * max_keep),
+             sc = span(count, (int64_t)4 * c->rows), sw = kv_scratch(c->rows, c->pages, ws);
+  // (a row's length is written after its position and count are read: pos may be lens)
+  if (!apart({sw, tables_of(*c), refs_of(*c), status_of(*c)}, {sp, sk, sc, lens_of(*c), pool_k(*c), pool_v(*c)}) ||
+      !apart({pool_k(*c)}, {sp, sk, sc, lens_of(*c)}) || !apart({pool_v(*c)}, {sp, sk, sc, lens_of(*c)}))
+    return QGEMV_ERR_VALUE;
   qg::KvScratch w;
   if ((rc = scratch(c->rows, c->pages, ws, ws_bytes, &w))) return rc;
   if (!c->rows) return QGEMV_OK;

@@ -108,6 +108,10 @@ typedef struct {
 #define QGEMV_KV_BAD_INDEX 4  /* a parent, kept node or count outside its range     */
 #define QGEMV_KV_SHARED 8     /* kv_compact would write to a page another row holds */
 
+/* Every call: QGEMV_ERR_VALUE where something that it writes (its results, the
+ * workspace, the state above) overlaps something else that it writes or reads;
+ * kv_compact's pos, keep and count may lie in lens. */
+
 /* Scratch of kv_reserve, kv_fork and kv_compact: [dev], 16-byte aligned, no
  * initial contents.  rows: the larger of the caches' rows. */
 size_t qgemv_kv_workspace_bytes(int rows, int pages);

@@ -59,3 +59,57 @@ def test_no_call_depends_on_a_source_of_randomness_that_throws(L):  # noqa: F811
         pytest.skip("needs nm")
     names = subprocess.run([nm, "-D", "--undefined-only", q.LIB_PATH], stdout=subprocess.PIPE, check=True, text=True).stdout
     assert "random_device" not in names
+
+
+def test_what_a_cache_call_writes_is_apart_from_the_rest(L):  # noqa: F811
+    """Positions, the workspace and the cache's state: none inside another, and none inside what the call reads."""
+    import ctypes
+
+    b, VALUE = ctypes.byref, q.ERR_VALUE
+    at = {n: getattr(cache(), n) for n in ("k", "v", "tables", "lens", "refs", "status")}
+    state = [dict(tables=at["lens"]), dict(tables=at["refs"]), dict(lens=at["refs"] + 16), dict(status=at["lens"] + 8),
+             dict(refs=at["k"] + 64), dict(tables=at["v"] + 128)]
+    reserve = lambda c=None, cu=FAKE * 20, pos=FAKE * 21, ws=FAKE * 22: L.qgemv_kv_reserve(  # noqa: E731
+        b(c or cache()), v(cu), v(pos), v(ws), 1 << 20, v(0))
+    for s in state:
+        assert reserve(cache(**s)) == VALUE, s
+    for x in at.values():
+        assert reserve(pos=x) == VALUE and reserve(ws=x) == VALUE
+    for n in ("tables", "lens", "refs", "status"):
+        assert reserve(cu=at[n]) == VALUE
+    assert reserve(pos=FAKE * 20 + 12) == VALUE and reserve(ws=FAKE * 20) == VALUE and reserve(ws=FAKE * 21) == VALUE
+    other = dict(tables=FAKE * 30, lens=FAKE * 31)
+    fork = lambda c=None, o=None, p=FAKE * 20, ws=FAKE * 22: L.qgemv_kv_fork(  # noqa: E731
+        b(c or cache()), v(p), b(o or cache(**other)), v(ws), 1 << 20, v(0))
+    for s in state[2:4]:
+        assert fork(cache(**s), cache(**{**other, **s})) == VALUE, s
+    for x in list(at.values()) + [FAKE * 30, FAKE * 31]:
+        assert fork(ws=x) == VALUE
+        if x not in (at["tables"], at["lens"]):  # (these are only read)
+            assert fork(p=x) == VALUE
+    assert fork(ws=FAKE * 20) == VALUE
+    assert fork(o=cache(tables=FAKE * 30, lens=at["refs"])) == VALUE
+    assert fork(o=cache(tables=at["k"], lens=FAKE * 31)) == VALUE
+    assert fork(o=cache(tables=FAKE * 30, lens=FAKE * 30 + 16)) == VALUE
+    compact = lambda c=None, pos=FAKE * 20, keep=FAKE * 21, count=FAKE * 23, ws=FAKE * 22: L.qgemv_kv_compact(  # noqa: E731
+        b(c or cache()), v(pos), v(keep), 4, v(count), v(ws), 1 << 20, v(0))
+    for s in state:
+        assert compact(cache(**s)) == VALUE, s
+    for n, x in at.items():
+        assert compact(ws=x) == VALUE
+        if n != "lens":  # (a row's length is written when its position and count are read)
+            assert compact(pos=x) == VALUE and compact(count=x) == VALUE and compact(keep=x) == VALUE
+    for x in (FAKE * 20, FAKE * 21, FAKE * 23):
+        assert compact(ws=x) == VALUE
+    write = lambda c=None, cu=FAKE * 20, pos=FAKE * 21: L.qgemv_kv_write(  # noqa: E731
+        b(c or cache()), 1, 5, b(heads(1, 128)), b(heads(2, 128)), v(cu), v(pos), v(0))
+    for x in (at["k"], at["v"]):
+        assert write(cu=x) == VALUE and write(pos=x) == VALUE and write(cache(tables=x)) == VALUE
+    tree = lambda o=4, ws=FAKE * 60: L.qgemv_attn_tree(  # noqa: E731
+        0, b(cache()), 1, 5, 4, 0.1, b(heads(1)), v(FAKE * 20), v(FAKE * 21), v(0), 0, b(heads(o)), v(ws), 1 << 40, v(0))
+    for n in ("lens", "refs", "status"):
+        assert tree(o=at[n] // FAKE) == VALUE and tree(ws=at[n]) == VALUE
+
+
+def test_what_is_empty_overlaps_nothing(L):  # noqa: F811
+    assert prompt(L, tokens=0, ho=heads(0, data=FAKE * 2 + 128)) == q.OK  # no output, "inside" the keys
