@@ -36,6 +36,7 @@ Span span(const qgemv_heads& x, int tokens, int heads, int dim) {
 
 constexpr int64_t STRIDE_MAX = (int64_t)1 << 40;  // (products with 32-bit counts stay in 64 bits once checked)
 constexpr int64_t KEYS_MAX = ((int64_t)1 << 31) - 1024;  // (the kernels look a few steps past a row's last key, in 32 bits)
+constexpr int WRITE_MAX = (1 << 26) - 4;  // tokens of one kv_write: a wave each, launches stay under 2^32 threads
 constexpr int64_t KEY_STRIDE_MAX = (int64_t)1 << 26;  // 16 keys of a tile lie within 32-bit offsets of one another
 
 // strides in range and, for an output, no element shared
@@ -349,7 +350,7 @@ int qgemv_kv_write(const qgemv_kv_cache* c, int layer, int tokens, const qgemv_h
   int rc = check_cache(c, false);
   if (rc) return rc;
   if (!k || !v || !k->data || !v->data || !cu || !pos) return QGEMV_ERR_NULL;
-  if (layer < 0 || layer >= c->layers || tokens < 0 || tokens >= 1 << 26) return QGEMV_ERR_SHAPE;
+  if (layer < 0 || layer >= c->layers || tokens < 0 || tokens > WRITE_MAX) return QGEMV_ERR_SHAPE;
   if ((rc = check_heads(*k, tokens, c->heads_kv, c->head_dim, false)) ||
       (rc = check_heads(*v, tokens, c->heads_kv, c->head_dim, false)))
     return rc;

@@ -126,7 +126,8 @@ int qgemv_kv_reserve(const qgemv_kv_cache *c, const int32_t *cu, int32_t *pos, v
 
 /* Writes one layer's new keys and values: token cu[b] + i of k and v goes to
  * position pos[b] + i of row b (pos from kv_reserve; rows at -1 are skipped,
- * and tokens at a position without a page are too). */
+ * and tokens at a position without a page are too).  Up to 2^26 - 4 tokens
+ * (SHAPE otherwise). */
 int qgemv_kv_write(const qgemv_kv_cache *c, int layer, int tokens, const qgemv_heads *k, const qgemv_heads *v,
                    const int32_t *cu, const int32_t *pos, qgemv_stream_t stream);
 

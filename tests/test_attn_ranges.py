@@ -113,3 +113,12 @@ def test_what_a_cache_call_writes_is_apart_from_the_rest(L):  # noqa: F811
 
 def test_what_is_empty_overlaps_nothing(L):  # noqa: F811
     assert prompt(L, tokens=0, ho=heads(0, data=FAKE * 2 + 128)) == q.OK  # no output, "inside" the keys
+
+
+def test_a_write_of_more_tokens_than_a_launch_has_waves(L):  # noqa: F811
+    import ctypes
+
+    b, c = ctypes.byref, cache(rows=1)
+    write = lambda n: L.qgemv_kv_write(b(c), 1, n, b(heads(1, 0)), b(heads(2, 0)), v(FAKE * 20), v(FAKE * 21), v(0))  # noqa: E731
+    most = (1 << 26) - 4  # (a wave a token, under 2^32 threads)
+    assert write(most + 1) == q.ERR_SHAPE and write((1 << 31) - 1) == q.ERR_SHAPE
