@@ -39,6 +39,12 @@ constexpr int64_t KEYS_MAX = ((int64_t)1 << 31) - 1024;  // (the kernels look a 
 constexpr int WRITE_MAX = (1 << 26) - 4;  // tokens of one kv_write: a wave each, launches stay under 2^32 threads
 constexpr int64_t KEY_STRIDE_MAX = (int64_t)1 << 26;  // 16 keys of a tile lie within 32-bit offsets of one another
 
+// the array with the strides that lead anywhere (that of a single token or head
+// may be anything: a view's of a padded row, say)
+qgemv_heads used(const qgemv_heads& x, int tokens, int heads) {
+  return {x.data, tokens > 1 ? x.token : 0, heads > 1 ? x.head : 0};
+}
+
 // strides in range and, for an output, no element shared
 int check_heads(const qgemv_heads& x, int tokens, int heads, int dim, bool output) {
   if (x.token < 0 || x.head < 0 || x.token > STRIDE_MAX || x.head > STRIDE_MAX) return QGEMV_ERR_SHAPE;
@@ -209,28 +215,30 @@ size_t qgemv_attn_prompt_workspace_bytes(int tokens, int tokens_k, int batch, in
 }
 
 int qgemv_attn_prompt(int dtype, int causal, int tokens, int tokens_k, int batch, int heads, int heads_kv,
-                      int head_dim, float scale, const qgemv_heads* q, const qgemv_heads* k, const qgemv_heads* v,
-                      const int32_t* cu_q, const int32_t* cu_k, const qgemv_heads* o, void* ws, size_t ws_bytes,
+                      int head_dim, float scale, const qgemv_heads* q_, const qgemv_heads* k_, const qgemv_heads* v_,
+                      const int32_t* cu_q, const int32_t* cu_k, const qgemv_heads* o_, void* ws, size_t ws_bytes,
                       qgemv_stream_t stream) {
-  if (!q || !k || !v || !o || !cu_q || !cu_k || !q->data || !k->data || !v->data || !o->data) return QGEMV_ERR_NULL;
+  if (!q_ || !k_ || !v_ || !o_ || !cu_q || !cu_k || !q_->data || !k_->data || !v_->data || !o_->data) return QGEMV_ERR_NULL;
   int rc = check_kind(dtype, head_dim);
   if (rc) return rc;
   if ((rc = check_counts(tokens, batch, heads, heads_kv))) return rc;
   if (tokens_k < 0 || tokens_k > KEYS_MAX || !launchable(tokens, batch, heads, heads_kv) ||
       !countable(tokens, batch, heads, heads_kv, tokens_k, false))
     return QGEMV_ERR_SHAPE;
-  if ((rc = check_heads(*q, tokens, heads, head_dim, false)) || (rc = check_heads(*k, tokens_k, heads_kv, head_dim, false)) ||
-      (rc = check_heads(*v, tokens_k, heads_kv, head_dim, false)) || (rc = check_heads(*o, tokens, heads, head_dim, true)))
+  const qgemv_heads q = used(*q_, tokens, heads), k = used(*k_, tokens_k, heads_kv), v = used(*v_, tokens_k, heads_kv),
+                    o = used(*o_, tokens, heads);
+  if ((rc = check_heads(q, tokens, heads, head_dim, false)) || (rc = check_heads(k, tokens_k, heads_kv, head_dim, false)) ||
+      (rc = check_heads(v, tokens_k, heads_kv, head_dim, false)) || (rc = check_heads(o, tokens, heads, head_dim, true)))
     return rc;
-  if (k->token >= KEY_STRIDE_MAX || v->token >= KEY_STRIDE_MAX) return QGEMV_ERR_SHAPE;
+  if (k.token >= KEY_STRIDE_MAX || v.token >= KEY_STRIDE_MAX) return QGEMV_ERR_SHAPE;
   if ((rc = check_scale(scale))) return rc;
-  if (!aligned_heads(*q) || !aligned_heads(*k) || !aligned_heads(*v) || !aligned_heads(*o) || !aligned(cu_q, 4) ||
+  if (!aligned_heads(q) || !aligned_heads(k) || !aligned_heads(v) || !aligned_heads(o) || !aligned(cu_q, 4) ||
       !aligned(cu_k, 4))
     return QGEMV_ERR_ALIGN;
   const size_t need = qgemv_attn_prompt_workspace_bytes(tokens, tokens_k, batch, heads, heads_kv, head_dim);
-  const Span so = span(*o, tokens, heads, head_dim), sw = span(ws, need && ws ? (int64_t)need : 0);
-  const Span in[] = {span(*q, tokens, heads, head_dim), span(*k, tokens_k, heads_kv, head_dim),
-                     span(*v, tokens_k, heads_kv, head_dim), span(cu_q, 4 * ((int64_t)batch + 1)),
+  const Span so = span(o, tokens, heads, head_dim), sw = span(ws, need && ws ? (int64_t)need : 0);
+  const Span in[] = {span(q, tokens, heads, head_dim), span(k, tokens_k, heads_kv, head_dim),
+                     span(v, tokens_k, heads_kv, head_dim), span(cu_q, 4 * ((int64_t)batch + 1)),
                      span(cu_k, 4 * ((int64_t)batch + 1))};
   if (writes_input(so, sw, in, 5)) return QGEMV_ERR_VALUE;
   if (need && (!ws || ws_bytes < need)) return QGEMV_ERR_WORKSPACE;
@@ -246,10 +254,10 @@ int qgemv_attn_prompt(int dtype, int causal, int tokens, int tokens_k, int batch
   a.rows = batch;
   a.causal = causal != 0;
   a.scale = scale * 1.4426950408889634f;
-  a.q = q->data, a.q_token = q->token, a.q_head = q->head;
-  a.k = k->data, a.k_token = k->token, a.k_head = k->head;
-  a.v = v->data, a.v_token = v->token, a.v_head = v->head;
-  a.o = o->data, a.o_token = o->token, a.o_head = o->head;
+  a.q = q.data, a.q_token = q.token, a.q_head = q.head;
+  a.k = k.data, a.k_token = k.token, a.k_head = k.head;
+  a.v = v.data, a.v_token = v.token, a.v_head = v.head;
+  a.o = o.data, a.o_token = o.token, a.o_head = o.head;
   a.cu = cu_q;
   a.cu_k = cu_k;
   a.tokens_k = tokens_k;
@@ -269,9 +277,9 @@ size_t qgemv_attn_tree_workspace_bytes(int tokens, int rows, int heads, int head
 }
 
 int qgemv_attn_tree(int dtype, const qgemv_kv_cache* c, int layer, int tokens, int heads, float scale,
-                    const qgemv_heads* q, const int32_t* cu, const int32_t* pos, const uint64_t* mask,
-                    int mask_words, const qgemv_heads* o, void* ws, size_t ws_bytes, qgemv_stream_t stream) {
-  if (!c || !c->k || !c->v || !c->tables || !q || !q->data || !o || !o->data || !cu || !pos) return QGEMV_ERR_NULL;
+                    const qgemv_heads* q_, const int32_t* cu, const int32_t* pos, const uint64_t* mask,
+                    int mask_words, const qgemv_heads* o_, void* ws, size_t ws_bytes, qgemv_stream_t stream) {
+  if (!c || !c->k || !c->v || !c->tables || !q_ || !q_->data || !o_ || !o_->data || !cu || !pos) return QGEMV_ERR_NULL;
   int rc = check_kind(dtype, c->head_dim);
   if (rc) return rc;
   if ((rc = check_cache(c, false))) return rc;
@@ -281,14 +289,15 @@ int qgemv_attn_tree(int dtype, const qgemv_kv_cache* c, int layer, int tokens, i
     return QGEMV_ERR_SHAPE;
   if (layer < 0 || layer >= c->layers || mask_words < 0 || mask_words > 1 << 20 || (mask != nullptr) != (mask_words > 0))
     return QGEMV_ERR_SHAPE;
-  if ((rc = check_heads(*q, tokens, heads, c->head_dim, false)) || (rc = check_heads(*o, tokens, heads, c->head_dim, true)))
+  const qgemv_heads q = used(*q_, tokens, heads), o = used(*o_, tokens, heads);
+  if ((rc = check_heads(q, tokens, heads, c->head_dim, false)) || (rc = check_heads(o, tokens, heads, c->head_dim, true)))
     return rc;
   if ((rc = check_scale(scale))) return rc;
-  if (!aligned_heads(*q) || !aligned_heads(*o) || !aligned(cu, 4) || !aligned(pos, 4) || !aligned(mask, 8))
+  if (!aligned_heads(q) || !aligned_heads(o) || !aligned(cu, 4) || !aligned(pos, 4) || !aligned(mask, 8))
     return QGEMV_ERR_ALIGN;
   const size_t need = qgemv_attn_tree_workspace_bytes(tokens, c->rows, heads, c->heads_kv, c->head_dim);
-  const Span so = span(*o, tokens, heads, c->head_dim), sw = span(ws, need && ws ? (int64_t)need : 0);
-  const Span in[] = {span(*q, tokens, heads, c->head_dim), pool_k(*c), pool_v(*c), tables_of(*c), lens_of(*c),
+  const Span so = span(o, tokens, heads, c->head_dim), sw = span(ws, need && ws ? (int64_t)need : 0);
+  const Span in[] = {span(q, tokens, heads, c->head_dim), pool_k(*c), pool_v(*c), tables_of(*c), lens_of(*c),
                      refs_of(*c), status_of(*c), span(cu, 4 * ((int64_t)c->rows + 1)), span(pos, (int64_t)4 * c->rows),
                      span(mask, (int64_t)8 * tokens * mask_words)};
   if (writes_input(so, sw, in, 10)) return QGEMV_ERR_VALUE;
@@ -306,10 +315,10 @@ int qgemv_attn_tree(int dtype, const qgemv_kv_cache* c, int layer, int tokens, i
   a.causal = 1;
   a.scale = scale * 1.4426950408889634f;
   const int64_t row = (int64_t)c->heads_kv * c->head_dim, in_layer = (int64_t)c->pages * c->page_size * row;
-  a.q = q->data, a.q_token = q->token, a.q_head = q->head;
+  a.q = q.data, a.q_token = q.token, a.q_head = q.head;
   a.k = c->k + layer * in_layer, a.k_token = row, a.k_head = c->head_dim;
   a.v = c->v + layer * in_layer, a.v_token = row, a.v_head = c->head_dim;
-  a.o = o->data, a.o_token = o->token, a.o_head = o->head;
+  a.o = o.data, a.o_token = o.token, a.o_head = o.head;
   a.cu = cu;
   a.tables = c->tables;
   a.pos = pos;
@@ -345,22 +354,23 @@ int qgemv_kv_reserve(const qgemv_kv_cache* c, const int32_t* cu, int32_t* pos, v
   return qg::hip_status(qg::launch_kv_reserve(cache_args(*c), cu, pos, w, stream_of(stream)));
 }
 
-int qgemv_kv_write(const qgemv_kv_cache* c, int layer, int tokens, const qgemv_heads* k, const qgemv_heads* v,
+int qgemv_kv_write(const qgemv_kv_cache* c, int layer, int tokens, const qgemv_heads* k_, const qgemv_heads* v_,
                    const int32_t* cu, const int32_t* pos, qgemv_stream_t stream) {
   int rc = check_cache(c, false);
   if (rc) return rc;
-  if (!k || !v || !k->data || !v->data || !cu || !pos) return QGEMV_ERR_NULL;
+  if (!k_ || !v_ || !k_->data || !v_->data || !cu || !pos) return QGEMV_ERR_NULL;
   if (layer < 0 || layer >= c->layers || tokens < 0 || tokens > WRITE_MAX) return QGEMV_ERR_SHAPE;
-  if ((rc = check_heads(*k, tokens, c->heads_kv, c->head_dim, false)) ||
-      (rc = check_heads(*v, tokens, c->heads_kv, c->head_dim, false)))
+  const qgemv_heads k = used(*k_, tokens, c->heads_kv), v = used(*v_, tokens, c->heads_kv);
+  if ((rc = check_heads(k, tokens, c->heads_kv, c->head_dim, false)) ||
+      (rc = check_heads(v, tokens, c->heads_kv, c->head_dim, false)))
     return rc;
-  if (!aligned_heads(*k) || !aligned_heads(*v) || !aligned(cu, 4) || !aligned(pos, 4)) return QGEMV_ERR_ALIGN;
-  const Span in[] = {span(*k, tokens, c->heads_kv, c->head_dim), span(*v, tokens, c->heads_kv, c->head_dim), tables_of(*c),
+  if (!aligned_heads(k) || !aligned_heads(v) || !aligned(cu, 4) || !aligned(pos, 4)) return QGEMV_ERR_ALIGN;
+  const Span in[] = {span(k, tokens, c->heads_kv, c->head_dim), span(v, tokens, c->heads_kv, c->head_dim), tables_of(*c),
                      span(cu, 4 * ((int64_t)c->rows + 1)), span(pos, (int64_t)4 * c->rows)};
   for (const Span& r : in)
     if (overlap(pool_k(*c), r) || overlap(pool_v(*c), r)) return QGEMV_ERR_VALUE;
   if (!tokens || !c->rows) return QGEMV_OK;
-  qg::KvWriteArgs a{cache_args(*c), layer, tokens, k->data, v->data, k->token, k->head, v->token, v->head, cu, pos};
+  qg::KvWriteArgs a{cache_args(*c), layer, tokens, k.data, v.data, k.token, k.head, v.token, v.head, cu, pos};
   return qg::hip_status(qg::launch_kv_write(a, stream_of(stream)));
 }
 

@@ -42,8 +42,8 @@ typedef enum { QGEMV_F16 = 0, QGEMV_BF16 = 1 } qgemv_dtype;
 /* A [tokens, heads, head_dim] array whose last dimension is contiguous:
  * element (t, h, d) is data[t * token + h * head + d].  data is 16-byte
  * aligned and the strides, in elements, are multiples of 8 (QGEMV_ERR_ALIGN),
- * and not negative (QGEMV_ERR_SHAPE).  So the parts of a fused QKV product are
- * read in place. */
+ * and not negative (QGEMV_ERR_SHAPE); the stride of a dimension of one is not
+ * looked at.  So the parts of a fused QKV product are read in place. */
 typedef struct {
   uint16_t *data;
   int64_t token, head;

@@ -122,3 +122,23 @@ def test_a_write_of_more_tokens_than_a_launch_has_waves(L):  # noqa: F811
     write = lambda n: L.qgemv_kv_write(b(c), 1, n, b(heads(1, 0)), b(heads(2, 0)), v(FAKE * 20), v(FAKE * 21), v(0))  # noqa: E731
     most = (1 << 26) - 4  # (a wave a token, under 2^32 threads)
     assert write(most + 1) == q.ERR_SHAPE and write((1 << 31) - 1) == q.ERR_SHAPE
+
+
+def test_strides_of_single_tokens_and_heads_do_not_count(L):  # noqa: F811
+    """One token of a padded row, one head of a wider array: the stride of a dimension of one leads nowhere."""
+    import ctypes
+
+    b = ctypes.byref
+    h = lambda at, token, head: heads(at, token, head)  # noqa: E731
+    for token in (260, -8, 1 << 60, 1 << 27):
+        one = dict(tokens=1, tokens_k=1, batch=1, wsb=0, hq=h(1, token, 64), hk=h(2, token, 64), hv=h(3, token, 64), ho=h(4, token, 64))
+        assert prompt(L, **one) == q.ERR_WORKSPACE, token  # (every check before the workspace's is passed)
+        one = dict(tokens=9, tokens_k=9, nh=1, kv=1, batch=1, wsb=0, hq=h(1, 64, token), hk=h(2, 64, token), hv=h(3, 64, token),
+                   ho=h(4, 64, token))
+        assert prompt(L, **one) == q.ERR_WORKSPACE, token
+        c = cache(rows=0)
+        assert L.qgemv_attn_tree(0, b(c), 0, 1, 4, 0.1, b(h(1, token, 64)), v(FAKE * 20), v(FAKE * 21), v(0), 0, b(h(4, token, 64)),
+                                 v(0), 0, v(0)) == q.OK
+        assert L.qgemv_kv_write(b(c), 0, 1, b(h(1, token, 64)), b(h(2, token, 64)), v(FAKE * 20), v(FAKE * 21), v(0)) == q.OK
+    assert prompt(L, tokens=2, tokens_k=2, hq=h(1, 260, 64)) == q.ERR_ALIGN
+    assert prompt(L, tokens=2, tokens_k=2, hk=h(2, 256, -8)) == q.ERR_SHAPE
