@@ -57,6 +57,10 @@ __device__ __forceinline__ uint32_t nonfinite(uint32_t w) {  // bits 15 and 31: 
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 constexpr float NEG_INF = -__builtin_inff();
+// Whether scores are multiplied by 0 (the same in the whole wave).  A score of
+// -inf then is NaN, but would be taken for an unseen key's; so the kernels put
+// score - score in its place: 0, or NaN where it is not finite.
+__device__ __forceinline__ bool zero_scale(float scale) { return (__float_as_uint(scale) & 0x7FFFFFFFu) == 0; }
 
 // max and sum over the lanes l, l ^ 32
 __device__ __forceinline__ float half_max(float v) {

@@ -272,6 +272,9 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
       if constexpr (decltype(more)::value) load_k(kb + 32 * WAVES, tok1);
       __builtin_amdgcn_sched_barrier(0);
 
+      if (zero_scale(a.scale))
+#pragma unroll
+        for (int i = 0; i < RT; ++i) sc[i][0] -= sc[i][0], sc[i][1] -= sc[i][1];
       const bool masked = kb + 32 > common;
       uint64_t odd = 0;  // keys of the step with a value that is not finite (masked steps)
       if (masked) {

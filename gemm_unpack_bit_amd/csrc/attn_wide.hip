@@ -341,6 +341,7 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
     uint64_t odd = 0;
     if (masked) odd = odd_keys(v_now);
     if (active) {
+      if (zero_scale(scale)) sc[0] -= sc[0], sc[1] -= sc[1];
       if (masked) {
         const AttnArgs a = args_again();
         const uint64_t seen = sight.window(a, r, kb) >> (4 * half);
