@@ -26,7 +26,9 @@
  * row b holds tokens cu[b] .. cu[b + 1] - 1 (none where they are equal).
  *
  * What a masked or missing key holds (also infinities and NaN) does not reach
- * the output, and a query that sees no key has output 0.
+ * the output, and a query that sees no key has output 0.  A seen key whose
+ * score is -inf has no weight (where scale is not 0), and a query all of whose
+ * scores are -inf has output 0 too.
  */
 #ifndef QGEMV_ATTN_H
 #define QGEMV_ATTN_H

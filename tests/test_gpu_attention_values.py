@@ -5,7 +5,7 @@ import pytest
 
 from tests.attn_ref import attend, f64
 from tests.gpu_util import say, torch
-from tests.test_gpu_attention import _cache, _cu, _dt, _gen, _rand
+from tests.test_gpu_attention import _cache, _cu, _dt, _gen, _rand, _words
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +52,84 @@ def test_a_scale_of_zero_over_the_cache(dtype, n):
     at = 9  # a cached one: the others
     cache.k[0, int(tables[0, at // 16]), at % 16, 0, 0] = float("-inf")
     assert np.isnan(f64(q_.attn_tree(q, cache, 0, _cu([n]), p, scale=0.0))[:, :2]).all()
+
+
+def _check_kinds(out, q, k, v, seen_of, group, scale, what):
+    o, qd, kd, vd = f64(out), f64(q), f64(k), f64(v)
+    for i in range(q.shape[0]):
+        for h in range(q.shape[1]):
+            with np.errstate(all="ignore"):
+                want = attend(qd[i, h], kd[:, h // group], vd[:, h // group], seen_of(i), scale)[0]
+            bad = _kinds(want) != _kinds(o[i, h])
+            assert not bad.any(), f"{what}: query {i} head {h}: {o[i, h][bad][:4]} for {want[bad][:4]}"
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,m", [(6, 6), (6, 300), (200, 200), (60, 2500)])  # narrow, wide, wide with split keys
+@pytest.mark.parametrize("causal", [True, False])
+def test_infinities_and_nan_each_in_their_place(dtype, D, n, m, causal):
+    """Values of +inf, -inf and NaN show in the queries that see them, in their column and with their sign; +inf and -inf
+    together are NaN; keys of NaN, and scores of +inf, make every column NaN."""
+    say("attn_prompt kinds", dtype, D, n, m, causal)
+    rng, g, dt = np.random.default_rng(n + m), _gen(n + m), _dt(dtype)
+    q = _rand(g, n, 2, D, dtype=dt, scale=0.5)
+    k, v = _rand(g, m, 1, D, dtype=dt), _rand(g, m, 1, D, dtype=dt)
+    inf = float("inf")
+    for at, d, x in ((0, 1, inf), (m // 3, 2, -inf), (m // 2, 3, float("nan")), (m - 1, 4, inf), (m // 2, 5, inf), (m - 2, 5, -inf),
+                     (m - n // 2, 6, -inf), (m // 4, D - 1, -inf)):
+        v[at, 0, d] = x
+    seen = lambda i: np.arange(m) <= i + m - n if causal else np.ones(m, bool)  # noqa: E731
+    out = q_.attn_prompt(q, k, v, _cu([n]), _cu([m]), causal=causal)
+    _check_kinds(out, q, k, v, seen, 2, D ** -0.5, f"values {n} {m}")
+    q.abs_()
+    for x in (inf, float("nan")):
+        k2 = k.clone()
+        k2[m - n // 2 - 1, 0, 0] = x
+        out = q_.attn_prompt(q, k2, v, _cu([n]), _cu([m]), causal=causal)
+        _check_kinds(out, q, k2, v, seen, 2, D ** -0.5, f"key {x} {n} {m}")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads,n", [(2, 7), (4, 7), (4, 33), (8, 33)])  # narrow (one and two tiles of rows), wide (4 and 8 waves)
+def test_trees_with_infinities_and_nan(dtype, D, heads, n):
+    say("attn_tree kinds", dtype, D, heads, n)
+    rng, dt, pos = np.random.default_rng(n), _dt(dtype), 131
+    cache, tables = _cache(n, dt, [pos + n], 16, 1, D, fill=float("nan"))
+    at = lambda p: (0, int(tables[0, p // 16]), p % 16, 0)  # noqa: E731
+    inf = float("inf")
+    for p, d, x in ((0, 1, inf), (60, 2, -inf), (130, 3, float("nan")), (pos, 4, -inf), (pos + 2, 5, inf), (pos + 3, 5, -inf),
+                    (pos + n - 1, 6, float("nan")), (pos + 1, D - 1, inf)):
+        cache.v[at(p)][d] = x
+    bits = [sorted(rng.choice(n, rng.integers(0, n), replace=False).tolist()) for _ in range(n)]
+    q = _rand(_gen(n), n, heads, D, dtype=dt, scale=0.5)
+    t = torch()
+    out = q_.attn_tree(q, cache, 0, _cu([n]), t.tensor([pos], dtype=t.int32, device="cuda"), _words(bits, 1))
+    k = t.stack([cache.k[at(p)] for p in range(pos + n)])[:, None]
+    v = t.stack([cache.v[at(p)] for p in range(pos + n)])[:, None]
+
+    def seen(i):
+        s = np.arange(pos + n) < pos
+        s[[pos + j for j in bits[i]]] = True
+        return s
+
+    _check_kinds(out, q, k, v, seen, heads, D ** -0.5, f"tree {n}")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("n", [4, 150])
+def test_scores_of_minus_infinity_weigh_nothing(dtype, n):
+    """A seen key whose score is -inf has no weight; a query all of whose scores are has output 0, like one without keys."""
+    t = torch()
+    say("attn_prompt scores of -inf", dtype, n)
+    g, dt = _gen(n), _dt(dtype)
+    q, v = t.ones(n, 2, 64, dtype=dt, device="cuda"), _rand(g, n, 2, 64, dtype=dt)
+    k = _rand(g, n, 2, 64, dtype=dt)
+    k[:n // 2, :, 9] = float("-inf")
+    out = f64(q_.attn_prompt(q, k, v, _cu([n])))
+    assert (out[:n // 2] == 0).all()
+    kd, vd = f64(k), f64(v)
+    for i in range(n // 2, n):
+        want = attend(np.ones(64), kd[n // 2:i + 1, 1], vd[n // 2:i + 1, 1], np.ones(i + 1 - n // 2, bool), 0.125)[0]
+        assert np.abs(out[i, 1] - want).max() < 2.0 ** -6 * np.abs(vd).max()  # (rounding is tested elsewhere)
