@@ -69,8 +69,11 @@ struct AttnArgs {
 // Waves per SIMD that the kernels' registers allow, and the workgroups (of one
 // wave per SIMD) that then fill the 256 compute units: the split of a tree's
 // keys is over that many.
-// (The narrow kernel's parts of an item are joined by one workgroup: at most
-// 256 of them.)
+// (The narrow kernel's parts of an item are joined by one workgroup.  Where all
+// are parts of one item, half the workgroups leave half of them: one query head
+// on 131072 keys 21 us with 256, 26 with 512, eight heads 33.5 with either.  Of
+// two items one may still have nearly all parts: a row of 300000 keys beside one
+// of a single key 38 us, alone 34.)
 inline int narrow_workgroups(int rows, int heads_kv) { return (int64_t)rows * heads_kv < 2 ? 256 : 512; }
 // (waves: per workgroup, 4 or 8; of 8, one workgroup fits a compute unit)
 constexpr int wide_waves(int head_dim, int waves) { return head_dim == 64 && waves == 4 ? 3 : 2; }
@@ -79,7 +82,10 @@ constexpr int PROMPT_WAVES = 4;
 constexpr size_t partial_bytes(size_t slots, int bm, int d) { return slots * bm * (size_t)(d + 2) * 4; }
 
 // 16-row tiles a wave of the narrow kernel holds (1 or 2) for the average
-// row's queries, or 0: the wide kernel
+// row's queries, or 0: the wide kernel.  Both sides at 16 query rows a key head
+// (one tile, two tiles): 16 rows of 4000 keys and 8 key heads 48 and 55 us, one
+// row of them 13.5 and 17; at 32 (two tiles, wide kernel): 58 and 58, one row 22
+// and 40, 16 rows of 1000 to 8200 keys 59 and 55.
 inline int narrow_tiles(int tokens, int rows, int group) {
   const int64_t avg = ((int64_t)tokens + rows - 1) / rows * group;
   return avg <= 16 ? 1 : avg <= 32 ? 2 : 0;
