@@ -62,6 +62,21 @@ constexpr float NEG_INF = -__builtin_inff();
 // score - score in its place: 0, or NaN where it is not finite.
 __device__ __forceinline__ bool zero_scale(float scale) { return (__float_as_uint(scale) & 0x7FFFFFFFu) == 0; }
 
+// Weights are 2^(x * scale - m), one fused operation a score; their reference m
+// is a rounded product.  From 2^16 on its rounding counts (from 2^24 a score may
+// lie whole powers of two off its own reference, which made weights overflow or
+// vanish), so there the product of every score is rounded likewise and m taken
+// off behind it: the largest score's weight is exact, and the others' errors are
+// those of the product.  (m of -inf or +inf: no.)
+__device__ __forceinline__ bool far(float m) {
+  return (__float_as_uint(m) & 0x7FFFFFFFu) - 0x47800000u < 0x7F800000u - 0x47800000u;
+}
+__device__ __forceinline__ float far_score(float x, float scale, float m) {
+#pragma clang fp contract(off)
+  const float product = x * scale;
+  return product - m;
+}
+
 // max and sum over the lanes l, l ^ 32
 __device__ __forceinline__ float half_max(float v) {
   const uint32_t u = __float_as_uint(v);

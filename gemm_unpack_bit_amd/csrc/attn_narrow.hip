@@ -311,23 +311,32 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
 
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        const f4 s0 = sc[i][0], s1 = sc[i][1];
+        f4 s0 = sc[i][0], s1 = sc[i][1];
         float mx = fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])), fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3])));
         mx = quarter_max(mx);
         mx = mx == NEG_INF ? NEG_INF : mx * a.scale;
-        if (__any(mx > m[i] + E::SLACK)) {
+        float by = a.scale, ref = m[i];
+        if (__any(mx > m[i] + E::SLACK || far(m[i]))) {
           const float mn = fmaxf(m[i], mx), w = mn == NEG_INF ? 1.f : exp2_(m[i] - mn);
-          m[i] = mn;
+          m[i] = ref = mn;
           l[i] *= w;
 #pragma unroll
           for (int j = 0; j < DL; ++j) o[i][j] *= w;
+          if (__any(far(mn))) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              s0[e] = far_score(s0[e], a.scale, mn == NEG_INF ? 0.f : mn);
+              s1[e] = far_score(s1[e], a.scale, mn == NEG_INF ? 0.f : mn);
+            }
+            by = 1.f, ref = 0.f;
+          }
         }
-        const float base = m[i] == NEG_INF ? 0.f : m[i] - E::LIFT;
+        const float base = ref == NEG_INF ? 0.f : ref - E::LIFT;
         float p[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float x = e < 4 ? s0[e & 3] : s1[e & 3];
-          p[e] = x == NEG_INF ? 0.f : exp2_(fmaf(x, a.scale, -base));
+          p[e] = x == NEG_INF ? 0.f : exp2_(fmaf(x, by, -base));
           l[i] += p[e];
         }
         const u4 pf = u4{E::pack(p[0], p[1]), E::pack(p[2], p[3]), E::pack(p[4], p[5]), E::pack(p[6], p[7])};

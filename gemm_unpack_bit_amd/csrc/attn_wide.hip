@@ -207,21 +207,29 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[x][i]);
     mx = half_max(mx);
     mx = mx == NEG_INF ? NEG_INF : mx * scale;
-    if (__any(mx > m + E::SLACK)) {
+    float by = scale, ref = m;
+    if (__any(mx > m + E::SLACK || far(m))) {
       const float mn = fmaxf(m, mx), w = mn == NEG_INF ? 1.f : exp2_(m - mn);
-      m = mn;
+      m = ref = mn;
       l *= w;
 #pragma unroll
       for (int i = 0; i < DB; ++i) o[i] *= w;
+      if (__any(far(m))) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sc[x][i] = far_score(sc[x][i], scale, m == NEG_INF ? 0.f : m);
+        by = 1.f, ref = 0.f;
+      }
     }
-    const float base = m == NEG_INF ? 0.f : m - E::LIFT;
+    const float base = ref == NEG_INF ? 0.f : ref - E::LIFT;
 #pragma unroll
     for (int k4 = 0; k4 < 4; ++k4) {
       const int x = k4 >> 1, e = 8 * (k4 & 1);
       float p[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        p[i] = exp2_(fmaf(sc[x][e + i], scale, -base));
+        p[i] = exp2_(fmaf(sc[x][e + i], by, -base));
         if constexpr (decltype(some)::value) p[i] = sc[x][e + i] == NEG_INF ? 0.f : p[i];
         l += p[i];
       }

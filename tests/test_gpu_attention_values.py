@@ -133,3 +133,55 @@ def test_scores_of_minus_infinity_weigh_nothing(dtype, n):
     for i in range(n // 2, n):
         want = attend(np.ones(64), kd[n // 2:i + 1, 1], vd[n // 2:i + 1, 1], np.ones(i + 1 - n // 2, bool), 0.125)[0]
         assert np.abs(out[i, 1] - want).max() < 2.0 ** -6 * np.abs(vd).max()  # (rounding is tested elsewhere)
+
+
+LARGE = [("f16", 300.0), ("f16", 1500.0), ("f16", 3000.0), ("f16", 5000.0), ("f16", 12000.0), ("bf16", 1e3), ("bf16", 1e5), ("bf16", 1e9),
+         ("bf16", 1e15)]
+
+
+def _check_largest(out, q, k, v, seen_of, group, what):
+    """Where a query's largest score is far above the others, its output is that key's value."""
+    o, qd, kd, vd = f64(out), f64(q), f64(k), f64(v)
+    checked = 0
+    for i in range(q.shape[0]):
+        seen = np.flatnonzero(seen_of(i))
+        for h in range(q.shape[1]):
+            assert np.isfinite(o[i, h]).all(), f"{what}: query {i} head {h}"
+            s = kd[seen, h // group] @ qd[i, h]
+            top = seen[s.argmax()]
+            # an fp32 sum of D products is off by D 2^-24 sum |q k| at most; 200 is 2^-288 in weight
+            off = q.shape[2] ** 0.5 * 2 * 2.0 ** -24 * (np.abs(kd[seen, h // group]) @ np.abs(qd[i, h])).max()
+            if len(s) > 1 and (s.max() - np.sort(s)[-2]) * q.shape[2] ** -0.5 < 200 + off:
+                continue
+            assert np.abs(o[i, h] - vd[top, h // group]).max() <= 2.0 ** -7 * np.abs(vd[top, h // group]).max(), f"{what}: {i} {h}"
+            checked += 1
+    assert checked > q.shape[0] // 2
+
+
+@pytest.mark.parametrize("dtype,size", LARGE)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,m", [(6, 6), (6, 300), (150, 150), (60, 2500)])  # narrow, wide, wide with split keys
+def test_large_scores_leave_the_largest(dtype, size, D, n, m):
+    """Scores far beyond what 32 bits hold the units of: weights must neither overflow nor vanish."""
+    say("attn_prompt large scores", dtype, size, D, n, m)
+    g, dt = _gen(n + m), _dt(dtype)
+    q, k = _rand(g, n, 2, D, dtype=dt, scale=size), _rand(g, m, 1, D, dtype=dt, scale=size)
+    v = _rand(g, m, 1, D, dtype=dt)
+    out = q_.attn_prompt(q, k, v, _cu([n]), _cu([m]))
+    _check_largest(out, q, k, v, lambda i: np.arange(m) <= i + m - n, 2, f"{size} {n} {m}")
+
+
+@pytest.mark.parametrize("dtype,size", LARGE)
+@pytest.mark.parametrize("heads,n", [(2, 7), (4, 7), (4, 33), (8, 33)])  # narrow (one and two tiles of rows), wide (4 and 8 waves)
+def test_large_scores_over_the_cache(dtype, size, heads, n):
+    t = torch()
+    say("attn_tree large scores", dtype, size, heads, n)
+    dt, pos = _dt(dtype), 700
+    cache, tables = _cache(n, dt, [pos + n], 16, 1, 64, fill=float("nan"))
+    cache.k.mul_(size)
+    q = _rand(_gen(n), n, heads, 64, dtype=dt, scale=size)
+    out = q_.attn_tree(q, cache, 0, _cu([n]), t.tensor([pos], dtype=t.int32, device="cuda"))
+    at = lambda p: (0, int(tables[0, p // 16]), p % 16, 0)  # noqa: E731
+    k = t.stack([cache.k[at(p)] for p in range(pos + n)])[:, None]
+    v = t.stack([cache.v[at(p)] for p in range(pos + n)])[:, None]
+    _check_largest(out, q, k, v, lambda i: np.arange(pos + n) <= pos + i, heads, f"tree {size} {n}")
