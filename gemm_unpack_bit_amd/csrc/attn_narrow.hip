@@ -172,10 +172,10 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
     common = common < r.keys ? common : r.keys;
 
     f4 o[RT][DL];
-    float m[RT], l[RT];
+    float m[RT], l[RT], most[RT];  // a step with scores above most needs another m (far ones: every step)
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      m[i] = NEG_INF;
+      m[i] = most[i] = NEG_INF;
       l[i] = 0.f;
 #pragma unroll
       for (int j = 0; j < DL; ++j) o[i][j] = f4{0.f, 0.f, 0.f, 0.f};
@@ -316,9 +316,10 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attn_narrow_kernel(AttnArgs a, 
         mx = quarter_max(mx);
         mx = mx == NEG_INF ? NEG_INF : mx * a.scale;
         float by = a.scale, ref = m[i];
-        if (__any(mx > m[i] + E::SLACK || far(m[i]))) {
+        if (__any(mx > most[i])) {
           const float mn = fmaxf(m[i], mx), w = mn == NEG_INF ? 1.f : exp2_(m[i] - mn);
           m[i] = ref = mn;
+          most[i] = far(mn) ? NEG_INF : mn + E::SLACK;
           l[i] *= w;
 #pragma unroll
           for (int j = 0; j < DL; ++j) o[i][j] *= w;

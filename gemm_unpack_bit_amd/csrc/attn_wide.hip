@@ -193,7 +193,9 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
 #pragma unroll
   for (int i = 0; i < DB; ++i) o[i] = zero16();
   const float scale = a.scale;
-  float m = NEG_INF, l = 0.f;  // m: the weights' reference, at most E::SLACK below the largest score
+  // m: the weights' reference, at most E::SLACK below the largest score; a tile
+  // with scores above most_m needs another (far references: every tile)
+  float m = NEG_INF, l = 0.f, most_m = NEG_INF;
 
   // the tile's scores into weights (P^T, 16 keys a piece); with `some` there
   // may be unseen keys among them, at -inf (whose product with a scale of 0 is
@@ -208,9 +210,10 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
     mx = half_max(mx);
     mx = mx == NEG_INF ? NEG_INF : mx * scale;
     float by = scale, ref = m;
-    if (__any(mx > m + E::SLACK || far(m))) {
+    if (__any(mx > most_m)) {
       const float mn = fmaxf(m, mx), w = mn == NEG_INF ? 1.f : exp2_(m - mn);
       m = ref = mn;
+      most_m = far(mn) ? NEG_INF : mn + E::SLACK;
       l *= w;
 #pragma unroll
       for (int i = 0; i < DB; ++i) o[i] *= w;
