@@ -11,7 +11,7 @@
 // tiles of 64; a wave owns 32 rows and all keys of the tile.
 //
 // Measured (fp16, head_dim 128): a causal prompt of 16384 tokens, 64 heads over
-// 8 key heads, 4160 us: 1057 TFLOP/s of the visible pairs, against 1130 for a
+// 8 key heads, 4200 us: 1047 TFLOP/s of the visible pairs, against 1130 for a
 // dense product of 8192 x 8192 x 8192 in fp16 on the same card.  64-token bf16 trees
 // of 16 rows over 4000 tokens, 32 heads over 8: 99 us, 676 TFLOP/s, 2.7 TB/s
 // of keys and values.
