@@ -18,7 +18,9 @@ typedef float f2v __attribute__((ext_vector_type(2)));
 // SLACK: the weights' reference m may lie that far (in powers of two) below the
 // largest score before sums are rescaled to a new one, so that after the first
 // few tiles they hardly ever are; the largest weight, 2^(LIFT + SLACK), still
-// is a normal fp16 number.
+// is a normal fp16 number.  In bf16 it is 1 (weights down to 2^-118 of it stay
+// normal), so that sums of values near the type's largest overflow no sooner
+// than with weights from the largest score.
 // pack rounds two floats to nearest even; NONFINITE_* find
 // halves whose exponent is all ones: ((w & EXP) + ONE) has bit 15 of such a
 // half set, and the addition never carries into the next half.
@@ -38,7 +40,7 @@ struct F16 {
 };
 struct BF16 {
   static constexpr uint32_t EXP = 0x7F807F80u, ONE = 0x00800080u;
-  static constexpr float LIFT = 0.f, SLACK = 8.f;
+  static constexpr float LIFT = -8.f, SLACK = 8.f;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2v{a, b}, b2v));
   }

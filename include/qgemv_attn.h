@@ -28,7 +28,8 @@
  * What a masked or missing key holds (also infinities and NaN) does not reach
  * the output, and a query that sees no key has output 0.  A seen key whose
  * score is -inf has no weight (where scale is not 0), and a query all of whose
- * scores are -inf has output 0 too.
+ * scores are -inf has output 0 too.  A seen key's infinite value makes its column
+ * infinite, or NaN where its weight is too small for the element type.
  */
 #ifndef QGEMV_ATTN_H
 #define QGEMV_ATTN_H

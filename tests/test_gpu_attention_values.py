@@ -3,7 +3,7 @@ the definition gives: NaN, +inf and -inf each in its place."""
 import numpy as np
 import pytest
 
-from tests.attn_ref import attend, f64
+from tests.attn_ref import attend, f64, tolerance
 from tests.gpu_util import say, torch
 from tests.test_gpu_attention import _cache, _cu, _dt, _gen, _rand, _words
 
@@ -185,3 +185,45 @@ def test_large_scores_over_the_cache(dtype, size, heads, n):
     k = t.stack([cache.k[at(p)] for p in range(pos + n)])[:, None]
     v = t.stack([cache.v[at(p)] for p in range(pos + n)])[:, None]
     _check_largest(out, q, k, v, lambda i: np.arange(pos + n) <= pos + i, heads, f"tree {size} {n}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 64])  # narrow and wide kernel
+@pytest.mark.parametrize("step", [0.0, 5.2, -5.2])
+def test_large_bf16_values_do_not_overflow(D, n, step):
+    """Values of 1e36, whose sum over the keys 32 bits hold, while later keys' scores go past the earlier ones'."""
+    t = torch()
+    say("attn_prompt large values", D, n, step)
+    m = 256
+    q, k = t.zeros(n, 2, D, dtype=t.bfloat16, device="cuda"), t.zeros(m, 1, D, dtype=t.bfloat16, device="cuda")
+    q[:, :, 0] = 1
+    k[m // 2:, :, 0] = step
+    v = t.full((m, 1, D), 1e36, dtype=t.bfloat16, device="cuda")
+    v[:, :, 1::2] *= -1
+    out = q_.attn_prompt(q, k, v, _cu([n]), _cu([m]), causal=False, scale=1.0)
+    want = v[:1].expand(n, 2, D).double()
+    assert bool(((out.double() - want).abs() <= 2.0 ** -7 * want.abs()).all())  # (two roundings of 2^-8)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,m", [(3, 40), (64, 300)])  # narrow and wide kernel
+@pytest.mark.parametrize("which", ["queries and keys", "values"])
+def test_subnormal_fp16_inputs_count(D, n, m, which):
+    """Elements below 2^-14, the smallest normal number of fp16."""
+    t = torch()
+    say("attn_prompt subnormal", D, n, m, which)
+    g, tiny = _gen(D + n), 2.0 ** -17
+    a, b = (tiny, 1.0) if which == "queries and keys" else (1.0, tiny)
+    q, k, v = (_rand(g, x, h, D, dtype=t.float16, scale=c) for x, h, c in ((n, 2, a), (m, 1, a), (m, 1, b)))
+    assert 0 < float((v if a == 1 else q).abs().max()) < 2.0 ** -14
+    scale = 2.0 * D ** -0.5 / a ** 2  # scores of about 2
+    out = f64(q_.attn_prompt(q, k, v, _cu([n]), _cu([m]), causal=False, scale=scale))
+    qd, kd, vd = f64(q), f64(k), f64(v)
+    for i in range(n):
+        for h in range(2):
+            want, A, reach = attend(qd[i, h], kd[:, 0], vd[:, 0], np.ones(m, bool), scale)
+            tol = tolerance(A, reach, m, D, "f16", np.abs(vd).max())
+            assert (np.abs(out[i, h] - want) <= tol).all(), (i, h)
+            # (taken for 0, they would give the mean of the values, or 0)
+            other = vd[:, 0].mean(0) if b == 1 else np.zeros(D)
+            assert (np.abs(other - want) > 4 * tol).any(), "the case does not tell"
