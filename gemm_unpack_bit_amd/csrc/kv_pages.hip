@@ -426,7 +426,10 @@ __global__ void __launch_bounds__(256) kv_compact_move_kernel(KvArgs c, const in
   const int32_t* keep = keep_ + (int64_t)b * max_keep;
   const int32_t* table = c.tables + (int64_t)b * c.max_pages;
   const int inside = (1 << c.page_shift) - 1;
-  const bool sound = pos >= 0 && count >= 0 && count <= max_keep && pos <= len && pages_of(len, c.page_shift) <= c.max_pages;
+  // (the kept ones are ascending and inside the row, so there are no more of
+  // them than tokens, and no position below passes 32 bits)
+  const bool sound = pos >= 0 && count >= 0 && count <= max_keep && pos <= len && count <= len - pos &&
+                     pages_of(len, c.page_shift) <= c.max_pages;
   // token t of the kept ones: its source and destination in the pool (in
   // tokens), and what is wrong with it
   int64_t from, to;

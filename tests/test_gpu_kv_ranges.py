@@ -43,3 +43,24 @@ def test_reserve_adds_up_more_pages_than_32_bits_count(rows, max_pages):
     assert c.refs.tolist() == [1] + [0] * (pages - 1)
     assert tables[0, :3].tolist() == [0, -1, -1] and bool((tables[1:, :3] == -1).all())
     assert int(c.status) == q_.KV_NO_PAGES | q_.KV_BAD_INDEX
+
+
+@pytest.mark.parametrize("page", [16, 256])
+def test_compact_of_more_tokens_than_the_row_has(page):
+    """A count past the row's end at the far end of the longest table: refused, and no position is looked up for it."""
+    t = torch()
+    say("kv_compact far count", page)
+    max_pages = ((1 << 31) - 1024) // page
+    cap, keeps = max_pages * page, 4096
+    tables = t.zeros((2, max_pages), dtype=t.int32, device="cuda")
+    k = t.zeros(1, 4, page, 1, 64, dtype=t.float16, device="cuda")
+    refs = t.tensor([1, 1, 1, 1], dtype=t.int32, device="cuda")
+    c = q_.KvCache(k, k.clone(), tables, t.tensor([cap, 40], dtype=t.int32, device="cuda"), refs)
+    keep = t.arange(keeps, dtype=t.int32, device="cuda").repeat(2, 1)
+    pos = t.tensor([cap - 10, 30], dtype=t.int32, device="cuda")
+    q_.kv_compact(c, pos, keep, t.tensor([keeps, 11], dtype=t.int32, device="cuda"))
+    assert c.lens.tolist() == [cap, 40] and c.refs.tolist() == [1] * 4 and int(c.status) == q_.KV_BAD_INDEX
+    assert int(tables.min()) == int(tables.max()) == 0
+    c.status.zero_()
+    q_.kv_compact(c, pos, keep, t.tensor([10, 10], dtype=t.int32, device="cuda"))  # all that there are: as they lie
+    assert c.lens.tolist() == [cap, 40] and int(c.status) == 0
