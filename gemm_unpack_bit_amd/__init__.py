@@ -76,6 +76,20 @@ _SIGS = {
     "qgemv_kv_write": (_i, [_vp, _i, _i, _vp, _vp, _vp, _vp, _vp]),
     "qgemv_kv_fork": (_i, [_vp, _vp, _vp, _vp, _sz, _vp]),
     "qgemv_kv_compact": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "qgemv_kv_append": (_i, [_i, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp]),
+    "qgemv_kv_read": (_i, [_vp, _i, _i, _vp, _vp, _vp, _vp, _vp]),
+    "qgemv_kv8_reserve": (_i, [_vp, _vp, _vp, _vp, _sz, _vp]),
+    "qgemv_kv8_append": (_i, [_i, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp]),
+    "qgemv_kv8_read": (_i, [_i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp]),
+    "qgemv_kv8_fork": (_i, [_vp, _vp, _vp, _vp, _sz, _vp]),
+    "qgemv_kv8_compact": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "qgemv_attn_tree8": (_i, [_i, _vp, _i, _i, _i, ctypes.c_float, _vp, _vp, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    # include/qgemv_step.h
+    "qgemv_rms_norm": (_i, [_i, _i, _i, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "qgemv_rms_norm_q8": (_i, [_i, _i, _i, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "qgemv_w4a8_rows": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "qgemv_sample_workspace_bytes": (_sz, [_i, _i]),
+    "qgemv_sample": (_i, [_i, _i, _i, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -588,15 +602,17 @@ def stream_read(buf, sink, nbytes=None, workgroups=1024, threads=512, offset=0):
 # ---------------------------------------------------------------------------
 
 _ATTENTION = ("KvCache", "attn_prompt", "attn_prompt_workspace_bytes", "attn_tree", "attn_tree_workspace_bytes",
-              "kv_compact", "kv_fork", "kv_reserve", "kv_write")
+              "kv_append", "kv_compact", "kv_fork", "kv_read", "kv_reserve", "kv_write")
+_STEP = ("rms_norm", "rms_norm_q8", "sample", "sample_workspace_bytes", "w4a8_rows")
 
 
 def __getattr__(name):
-    """The names of ``attention`` (imported with torch at their first use)."""
-    if name in _ATTENTION:
-        from . import attention
+    """The names of ``attention`` and ``step`` (imported with torch at their first use)."""
+    if name in _ATTENTION or name in _STEP:
+        from . import attention, step
 
-        for n in _ATTENTION:
-            globals()[n] = getattr(attention, n)
+        for m, names in ((attention, _ATTENTION), (step, _STEP)):
+            for n in names:
+                globals()[n] = getattr(m, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -26,6 +26,14 @@ class _Cache(ctypes.Structure):  # qgemv_kv_cache
     _fields_ += [(n, ctypes.c_void_p) for n in ("k", "v", "tables", "lens", "refs", "status")]
 
 
+class _Cache8(ctypes.Structure):  # qgemv_kv8_cache
+    _fields_ = _Cache._fields_[:9] + [(n, ctypes.c_void_p) for n in ("k_exps", "v_exps")] + _Cache._fields_[9:]
+
+
+_E4M3 = torch.float8_e4m3fn
+_BLOCK = 16  # tokens that share an exponent in a cache of 8 bits
+
+
 # These checks run on every call of a decode loop, so each is a handful of
 # attribute reads; a tensor's device number is -1 off the GPU.
 
@@ -123,15 +131,30 @@ class KvCache:
     refs [pages] (0: free) and status [1] (KV_* bits, set by the calls below and
     cleared by the user).  The tensors are used in place.  ``ws`` is scratch of
     the calls that move pages; calls on one cache and its forks belong on one
-    stream, or must be ordered by the caller."""
+    stream, or must be ordered by the caller.
 
-    def __init__(self, k, v, tables, lens, refs, status=None, ws=None):
-        dtype, dev = _kind(k, "k"), k.get_device()
+    Pools are fp16 or bf16, or e4m3 codes (torch.float8_e4m3fn) with k_exps,
+    v_exps uint8 [layers, pages, page_size / 16, heads_kv]: the value is code *
+    2^(exponent - 127).  Such a cache takes its tokens by kv_append, and queries
+    and new tokens of either 16-bit type."""
+
+    def __init__(self, k, v, tables, lens, refs, status=None, ws=None, k_exps=None, v_exps=None):
+        eight = isinstance(k, torch.Tensor) and k.dtype is _E4M3
+        dtype, dev = _E4M3 if eight else _kind(k, "k"), k.get_device()
         for name, t in (("k", k), ("v", v)):
-            if _kind(t, name) is not dtype or t.get_device() != dev or dev < 0:
+            if t.dtype is not dtype or t.get_device() != dev or dev < 0:
                 raise TypeError("k and v must be CUDA tensors of one type and device")
             if t.dim() != 5 or not t.is_contiguous() or t.shape != k.shape:
                 raise ValueError("k and v must be contiguous [layers, pages, page_size, heads_kv, head_dim]")
+        if eight != (k_exps is not None) or eight != (v_exps is not None):
+            raise ValueError("k_exps and v_exps go with pools of float8_e4m3fn")
+        if eight:
+            shape = (*k.shape[:2], k.shape[2] // _BLOCK, k.shape[3])
+            for name, t in (("k_exps", k_exps), ("v_exps", v_exps)):
+                if t.dtype is not torch.uint8 or t.get_device() != dev:
+                    raise TypeError(f"{name} must be a uint8 CUDA tensor on the same device as the others")
+                if t.shape != shape or not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous [layers, pages, page_size / 16, heads_kv]")
         if tables.dim() != 2:
             raise ValueError("tables must be [rows, max_pages]")
         rows, max_pages = tables.shape
@@ -146,20 +169,26 @@ class KvCache:
         if self._ws[1] < need:
             raise ValueError(f"ws must hold {need} bytes")
         self.k, self.v, self.tables, self.lens, self.refs, self.status, self.ws = k, v, tables, lens, refs, status, ws
+        self.k_exps, self.v_exps = k_exps, v_exps
         self.rows, self.max_pages = rows, max_pages
         self.page_size, self.heads_kv, self.head_dim = k.shape[2:]
-        self.dtype, self._dev = dtype, dev
-        self._c = _Cache(*k.shape, rows, max_pages, k.data_ptr(), v.data_ptr(), *pointers)
+        self.dtype, self._dev, self._eight = dtype, dev, eight
+        pools = [t.data_ptr() for t in ((k, v, k_exps, v_exps) if eight else (k, v))]
+        self._c = (_Cache8 if eight else _Cache)(*k.shape, rows, max_pages, *pools, *pointers)
         self._ref = ctypes.addressof(self._c)
 
     @classmethod
     def empty(cls, layers, pages, page_size, heads_kv, head_dim, rows, max_pages, dtype=torch.float16, device="cuda"):
-        """A cache with no tokens; its pools start as they come."""
+        """A cache with no tokens; its pools start as they come.  dtype: float16, bfloat16 or float8_e4m3fn."""
         shape = (layers, pages, page_size, heads_kv, head_dim)
+        exps = {}
+        if dtype is _E4M3:
+            exps = {n: torch.empty((layers, pages, page_size // _BLOCK, heads_kv), dtype=torch.uint8, device=device)
+                    for n in ("k_exps", "v_exps")}
         return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device),
                    torch.full((rows, max_pages), -1, dtype=torch.int32, device=device),
                    torch.zeros(rows, dtype=torch.int32, device=device),
-                   torch.zeros(pages, dtype=torch.int32, device=device))
+                   torch.zeros(pages, dtype=torch.int32, device=device), **exps)
 
     def empty_rows(self, rows=None):
         """Another set of (empty) rows over the same pools, for kv_fork's ``out``; as many rows as this one has by
@@ -167,7 +196,12 @@ class KvCache:
         rows = self.rows if rows is None else rows
         return KvCache(self.k, self.v,
                        torch.full((rows, self.max_pages), -1, dtype=torch.int32, device=self.k.device),
-                       torch.zeros(rows, dtype=torch.int32, device=self.k.device), self.refs, self.status)
+                       torch.zeros(rows, dtype=torch.int32, device=self.k.device), self.refs, self.status,
+                       k_exps=self.k_exps, v_exps=self.v_exps)
+
+    def _type(self, t, name):
+        """The 16-bit type of a call on this cache whose new or read tokens, or queries, are t."""
+        return _kind(t, name) if self._eight else self.dtype
 
 
 def kv_reserve(cache, cu, out=None):
@@ -177,21 +211,97 @@ def kv_reserve(cache, cu, out=None):
     rows, dev = cache.rows, cache._dev
     if out is None:
         out = torch.empty(rows, dtype=torch.int32, device=cache.k.device)
-    _done("qgemv_kv_reserve", _lib.qgemv_kv_reserve(cache._ref, _ints(cu, "cu", rows + 1, dev), _ints(out, "out", rows, dev),
-                                                    *cache._ws, _raw_stream(dev)))
+    name = "qgemv_kv8_reserve" if cache._eight else "qgemv_kv_reserve"
+    _done(name, getattr(_lib, name)(cache._ref, _ints(cu, "cu", rows + 1, dev), _ints(out, "out", rows, dev), *cache._ws,
+                                    _raw_stream(dev)))
     return out
 
 
 def kv_write(cache, layer, k, v, cu, pos):
     """Writes one layer's new keys and values [tokens, heads_kv, head_dim] to the
-    positions that kv_reserve gave (token cu[b] + i of row b to pos[b] + i)."""
+    positions that kv_reserve gave (token cu[b] + i of row b to pos[b] + i).  A
+    cache of 8 bits takes its tokens by kv_append."""
     rows, dev, dtype = cache.rows, cache._dev, cache.dtype
+    if cache._eight:
+        raise TypeError("a cache of 8 bits takes its tokens by kv_append")
     hk, hv = _heads(k, "k", dtype, dev), _heads(v, "v", dtype, dev)
     tokens, heads_kv, dim = k.shape
     if v.shape != k.shape or heads_kv != cache.heads_kv or dim != cache.head_dim:
         raise ValueError("k and v must be [tokens, heads_kv, head_dim] of the cache")
     _done("qgemv_kv_write", _lib.qgemv_kv_write(cache._ref, layer, tokens, hk, hv, _ints(cu, "cu", rows + 1, dev),
                                                 _ints(pos, "pos", rows, dev), _raw_stream(dev)))
+
+
+def kv_append(cache, layer, k, v, cu, pos, q=None, freqs=None, at=None, interleaved=False, out=None):
+    """kv_write with the position rotation: keys (and queries) turn by the angles
+    position * freqs[i], fp32 [rot / 2], in pairs of elements i and i + rot / 2,
+    or with ``interleaved`` 2 i and 2 i + 1; elements from rot on, and values,
+    stay.  at: int32 [tokens] positions for the angles, by default those in the
+    row.  freqs None: no rotation.  q [tokens, heads, head_dim]: queries to turn
+    into ``out`` (which may be q).  A cache of 8 bits rounds each block of 16
+    tokens and head under an exponent of its own.  Returns out, or None without
+    q."""
+    rows, dev = cache.rows, cache._dev
+    dtype = cache._type(k, "k")
+    hk, hv = _heads(k, "k", dtype, dev), _heads(v, "v", dtype, dev)
+    tokens, heads_kv, dim = k.shape
+    if v.shape != k.shape or heads_kv != cache.heads_kv or dim != cache.head_dim:
+        raise ValueError("k and v must be [tokens, heads_kv, head_dim] of the cache")
+    heads, hq, ho = 0, None, None
+    if q is not None:
+        hq, heads = _heads(q, "q", dtype, dev), q.shape[1]
+        if q.shape[0] != tokens or q.shape[2] != dim:
+            raise ValueError("q must be [tokens, heads, head_dim] with k's tokens and head_dim")
+        if out is None:
+            out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        elif out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        ho = _heads(out, "out", dtype, dev)
+    elif out is not None:
+        raise ValueError("out goes with q")
+    rot, pf, pa = 0, None, None
+    if freqs is not None:
+        if freqs.get_device() != dev or freqs.dtype is not torch.float32:
+            raise TypeError("freqs must be a float32 CUDA tensor on the same device as the others")
+        if not freqs.is_contiguous():
+            raise ValueError("freqs must be contiguous")
+        rot, pf = 2 * freqs.numel(), freqs.data_ptr() or 16
+        if at is not None:
+            pa = _ints(at, "at", tokens, dev)
+    elif at is not None:
+        raise ValueError("at goes with freqs")
+    name = "qgemv_kv8_append" if cache._eight else "qgemv_kv_append"
+    _done(name, getattr(_lib, name)(
+        _DTYPES[dtype], cache._ref, layer, tokens, heads, hq, hk, hv, _ints(cu, "cu", rows + 1, dev),
+        _ints(pos, "pos", rows, dev), pf, rot, int(interleaved), pa, ho, _raw_stream(dev)))
+    return out
+
+
+def kv_read(cache, layer, cu, start, tokens=None, dtype=None, out=None):
+    """Copies tokens of the cache into packed arrays: token cu[b] + i of the
+    result is position start[b] + i of row b (start -1: none; tokens of no row
+    and positions without a page stay as they were).  tokens: how many there are
+    (cu's last); dtype: of the values of a cache of 8 bits, float16 by default;
+    or out: the pair of arrays [tokens, heads_kv, head_dim] to fill.  Returns
+    (k, v)."""
+    rows, dev = cache.rows, cache._dev
+    if out is None:
+        if tokens is None:
+            raise ValueError("tokens or out is needed")
+        dtype = (dtype or torch.float16) if cache._eight else cache.dtype
+        shape = (tokens, cache.heads_kv, cache.head_dim)
+        out = (torch.empty(shape, dtype=dtype, device=cache.k.device), torch.empty(shape, dtype=dtype, device=cache.k.device))
+    k, v = out
+    dtype = cache._type(k, "k")
+    hk, hv = _heads(k, "k", dtype, dev), _heads(v, "v", dtype, dev)
+    if v.shape != k.shape or k.shape[1:] != (cache.heads_kv, cache.head_dim) or (tokens is not None and k.shape[0] != tokens):
+        raise ValueError("out must be two arrays [tokens, heads_kv, head_dim] of the cache")
+    pc, ps = _ints(cu, "cu", rows + 1, dev), _ints(start, "start", rows, dev)
+    if cache._eight:
+        _done("qgemv_kv8_read", _lib.qgemv_kv8_read(_DTYPES[dtype], cache._ref, layer, k.shape[0], pc, ps, hk, hv, _raw_stream(dev)))
+    else:
+        _done("qgemv_kv_read", _lib.qgemv_kv_read(cache._ref, layer, k.shape[0], pc, ps, hk, hv, _raw_stream(dev)))
+    return k, v
 
 
 def kv_fork(cache, parents, out=None):
@@ -205,8 +315,10 @@ def kv_fork(cache, parents, out=None):
         out = cache.empty_rows(parents.numel())
     dev = cache._dev
     ws = cache._ws if cache._ws[1] >= out._ws[1] else out._ws
-    _done("qgemv_kv_fork", _lib.qgemv_kv_fork(cache._ref, _ints(parents, "parents", out.rows, dev), out._ref, *ws,
-                                              _raw_stream(dev)))
+    if out._eight != cache._eight:
+        raise ValueError("out must be a cache over the same pools")
+    name = "qgemv_kv8_fork" if cache._eight else "qgemv_kv_fork"
+    _done(name, getattr(_lib, name)(cache._ref, _ints(parents, "parents", out.rows, dev), out._ref, *ws, _raw_stream(dev)))
     return out
 
 
@@ -218,7 +330,8 @@ def kv_compact(cache, pos, keep, count):
     if keep.dim() != 2:
         raise ValueError("keep must be [rows, max_keep]")
     rows, dev, max_keep = cache.rows, cache._dev, keep.shape[1]
-    _done("qgemv_kv_compact", _lib.qgemv_kv_compact(
+    name = "qgemv_kv8_compact" if cache._eight else "qgemv_kv_compact"
+    _done(name, getattr(_lib, name)(
         cache._ref, _ints(pos, "pos", rows, dev), _ints(keep, "keep", rows * max_keep, dev), max_keep,
         _ints(count, "count", rows, dev), *cache._ws, _raw_stream(dev)))
 
@@ -231,7 +344,7 @@ def attn_tree(q, cache, layer, cu, pos, mask=None, scale=None, out=None, ws=None
     drafted tree: its ancestors and itself).  mask None: the new tokens up to
     itself; with one token per row that is a decode step.  ws: optional scratch
     of attn_tree_workspace_bytes(...) bytes.  Returns out, like q."""
-    dtype, dev, rows = cache.dtype, cache._dev, cache.rows
+    dtype, dev, rows = cache._type(q, "q"), cache._dev, cache.rows
     hq = _heads(q, "q", dtype, dev)
     tokens, heads, dim = q.shape
     if dim != cache.head_dim:
@@ -251,7 +364,8 @@ def attn_tree(q, cache, layer, cu, pos, mask=None, scale=None, out=None, ws=None
         ws = torch.empty(attn_tree_workspace_bytes(tokens, rows, heads, cache.heads_kv, dim), dtype=torch.uint8,
                          device=q.device)
     wp, wn = _ws(ws, dev)
-    _done("qgemv_attn_tree", _lib.qgemv_attn_tree(
+    name = "qgemv_attn_tree8" if cache._eight else "qgemv_attn_tree"
+    _done(name, getattr(_lib, name)(
         _DTYPES[dtype], cache._ref, layer, tokens, heads, 1.0 / math.sqrt(dim) if scale is None else scale, hq,
         _ints(cu, "cu", rows + 1, dev), _ints(pos, "pos", rows, dev), pm, words, _heads(out, "out", dtype, dev), wp, wn,
         _raw_stream(dev)))

@@ -1,6 +1,7 @@
 // C ABI of libqgemv.so: argument validation, dispatch and launch.
 // Host-only code (built with the host compiler); kernels live in the .hip files.
 #include "qgemv.h"
+#include "qgemv_step.h"
 
 #include <hip/hip_runtime.h>
 
@@ -303,7 +304,7 @@ int w4a8_call(int M, int N, int K, const uint16_t* x, const uint32_t* wq, const 
                  reinterpret_cast<float*>(w + lay.sx), mode,
                  mode == qg::W4A8_SPLIT ? reinterpret_cast<uint8_t*>(w + lay.xl) : nullptr,
                  mode == qg::W4A8_ASYM ? reinterpret_cast<int*>(w + lay.zx) : nullptr,
-                 mode == qg::W4A8_ASYM ? reinterpret_cast<int*>(w + lay.xsum) : nullptr};
+                 mode == qg::W4A8_ASYM ? reinterpret_cast<int*>(w + lay.xsum) : nullptr, false};
   int wk = qg::w4a8_waves(N, K);
   if (const char* e = tune_env("QGEMV_W4A8_WK")) wk = std::atoi(e);  // tuning override
   return hip_status(qg::launch_gemv_w4a8(a, wk, reinterpret_cast<hipStream_t>(stream)));
@@ -316,6 +317,27 @@ int qgemv_w4a8(int M, int N, int K, const uint16_t* x, const uint32_t* wq, const
   int rc = check_mnk(M, N, K, 4);
   if (rc) return rc;
   return w4a8_call(M, N, K, x, wq, scales, zeros, y, ws, ws_bytes, true, stream);
+}
+
+int qgemv_w4a8_rows(int M, int N, int K, const int8_t* x8, const float* step, const uint32_t* wq,
+                    const uint16_t* scales, const uint32_t* zeros, uint16_t* y, qgemv_stream_t stream) {
+  if (!x8 || !step || !wq || !scales || !zeros || !y) return QGEMV_ERR_NULL;
+  int rc = check_mnk(M, N, K, 4);
+  if (rc) return rc;
+  if (!aligned16(x8) || ((uintptr_t)step & 3u) || !aligned16(wq) || ((uintptr_t)scales & 1u) ||
+      ((uintptr_t)zeros & 3u) || ((uintptr_t)y & 1u))
+    return QGEMV_ERR_ALIGN;
+  const size_t ybytes = (size_t)M * N * 2, G = K / QGEMV_GROUP;
+  if (overlaps(y, ybytes, x8, (size_t)M * K) || overlaps(y, ybytes, step, (size_t)M * 4) ||
+      overlaps(y, ybytes, wq, words(4, QGEMV_LAYOUT_DEVICE, N, K) * 4) || overlaps(y, ybytes, scales, G * N * 2) ||
+      overlaps(y, ybytes, zeros, words(4, QGEMV_LAYOUT_PLAIN, N, (int)G) * 4))
+    return QGEMV_ERR_VALUE;
+  // (the kernel reads them only)
+  qg::W4A8Args a{M, N, K, nullptr, wq, scales, zeros, y, const_cast<int8_t*>(x8), const_cast<float*>(step), qg::W4A8_PAD,
+                 nullptr, nullptr, nullptr, true};
+  int wk = qg::w4a8_waves(N, K);
+  if (const char* e = tune_env("QGEMV_W4A8_WK")) wk = std::atoi(e);  // tuning override
+  return hip_status(qg::launch_gemv_w4a8(a, wk, reinterpret_cast<hipStream_t>(stream)));
 }
 
 size_t qgemv_w4a8_split_workspace_bytes(int M, int K) {

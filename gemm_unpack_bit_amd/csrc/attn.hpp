@@ -7,10 +7,15 @@
 
 namespace qg {
 
-// the paged cache as the kernels take it (page_size = 1 << page_shift)
+// the paged cache as the kernels take it (page_size = 1 << page_shift).  In a
+// cache of 8 bits k and v are e4m3 codes, a byte an element, and k_exps and
+// v_exps hold the exponents of their blocks of KV_BLOCK tokens, a byte per
+// [layer][page][block][head]: the value is code * 2^(byte - 127).
+constexpr int KV_BLOCK = 16;
 struct KvArgs {
   int layers, pages, page_shift, heads_kv, head_dim, rows, max_pages;
   uint16_t *k, *v;
+  uint8_t *k_exps, *v_exps;  // NULL: 16 bits
   int32_t *tables, *lens, *refs, *status;
 };
 
@@ -33,6 +38,31 @@ struct KvWriteArgs {
   const int32_t *cu, *pos;
 };
 hipError_t launch_kv_write(const KvWriteArgs& a, hipStream_t s);
+
+// Writes new keys and values behind a rotation of queries and keys by their
+// positions; a cache of 8 bits takes it too.
+struct KvAppendArgs {
+  KvArgs c;
+  int bf16, layer, tokens, heads;  // heads 0: no queries
+  int rot, interleaved;            // elements of a head that turn (0: none), in neighbouring pairs
+  const uint16_t *q, *k, *v;
+  uint16_t* o;  // the rotated queries
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
+  const float* freqs;  // [rot / 2] radians a position
+  const int32_t *at;   // [tokens] positions, or NULL: those in the row
+  const int32_t *cu, *pos;
+};
+hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t s);
+
+// Reads values of a layer back into packed arrays.
+struct KvReadArgs {
+  KvArgs c;
+  int bf16, layer, tokens;
+  uint16_t *k, *v;
+  int64_t k_token, k_head, v_token, v_head;
+  const int32_t *cu, *start;
+};
+hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t s);
 
 hipError_t launch_kv_fork(const KvArgs& c, const int32_t* parents, const KvArgs& out, const KvScratch& w,
                           hipStream_t s);
@@ -57,6 +87,7 @@ struct AttnArgs {
   // paged keys
   const int32_t *tables, *pos;
   int pages, page_shift, max_pages;
+  const uint8_t *k_exps, *v_exps;  // a cache of 8 bits: of the layer, else NULL (k and v then point at codes)
   const uint64_t* mask;
   int mask_words;
   float* ws;
@@ -112,5 +143,8 @@ inline int prompt_splits(int tokens, int tokens_k, int rows, int heads_kv, int g
 
 hipError_t launch_attn_narrow(const AttnArgs& a, int rt, hipStream_t s);
 hipError_t launch_attn_wide(const AttnArgs& a, hipStream_t s);
+// (the instances of the same kernels for a cache of 8 bits)
+hipError_t launch_attn_narrow8(const AttnArgs& a, int rt, hipStream_t s);
+hipError_t launch_attn_wide8(const AttnArgs& a, hipStream_t s);
 
 }  // namespace qg

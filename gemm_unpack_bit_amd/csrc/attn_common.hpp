@@ -79,6 +79,9 @@ __device__ __forceinline__ float far_score(float x, float scale, float m) {
   return product - m;
 }
 
+// a row offset from the device, within the call's tokens
+__device__ __forceinline__ int clamp_cu(int x, int tokens) { return x < 0 ? 0 : x > tokens ? tokens : x; }
+
 // max and sum over the lanes l, l ^ 32
 __device__ __forceinline__ float half_max(float v) {
   const uint32_t u = __float_as_uint(v);

@@ -484,11 +484,11 @@ hipError_t launch_gemv_w4a8(const W4A8Args& a, int wk, hipStream_t s) {
   const dim3 gg(tr == 2 ? (NT + 1) / 2 : NT), gb(64 * wk);
   switch (a.mode * 10 + tr) {
     case W4A8_PAD * 10 + 1:
-      hipLaunchKernelGGL(quant_rows_kernel<W4A8_PAD>, qg, dim3(QT), 0, s, a);
+      if (!a.ready) hipLaunchKernelGGL(quant_rows_kernel<W4A8_PAD>, qg, dim3(QT), 0, s, a);
       hipLaunchKernelGGL((gemv_w4a8_kernel<1, W4A8_PAD>), gg, gb, lds, s, a);
       break;
     case W4A8_PAD * 10 + 2:
-      hipLaunchKernelGGL(quant_rows_kernel<W4A8_PAD>, qg, dim3(QT), 0, s, a);
+      if (!a.ready) hipLaunchKernelGGL(quant_rows_kernel<W4A8_PAD>, qg, dim3(QT), 0, s, a);
       hipLaunchKernelGGL((gemv_w4a8_kernel<2, W4A8_PAD>), gg, gb, lds, s, a);
       break;
     case W4A8_SPLIT * 10 + 1:

@@ -129,6 +129,7 @@ struct W4A8Args {
   uint8_t* xl;  // split: the low slices l as fp8 [M, K]
   int* zx;      // asym: activation zero points [16]
   int* xsum;    // asym: per-group sums of the int8 activations [K/128][16]
+  bool ready;   // pad: xq and sx hold the activations already (x is not read)
 };
 // workspace layout of each mode: the byte offsets of xq, xl, sx, zx, xsum
 // and the total (unused parts 0)

@@ -17,7 +17,13 @@
 //
 // Every page number read from a table is checked against the pool before it is
 // used, and every row, slot and count against its range.
+//
+// In a cache of 8 bits a token's piece holds 16 codes, and the blocks' exponents
+// go with their pages.  Compaction there moves tokens between blocks of
+// different exponents: a block that gains tokens takes the largest of those that
+// its tokens come from.
 #include "attn.hpp"
+#include "e4m3.hpp"
 #include "rows.hpp"
 
 namespace qg {
@@ -384,13 +390,24 @@ __global__ void __launch_bounds__(SCAN) kv_fork_small_kernel(KvArgs c, const int
 
 // Copies the tokens of the pages that kv_fork_pages_kernel gave out: grid
 // (pieces of one token over all layers, keys and values; rows).  A thread
-// moves its 16-byte piece of every token, four at a time in flight.
+// moves its 16-byte piece of every token, four at a time in flight.  Behind the
+// pieces, in a cache of 8 bits, a thread per layer, key or value and head moves
+// the exponents of the page's blocks.
 __global__ void __launch_bounds__(256) kv_fork_copy_kernel(KvArgs c, KvArgs out, KvScratch w, int n) {
   const int b = blockIdx.y, src = w.src[b];
   if (src < 0) return;
   const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (j >= (int64_t)2 * c.layers * n) return;
   const int tokens = out.lens[b] & ((1 << c.page_shift) - 1);
+  const int64_t more = j - (int64_t)2 * c.layers * n;
+  if (more >= 0) {
+    if (!c.k_exps || more >= (int64_t)2 * c.layers * c.heads_kv) return;
+    const int r = (int)(more % (2 * c.heads_kv)), blocks = (1 << c.page_shift) / KV_BLOCK;
+    uint8_t* exps = (r < c.heads_kv ? c.k_exps : c.v_exps) + r % c.heads_kv;
+    const int64_t base = more / (2 * c.heads_kv) * c.pages;
+    for (int i = 0; i * KV_BLOCK < tokens; ++i)
+      exps[((base + w.dst[b]) * blocks + i) * c.heads_kv] = exps[((base + src) * blocks + i) * c.heads_kv];
+    return;
+  }
   const int layer = (int)(j / (2 * n)), r = (int)(j % (2 * n));
   u4* pool = reinterpret_cast<u4*>(r < n ? c.k : c.v);
   const int64_t base = (int64_t)layer * c.pages;
@@ -411,29 +428,25 @@ __global__ void __launch_bounds__(256) kv_fork_copy_kernel(KvArgs c, KvArgs out,
 // compact
 // ---------------------------------------------------------------------------
 
-// Moves the kept tokens: grid (pieces of one token over all layers, keys and
-// values; rows).  Lane j of every wave looks up kept token j (64 at a time):
-// where it is and goes, and whether the row can be compacted at all, from the
-// state before the call, so every workgroup of a row comes to the same answer;
-// the first one leaves it for the next kernel.  Then a thread moves its 16-byte
-// piece of every token in order, eight at a time: keep is strictly ascending,
-// so the places that a batch writes (up to pos + j + 7) are never sources of a
-// later one (from pos + j + 8 on).
-__global__ void __launch_bounds__(256) kv_compact_move_kernel(KvArgs c, const int32_t* pos_, const int32_t* keep_,
-                                                              int max_keep, const int32_t* count_, KvScratch w, int n) {
-  const int b = blockIdx.y, lane = threadIdx.x & 63;
-  const int pos = pos_[b], count = count_[b], len = c.lens[b];
-  const int32_t* keep = keep_ + (int64_t)b * max_keep;
-  const int32_t* table = c.tables + (int64_t)b * c.max_pages;
-  const int inside = (1 << c.page_shift) - 1;
-  // (the kept ones are ascending and inside the row, so there are no more of
-  // them than tokens, and no position below passes 32 bits)
-  const bool sound = pos >= 0 && count >= 0 && count <= max_keep && pos <= len && count <= len - pos &&
-                     pages_of(len, c.page_shift) <= c.max_pages;
+// The kept tokens of a row and whether the row can be compacted at all, from the
+// state before the call, so that every wave of a row comes to the same answer.
+struct Kept {
+  const KvArgs& c;
+  const int32_t *keep, *table;
+  int pos, count, len, inside;
+  bool sound;
+  __device__ __forceinline__ Kept(const KvArgs& c, const int32_t* pos_, const int32_t* keep_, int max_keep,
+                                  const int32_t* count_, int b)
+      : c(c), keep(keep_ + (int64_t)b * max_keep), table(c.tables + (int64_t)b * c.max_pages), pos(pos_[b]), count(count_[b]),
+        len(c.lens[b]), inside((1 << c.page_shift) - 1) {
+    // (the kept ones are ascending and inside the row, so there are no more of
+    // them than tokens, and no position below passes 32 bits)
+    sound = pos >= 0 && count >= 0 && count <= max_keep && pos <= len && count <= len - pos &&
+            pages_of(len, c.page_shift) <= c.max_pages;
+  }
   // token t of the kept ones: its source and destination in the pool (in
   // tokens), and what is wrong with it
-  int64_t from, to;
-  auto look = [&](int t) -> int {
+  __device__ __forceinline__ int look(int t, int64_t& from, int64_t& to) const {
     from = to = 0;
     if (!sound || t >= count) return 0;
     const int s = keep[t], before = t ? keep[t - 1] : -1, p = pos + t;
@@ -449,18 +462,40 @@ __global__ void __launch_bounds__(256) kv_compact_move_kernel(KvArgs c, const in
     from = ((int64_t)src << c.page_shift) + ((pos + s) & inside);
     to = ((int64_t)dst << c.page_shift) + (p & inside);
     return 0;
-  };
-  int wrong = 0;
-  for (int t0 = 64; t0 < count && sound; t0 += 64) wrong |= look(t0 + lane);
-  wrong |= look(lane);  // (the first 64 stay looked up)
-  if (sound && count == 0 && pos & inside) {  // ends inside a page that stays
-    const int page = table[pos >> c.page_shift];
-    if ((unsigned)page >= (unsigned)c.pages) wrong |= KV_BAD_INDEX;
-    else if (c.refs[page] > 1) wrong |= KV_SHARED;
   }
-  int bad = __ballot(wrong & KV_BAD_INDEX) ? KV_BAD_INDEX : __ballot(wrong & KV_SHARED) ? KV_SHARED : 0;
-  if (!sound) bad = pos == -1 ? 0 : KV_BAD_INDEX;
-  const bool ok = sound && !bad;
+  // Looks all kept tokens up, a lane each; the first 64 stay looked up.  Returns
+  // the bits to report, and whether the row is compacted.
+  __device__ __forceinline__ int decide(int lane, int64_t& from, int64_t& to, bool& ok) const {
+    int wrong = 0;
+    for (int t0 = 64; t0 < count && sound; t0 += 64) wrong |= look(t0 + lane, from, to);
+    wrong |= look(lane, from, to);
+    if (sound && count == 0 && pos & inside) {  // ends inside a page that stays
+      const int page = table[pos >> c.page_shift];
+      if ((unsigned)page >= (unsigned)c.pages) wrong |= KV_BAD_INDEX;
+      else if (c.refs[page] > 1) wrong |= KV_SHARED;
+    }
+    int bad = __ballot(wrong & KV_BAD_INDEX) ? KV_BAD_INDEX : __ballot(wrong & KV_SHARED) ? KV_SHARED : 0;
+    if (!sound) bad = pos == -1 ? 0 : KV_BAD_INDEX;
+    ok = sound && !bad;
+    return bad;
+  }
+};
+
+// Moves the kept tokens: grid (pieces of one token over all layers, keys and
+// values; rows).  Lane j of every wave looks up kept token j (64 at a time):
+// where it is and goes, and whether the row can be compacted at all; the first
+// workgroup of a row leaves that for the next kernel.  Then a thread moves its
+// 16-byte piece of every token in order, eight at a time: keep is strictly
+// ascending, so the places that a batch writes (up to pos + j + 7) are never
+// sources of a later one (from pos + j + 8 on).
+__global__ void __launch_bounds__(256) kv_compact_move_kernel(KvArgs c, const int32_t* pos_, const int32_t* keep_,
+                                                              int max_keep, const int32_t* count_, KvScratch w, int n) {
+  const int b = blockIdx.y, lane = threadIdx.x & 63;
+  const Kept kept(c, pos_, keep_, max_keep, count_, b);
+  const int count = kept.count;
+  int64_t from, to;
+  bool ok;
+  const int bad = kept.decide(lane, from, to, ok);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     w.src[b] = ok;
     if (bad) atomicOr(c.status, bad);
@@ -472,7 +507,7 @@ __global__ void __launch_bounds__(256) kv_compact_move_kernel(KvArgs c, const in
   u4* pool = reinterpret_cast<u4*>(r < n ? c.k : c.v) + (((int64_t)(mine ? layer : 0) * c.pages) << c.page_shift) * n +
              (r < n ? r : r - n);
   for (int t0 = 0; t0 < count; t0 += 64) {
-    if (t0) look(t0 + lane);
+    if (t0) kept.look(t0 + lane, from, to);
     const int m = min(64, count - t0);
     for (int i0 = 0; i0 < m; i0 += 8) {
       u4 x[8];
@@ -486,6 +521,82 @@ __global__ void __launch_bounds__(256) kv_compact_move_kernel(KvArgs c, const in
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (mine && i0 + i < m && f[i] != d[i]) pool[d[i] * n] = x[i];
+    }
+  }
+}
+
+// The same for a cache of 8 bits: a wave has `group` heads of the keys or values
+// of one layer and row (grid: layer, keys or values, heads in waves; rows), and
+// takes the row's blocks from pos on in order, 16 tokens at once: it reads the
+// codes of all a block's tokens and the exponents that they are under, then
+// writes them under the largest.  Places written lie before all later sources,
+// as above.  A block none of whose tokens moves stays.
+template <int D>
+__global__ void __launch_bounds__(256) kv_compact_move8_kernel(KvArgs c, const int32_t* pos_, const int32_t* keep_,
+                                                               int max_keep, const int32_t* count_, KvScratch w, int group) {
+  constexpr int U = D / 16, TP = 64 / U, PASSES = KV_BLOCK / TP;
+  const int b = blockIdx.y, lane = threadIdx.x & 63;
+  const Kept kept(c, pos_, keep_, max_keep, count_, b);
+  int64_t from, to;
+  bool ok;
+  const int bad = kept.decide(lane, from, to, ok);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    w.src[b] = ok;
+    if (bad) atomicOr(c.status, bad);
+  }
+  if (!ok) return;
+  const int parts = (c.heads_kv + group - 1) / group;
+  const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (wave >= (int64_t)2 * c.layers * parts) return;
+  const int layer = (int)(wave / (2 * parts)), which = (int)(wave % (2 * parts)) / parts, h0 = (int)(wave % parts) * group;
+  const int64_t base = ((int64_t)layer * c.pages) << c.page_shift;
+  uint8_t* codes = reinterpret_cast<uint8_t*>(which ? c.v : c.k) + base * c.heads_kv * D;
+  uint8_t* exps = (which ? c.v_exps : c.k_exps) + base / KV_BLOCK * c.heads_kv;
+  const int end = kept.pos + kept.count;
+  for (int first = kept.pos & ~(KV_BLOCK - 1); first < end; first += KV_BLOCK) {
+    // the lane's tokens of the block: from, to (-1: none)
+    int64_t f[PASSES], t[PASSES];
+    bool moves = false;
+#pragma unroll
+    for (int x = 0; x < PASSES; ++x) {
+      const int p = first + TP * x + lane / U;
+      f[x] = t[x] = -1;
+      if (p < kept.pos) {
+        f[x] = t[x] = ((int64_t)kept.table[p >> c.page_shift] << c.page_shift) + (p & kept.inside);
+      } else if (p < end) {
+        kept.look(p - kept.pos, f[x], t[x]);
+        if (kept.keep[p - kept.pos] == p - kept.pos) {  // (looked up only where it has to be)
+          f[x] = t[x] = ((int64_t)kept.table[p >> c.page_shift] << c.page_shift) + (p & kept.inside);
+        } else {
+          moves = true;
+        }
+      }
+    }
+    if (!__any(moves)) continue;
+    const int64_t pool = (int64_t)c.pages << c.page_shift;
+    for (int h = h0; h < min(h0 + group, c.heads_kv); ++h) {
+      u4 v[PASSES];
+      int e[PASSES], most = EXP_LEAST;
+#pragma unroll
+      for (int x = 0; x < PASSES; ++x) {
+        e[x] = EXP_LEAST;
+        if ((uint64_t)f[x] >= (uint64_t)pool || (uint64_t)t[x] >= (uint64_t)pool) continue;
+        v[x] = *reinterpret_cast<const u4*>(codes + (f[x] * c.heads_kv + h) * D + 16 * (lane % U));
+        e[x] = exps[f[x] / KV_BLOCK * c.heads_kv + h];
+        e[x] = e[x] > EXP_MOST ? EXP_MOST : e[x] < EXP_LEAST ? EXP_LEAST : e[x];
+        most = max(most, e[x]);
+      }
+#pragma unroll
+      for (int d = U; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
+#pragma unroll
+      for (int x = 0; x < PASSES; ++x) {
+        if ((uint64_t)f[x] >= (uint64_t)pool || (uint64_t)t[x] >= (uint64_t)pool) continue;
+        const float by = exp_ratio(e[x], most);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[x][i] = e[x] == most ? v[x][i] : rescale4(v[x][i], by);
+        if (f[x] != t[x] || e[x] != most) *reinterpret_cast<u4*>(codes + (t[x] * c.heads_kv + h) * D + 16 * (lane % U)) = v[x];
+        if (lane % U == 0) exps[t[x] / KV_BLOCK * c.heads_kv + h] = (uint8_t)most;
+      }
     }
   }
 }
@@ -506,8 +617,11 @@ __global__ void __launch_bounds__(64) kv_compact_rows_kernel(KvArgs c, const int
   if (threadIdx.x == 0) c.lens[b] = end;
 }
 
-int pieces(const KvArgs& c) { return c.heads_kv * c.head_dim / 8; }
-unsigned piece_blocks(const KvArgs& c) { return (unsigned)(((int64_t)2 * c.layers * pieces(c) + 255) / 256); }
+int pieces(const KvArgs& c) { return c.heads_kv * c.head_dim / (c.k_exps ? 16 : 8); }
+unsigned piece_blocks(const KvArgs& c) {
+  const int64_t exps = c.k_exps ? c.heads_kv : 0;  // (the threads of kv_fork_copy_kernel that move exponents)
+  return (unsigned)((2 * c.layers * (pieces(c) + exps) + 255) / 256);
+}
 
 }  // namespace
 
@@ -538,8 +652,20 @@ hipError_t launch_kv_fork(const KvArgs& c, const int32_t* parents, const KvArgs&
 
 hipError_t launch_kv_compact(const KvArgs& c, const int32_t* pos, const int32_t* keep, int max_keep,
                              const int32_t* count, const KvScratch& w, hipStream_t s) {
-  hipLaunchKernelGGL(kv_compact_move_kernel, dim3(piece_blocks(c), (unsigned)c.rows), dim3(256), 0, s, c, pos, keep,
-                     max_keep, count, w, pieces(c));
+  if (c.k_exps) {
+    // (heads that a wave takes with one look at the kept tokens: as many as
+    // leave enough waves)
+    int group = 1;
+    while (group < 8 && group < c.heads_kv && (int64_t)c.rows * c.layers * c.heads_kv / group >= 4096) group *= 2;
+    const int64_t waves = (int64_t)2 * c.layers * ((c.heads_kv + group - 1) / group);
+    const dim3 grid((unsigned)((waves + 3) / 4), (unsigned)c.rows);
+    if (c.head_dim == 128)
+      hipLaunchKernelGGL(kv_compact_move8_kernel<128>, grid, dim3(256), 0, s, c, pos, keep, max_keep, count, w, group);
+    else hipLaunchKernelGGL(kv_compact_move8_kernel<64>, grid, dim3(256), 0, s, c, pos, keep, max_keep, count, w, group);
+  } else {
+    hipLaunchKernelGGL(kv_compact_move_kernel, dim3(piece_blocks(c), (unsigned)c.rows), dim3(256), 0, s, c, pos, keep,
+                       max_keep, count, w, pieces(c));
+  }
   hipLaunchKernelGGL(kv_compact_rows_kernel, dim3((unsigned)c.rows), dim3(64), 0, s, c, pos, count, w);
   return hipGetLastError();
 }

@@ -177,6 +177,90 @@ int qgemv_attn_tree(int dtype, const qgemv_kv_cache *c, int layer, int tokens, i
                     const qgemv_heads *q, const int32_t *cu, const int32_t *pos, const uint64_t *mask,
                     int mask_words, const qgemv_heads *o, void *ws, size_t ws_bytes, qgemv_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Writing new keys and values with their position rotation, which turns the
+ * queries too: pair i < rot / 2 of a head turns by the angle
+ * t = position * freqs[i],
+ *     (a, b) -> (a cos t - b sin t, a sin t + b cos t),
+ * in fp32 (t's whole turns are taken off in 64 bits), rounded once; elements
+ * from rot on stay as they are, and so do values.
+ *   dtype       of q, k, v and o: QGEMV_F16 or QGEMV_BF16 (of a cache of 16
+ *               bits: its own)
+ *   heads       query heads, any number; 0: no queries (q and o may be NULL)
+ *   rot         elements of a head that turn: a multiple of 16 up to head_dim
+ *               (UNSUPPORTED otherwise), 0: none (freqs may be NULL)
+ *   freqs [dev] fp32 [rot / 2], 16-byte aligned: radians a position
+ *   interleaved pair i is elements 2 i and 2 i + 1; else i and i + rot / 2
+ *   at [dev]    int32 [tokens]: positions for the angles, or NULL: those in the
+ *               row (a drafted tree's nodes turn by their depth, say)
+ *   o           takes the rotated queries; it may be q itself (the same data
+ *               and strides)
+ * Token cu[b] + i goes to position pos[b] + i of row b (pos from
+ * qgemv_kv_reserve).  Tokens of rows at -1 and tokens of no row are skipped, in
+ * o too; keys and values at a position without a page are.  The sum of tokens
+ * * (heads + heads_kv) is at most about 2^28 (SHAPE).
+ * Checks, in order: null, dtype, cache, rot, shape, alignment, overlap.
+ * ------------------------------------------------------------------------ */
+int qgemv_kv_append(int dtype, const qgemv_kv_cache *c, int layer, int tokens, int heads, const qgemv_heads *q,
+                    const qgemv_heads *k, const qgemv_heads *v, const int32_t *cu, const int32_t *pos,
+                    const float *freqs, int rot, int interleaved, const int32_t *at, const qgemv_heads *o,
+                    qgemv_stream_t stream);
+
+/* Copies tokens of the cache into packed arrays: token cu[b] + i of k and v
+ * becomes position start[b] + i of row b (rows at -1, tokens of no row and
+ * positions without a page are skipped: k and v stay as they were there). */
+int qgemv_kv_read(const qgemv_kv_cache *c, int layer, int tokens, const int32_t *cu, const int32_t *start,
+                  const qgemv_heads *k, const qgemv_heads *v, qgemv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The paged cache in 8 bits: pools of e4m3 codes (bias 7, no infinities, 0x7F
+ * and 0xFF are NaN), and an exponent for every block of 16 tokens and head,
+ *     k, v           [dev] uint8 [layers][pages][page_size][heads_kv][head_dim]
+ *     k_exps, v_exps [dev] uint8 [layers][pages][page_size / 16][heads_kv]
+ *     value = code * 2^(exponent - 127)
+ * (exponents 1 to 254; 0 and 255 count as those).  The rest is as in
+ * qgemv_kv_cache, and so are the calls, but for what follows; qgemv_kv_write's
+ * place is taken by qgemv_kv8_append (with rot 0).
+ *
+ * Writing a token: keys after their rotation and values, in fp32, are rounded to
+ * nearest even under the block's exponent e, the least with
+ * max |x| <= 448 * 2^(e - 127) over the block's new tokens and heads' elements,
+ * at least 63, and at least what the block has where it holds earlier tokens of
+ * the row.  If it grows, the codes of the earlier tokens are written anew under
+ * it, rounded to nearest even (exact but for codes that become subnormal).
+ * Infinities and NaN become NaN and do not count in the maximum.
+ *
+ * kv8_compact: a block that gains tokens has the largest exponent of the blocks
+ * that its tokens come from, and codes of others are rewritten under it
+ * likewise.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int layers, pages, page_size, heads_kv, head_dim, rows, max_pages;
+  uint8_t *k, *v, *k_exps, *v_exps;
+  int32_t *tables, *lens, *refs, *status;
+} qgemv_kv8_cache;
+
+int qgemv_kv8_reserve(const qgemv_kv8_cache *c, const int32_t *cu, int32_t *pos, void *ws, size_t ws_bytes,
+                      qgemv_stream_t stream);
+int qgemv_kv8_append(int dtype, const qgemv_kv8_cache *c, int layer, int tokens, int heads, const qgemv_heads *q,
+                     const qgemv_heads *k, const qgemv_heads *v, const int32_t *cu, const int32_t *pos,
+                     const float *freqs, int rot, int interleaved, const int32_t *at, const qgemv_heads *o,
+                     qgemv_stream_t stream);
+/* (values past fp16's range are infinite in a read of QGEMV_F16) */
+int qgemv_kv8_read(int dtype, const qgemv_kv8_cache *c, int layer, int tokens, const int32_t *cu, const int32_t *start,
+                   const qgemv_heads *k, const qgemv_heads *v, qgemv_stream_t stream);
+int qgemv_kv8_fork(const qgemv_kv8_cache *c, const int32_t *parents, const qgemv_kv8_cache *out, void *ws,
+                   size_t ws_bytes, qgemv_stream_t stream);
+int qgemv_kv8_compact(const qgemv_kv8_cache *c, const int32_t *pos, const int32_t *keep, int max_keep,
+                      const int32_t *count, void *ws, size_t ws_bytes, qgemv_stream_t stream);
+
+/* qgemv_attn_tree over a cache of 8 bits: keys and values are its values in the
+ * queries' type (exact in bf16; in fp16 from 2^-24 to 65504, infinite past
+ * that). */
+int qgemv_attn_tree8(int dtype, const qgemv_kv8_cache *c, int layer, int tokens, int heads, float scale,
+                     const qgemv_heads *q, const int32_t *cu, const int32_t *pos, const uint64_t *mask,
+                     int mask_words, const qgemv_heads *o, void *ws, size_t ws_bytes, qgemv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
