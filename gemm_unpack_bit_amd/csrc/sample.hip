@@ -18,25 +18,27 @@
 //
 // A prefix of the order ends at one logit and index.  No row is sorted to find
 // them: a histogram of 1024 bins of equal width, from the row's largest logit to
-// its smallest, with counts and weights, says in which bin the prefix ends; the
-// row is searched for the elements of that bin alone (or, where they are few, of
-// all bins up to it), and these are sorted.
+// its smallest, says in which bin it ends, and the elements of that bin alone
+// (with top-k, where they are few, of all bins up to it) are listed and sorted.
 //
-// Bound: the logits are read once from memory and up to three times more from
-// the caches, and every weight takes about 20 operations of 64 bits; for one row
-// it is the launches.  Kernels: `slices` of the vocabulary for what touches every
-// logit (scan, histogram, sums), a workgroup per row for what follows from it
-// (cut, draw).
+// Kernels.  `slices` of the vocabulary, each a workgroup, do what touches every
+// logit: sample_scan_kernel (largest and smallest), sample_bins_kernel (the
+// histogram, where a row has top-k or top-p), sample_sums_kernel (the list, and
+// the sum of what is kept for certain); a workgroup per row does the rest
+// (sample_draw_kernel).
+//
+// Bound: for one row the launches; for many the three times that a logit is read
+// (once from memory, then from the caches) and a weight's 20 operations of 64
+// bits, twice with top-p.
 #include "attn_common.hpp"
 #include "step.hpp"
 
 namespace qg {
 namespace {
 
-constexpr int BINS = 1024, THREADS = 1024;  // (a thread a bin)
-constexpr int CAP = 4096;                   // elements sorted at once
+constexpr int BINS = 1024, THREADS = 1024;  // (of a row's workgroup: a thread a bin)
+constexpr int CAP = 4096;                   // elements listed
 constexpr int SLICE_THREADS = 256, PIECE = 8;
-constexpr double ONE = 0x1p42;  // the largest logit's weight
 
 // what a slice of a row leaves: its largest logit's key and place (the first
 // one), its smallest finite logit
@@ -46,29 +48,38 @@ struct Part {
   float least;
   int pad;
 };
-// where the kept prefix ends: keys above `key`, and of those equal the ones up
-// to index `at`; done: the row's token is chosen
+// how the end of a row's prefix is found: it has none, all that is left is in
+// the list, it lies in the bin `bin` whose elements are in the list, or neither
+// (the list is not used)
+enum : int { CUT_NONE = 0, CUT_FEW = 1, CUT_BIN = 2, CUT_MANY = 3 };
+struct Plan {
+  int mode, bin;
+  unsigned long long before;  // weights in front of the bin (by weight)
+  double goal;                // p S
+  unsigned long long total;   // S
+};
+// the end of a prefix: keys above `key`, and of those equal the ones up to
+// index `at`
 struct Cut {
   uint32_t key;
-  int at, done, pad;
+  int at;
 };
 
 struct Work {
-  unsigned long long *weights, *sums;  // [rows][BINS], [rows][slices]
-  uint32_t* counts;                    // [rows][BINS]
-  Cut* cuts;                           // [rows]
-  Part* parts;                         // [rows][slices]
-  __device__ __host__ __forceinline__ Work(void* ws, int64_t rows, int slices) {
+  unsigned long long *bins, *sums, *list;  // [rows][BINS], [rows][slices], [rows][CAP]
+  int* listed;                             // [rows]
+  Part* parts;                             // [rows][slices]
+  __device__ __forceinline__ Work(void* ws, int64_t rows, int slices) {
     char* p = reinterpret_cast<char*>(ws);
-    weights = reinterpret_cast<unsigned long long*>(p), p += rows * BINS * 8;
-    sums = reinterpret_cast<unsigned long long*>(p), p += (rows * slices * 8 + 15) / 16 * 16;
-    counts = reinterpret_cast<uint32_t*>(p), p += rows * BINS * 4;
-    cuts = reinterpret_cast<Cut*>(p), p += rows * 16;
-    parts = reinterpret_cast<Part*>(p);
+    bins = reinterpret_cast<unsigned long long*>(p), p += rows * BINS * 8;
+    list = reinterpret_cast<unsigned long long*>(p), p += rows * CAP * 8;
+    parts = reinterpret_cast<Part*>(p), p += rows * slices * 16;
+    sums = reinterpret_cast<unsigned long long*>(p), p += rows * slices * 8;
+    listed = reinterpret_cast<int*>(p);
   }
 };
 constexpr size_t work_bytes(int64_t rows, int slices) {
-  return (size_t)(rows * BINS * 12 + (rows * slices * 8 + 15) / 16 * 16 + rows * 16 + rows * slices * 16);
+  return (size_t)(rows * (BINS * 8 + CAP * 8 + 4) + rows * slices * 24);
 }
 
 // Keys: floats in their order as unsigned numbers; NaN as -infinity, -0 as 0.
@@ -115,32 +126,34 @@ __device__ __forceinline__ void load_piece(const void* row, int i, int end, floa
   }
 }
 
-// Weights.  2^x for x <= 0 by its power series around the nearest whole number:
-// |f ln 2| <= 0.347, so the 12th power's term, the first left out, is 2^-47.
+// Weights.  x = (l - M) log2(e) / T <= 0 is split into its nearest whole number
+// n and f; 2^f is a polynomial through 2^f at the ten Chebyshev points of
+// [-1/2, 1/2], off by 3e-14 of it at most (2^-42 is 2.3e-13); n goes into the
+// exponent.  The additions of 1.5 * 2^52 round to whole numbers and leave these in
+// the sum's low bits.
 struct Weigh {
   double top, by;  // M, log2(e) / T
   __device__ __forceinline__ double operator()(float l) const {
-    const double x = l == (float)top ? 0.0 : ((double)l - top) * by;
-    const double n = __builtin_rint(x), f = x - n;
-    double p = 4.44553827187081e-10;  // ln(2)^11 / 11!
-    p = fma(p, f, 7.054911620801121e-09);
-    p = fma(p, f, 1.0178086009239696e-07);
-    p = fma(p, f, 1.3215486790144305e-06);
-    p = fma(p, f, 1.5252733804059838e-05);
-    p = fma(p, f, 1.5403530393381606e-04);
-    p = fma(p, f, 1.3333558146428441e-03);
-    p = fma(p, f, 9.618129107628477e-03);
-    p = fma(p, f, 5.5504108664821576e-02);
-    p = fma(p, f, 2.402265069591007e-01);
-    p = fma(p, f, 6.931471805599453e-01);
+    constexpr double ROUND = 0x1.8p52;
+    const double x = l == (float)top ? 0.0 : ((double)l - top) * by, r = x + ROUND, f = x - (r - ROUND);
+    double p = 1.0205905413765595e-07;
+    p = fma(p, f, 1.325964524488711e-06);
+    p = fma(p, f, 1.5252672924850737e-05);
+    p = fma(p, f, 1.540343375125101e-04);
+    p = fma(p, f, 1.3333558200794592e-03);
+    p = fma(p, f, 9.618129193934313e-03);
+    p = fma(p, f, 5.550410866465167e-02);
+    p = fma(p, f, 2.402265069564034e-01);
+    p = fma(p, f, 6.931471805599462e-01);
     p = fma(p, f, 1.0);
+    const uint64_t n = __builtin_bit_cast(uint64_t, r) << 52;
     // (below 2^-64, and where x is NaN, as of -infinity at an infinite T: none)
-    return x > -64.0 ? __builtin_ldexp(p, (int)n) : 0.0;
+    return x > -64.0 ? __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, p) + n) : 0.0;
   }
 };
 // as a whole number of 2^-42, rounded to nearest
 __device__ __forceinline__ unsigned long long fixed(double w) {
-  return __builtin_bit_cast(unsigned long long, fma(w, ONE, 0x1p52)) - __builtin_bit_cast(unsigned long long, 0x1p52);
+  return __builtin_bit_cast(unsigned long long, fma(w, 0x1p42, 0x1p52)) & ((1ull << 52) - 1);
 }
 
 // What the row's settings ask for.
@@ -158,7 +171,8 @@ struct Settings {
     const float m = a.min_p ? a.min_p[row] : 0.f;
     least = m > 0.f ? (m < 1.f ? (double)m : 1.0) : 0.0;
   }
-  __device__ __forceinline__ bool cuts() const { return !greedy && (k > 0 || p < 1.0); }
+  __device__ __forceinline__ bool by_count(int vocab) const { return k > 0 && k < vocab; }
+  __device__ __forceinline__ bool by_weight() const { return p < 1.0; }
 };
 
 // max over a wave; sums over the wave's lanes up to and with the lane's
@@ -180,7 +194,8 @@ __device__ __forceinline__ unsigned long long wave_scan64(unsigned long long v) 
   return v;
 }
 
-// A workgroup's THREADS threads: sums up to and with the thread's, and of all.
+// A workgroup's T threads: sums up to and with the thread's, and of all.
+template <int T>
 __device__ __forceinline__ unsigned long long block_scan64(unsigned long long v, unsigned long long& total,
                                                            unsigned long long* red) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -189,7 +204,7 @@ __device__ __forceinline__ unsigned long long block_scan64(unsigned long long v,
   __syncthreads();
   unsigned long long before = 0, all = 0;
 #pragma unroll
-  for (int i = 0; i < THREADS / 64; ++i) {
+  for (int i = 0; i < T / 64; ++i) {
     before += i < w ? red[i] : 0;
     all += red[i];
   }
@@ -242,6 +257,44 @@ struct Binning {
   }
 };
 
+// The row's largest and smallest logits and what follows from its histogram, the
+// same in every workgroup of the row; T threads, all of them.
+template <int T>
+__device__ __forceinline__ Plan plan_of(const SampleArgs& a, const Settings& set, const unsigned long long* bins,
+                                        unsigned long long* red, Plan* shared) {
+  const bool by_count = set.by_count(a.vocab), by_weight = set.by_weight();
+  if (!by_count && !by_weight) return Plan{CUT_NONE, BINS, 0, 0.0, 0};
+  constexpr int E = BINS / T;
+  unsigned long long mine[E], sum = 0, total;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    mine[e] = bins[E * threadIdx.x + e];
+    sum += mine[e];
+  }
+  unsigned long long before = block_scan64<T>(sum, total, red) - sum;
+  // by count: the first bin with k elements up to it (all may be fewer); by
+  // weight: the first up to which the weights reach p S
+  const double goal = by_count ? (double)set.k : set.p * (double)total;
+  if (threadIdx.x == 0) *shared = Plan{CUT_NONE, BINS, 0, 0.0, 0};
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const unsigned long long upto = before + mine[e];
+    const bool first = E * threadIdx.x + e == 0;
+    if ((double)upto >= goal && (first || (double)before < goal)) {
+      Plan p{CUT_BIN, (int)(E * threadIdx.x) + e, before, goal, total};
+      if (by_count) p.mode = upto <= CAP ? CUT_FEW : by_weight ? CUT_MANY : CUT_BIN;
+      *shared = p;
+    }
+    before = upto;
+  }
+  __syncthreads();
+  Plan p = *shared;
+  // (fewer logits above -infinity than k: no end by count)
+  if (by_count && p.mode == CUT_NONE && by_weight) p.mode = total <= CAP ? CUT_FEW : CUT_MANY;
+  return p;
+}
+
 // ---------------------------------------------------------------------------
 // slices
 // ---------------------------------------------------------------------------
@@ -253,20 +306,30 @@ __global__ void __launch_bounds__(SLICE_THREADS) sample_scan_kernel(SampleArgs a
   const Work w(a.ws, a.rows, slices);
   const int begin = s * slice, end = min(begin + slice, a.vocab);
   const void* x = static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes;
-  unsigned long long best = 0;
-  float least = __builtin_inff();
-#pragma unroll 2
+  float most = NEG_INF, least = __builtin_inff();
+  int at = begin;
+#pragma unroll 4
   for (int i = begin + PIECE * threadIdx.x; i < end; i += PIECE * SLICE_THREADS) {
     float v[PIECE];
     load_piece<TYPE>(x, i, end, v);
+    float hi = v[0], lo = v[0];
 #pragma unroll
-    for (int e = 0; e < PIECE; ++e) {
-      const unsigned long long b = (unsigned long long)key_of(v[e]) << 32 | (uint32_t)~(i + e);
-      best = b > best ? b : best;
-      least = v[e] > NEG_INF ? fminf(least, v[e]) : least;
+    for (int e = 1; e < PIECE; ++e) hi = fmaxf(hi, v[e]), lo = fminf(lo, v[e]);
+    // (seldom, after the first pieces; elements come by rising index, so the
+    // first of equal ones stays)
+    if (hi > most) {
+      most = hi;
+#pragma unroll
+      for (int e = PIECE - 1; e >= 0; --e) at = v[e] == hi ? i + e : at;
     }
+    if (lo == NEG_INF) {
+      lo = __builtin_inff();
+#pragma unroll
+      for (int e = 0; e < PIECE; ++e) lo = v[e] > NEG_INF ? fminf(lo, v[e]) : lo;
+    }
+    least = fminf(least, lo);
   }
-  best = wave_max64(best);
+  unsigned long long best = wave_max64((unsigned long long)key_of(most) << 32 | (uint32_t)~at);
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) least = fminf(least, __shfl_xor(least, d));
   if ((threadIdx.x & 63) == 0) {
@@ -281,76 +344,87 @@ __global__ void __launch_bounds__(SLICE_THREADS) sample_scan_kernel(SampleArgs a
       least = fminf(least, __uint_as_float((uint32_t)red[SLICE_THREADS / 64 + i]));
     }
     w.parts[(int64_t)row * slices + s] = Part{(uint32_t)(best >> 32), (int)~(uint32_t)best, least, 0};
+    if (s == 0) w.listed[row] = 0;
   }
   // the row's histogram starts at 0, a part of it by each slice
   if (a.top_k || a.top_p)
-    for (int i = s * SLICE_THREADS + threadIdx.x; i < BINS; i += slices * SLICE_THREADS) {
-      w.weights[(int64_t)row * BINS + i] = 0;
-      w.counts[(int64_t)row * BINS + i] = 0;
-    }
+    for (int i = s * SLICE_THREADS + threadIdx.x; i < BINS; i += slices * SLICE_THREADS) w.bins[(int64_t)row * BINS + i] = 0;
 }
 
+// Counts (with top-k) or weights (with top-p alone) by bins.
 template <int TYPE>
-__global__ void __launch_bounds__(SLICE_THREADS) sample_histogram_kernel(SampleArgs a, int slices, int slice) {
+__global__ void __launch_bounds__(SLICE_THREADS) sample_bins_kernel(SampleArgs a, int slices, int slice) {
   __shared__ unsigned long long red[2 * SLICE_THREADS / 64];
-  __shared__ unsigned long long weights[BINS];
-  __shared__ uint32_t counts[BINS];
+  __shared__ unsigned long long bins[BINS];
   const int row = blockIdx.x / slices, s = blockIdx.x % slices;
   const Settings set(a, row);
-  if (!set.cuts()) return;
+  const bool by_count = set.by_count(a.vocab);
+  if (set.greedy || !(by_count || set.by_weight())) return;
   const Work w(a.ws, a.rows, slices);
-  for (int i = threadIdx.x; i < BINS; i += SLICE_THREADS) weights[i] = 0, counts[i] = 0;
+  for (int i = threadIdx.x; i < BINS; i += SLICE_THREADS) bins[i] = 0;
   const Top top = top_of<SLICE_THREADS>(w.parts + (int64_t)row * slices, slices, red);  // (with barriers)
   const Binning bin(top);
   const Weigh weigh{(double)top.most(), set.by};
   const int begin = s * slice, end = min(begin + slice, a.vocab);
   const void* x = static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes;
+  uint32_t* counts = reinterpret_cast<uint32_t*>(bins);
+#pragma unroll 2
   for (int i = begin + PIECE * threadIdx.x; i < end; i += PIECE * SLICE_THREADS) {
     float v[PIECE];
     load_piece<TYPE>(x, i, end, v);
+    if (by_count) {
 #pragma unroll
-    for (int e = 0; e < PIECE; ++e) {
-      if (v[e] == NEG_INF) continue;
-      const int b = bin(v[e]);
-      atomicAdd(&counts[b], 1u);
-      if (set.p < 1.0) {
+      for (int e = 0; e < PIECE; ++e)
+        if (v[e] != NEG_INF) atomicAdd(&counts[bin(v[e])], 1u);
+    } else {
+#pragma unroll
+      for (int e = 0; e < PIECE; ++e) {
         const unsigned long long f = fixed(weigh(v[e]));
-        if (f) atomicAdd(&weights[b], f);
+        if (f) atomicAdd(&bins[bin(v[e])], f);
       }
     }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < BINS; i += SLICE_THREADS) {
-    if (counts[i]) atomicAdd(&w.counts[(int64_t)row * BINS + i], counts[i]);
-    if (weights[i]) atomicAdd(&w.weights[(int64_t)row * BINS + i], weights[i]);
+    const unsigned long long f = by_count ? counts[i] : bins[i];
+    if (f) atomicAdd(&w.bins[(int64_t)row * BINS + i], f);
   }
 }
 
-// the weights that a slice keeps
+// The slice's elements of the bin in which the prefix ends go into the list (or
+// those of all bins up to it); the weights that it keeps of the bins in front of
+// it are summed.
 template <int TYPE>
 __global__ void __launch_bounds__(SLICE_THREADS) sample_sums_kernel(SampleArgs a, int slices, int slice) {
   __shared__ unsigned long long red[2 * SLICE_THREADS / 64];
+  __shared__ Plan plan_s;
   const int row = blockIdx.x / slices, s = blockIdx.x % slices;
   const Work w(a.ws, a.rows, slices);
   const Settings set(a, row);
   if (set.greedy) return;
-  Cut cut{0, 0, 0, 0};
-  if (a.top_k || a.top_p) cut = w.cuts[row];
-  if (cut.done) return;
+  const Plan plan = plan_of<SLICE_THREADS>(a, set, w.bins + (int64_t)row * BINS, red, &plan_s);
+  if (plan.mode == CUT_MANY) return;
   const Top top = top_of<SLICE_THREADS>(w.parts + (int64_t)row * slices, slices, red);
+  const Binning bin(top);
   const Weigh weigh{(double)top.most(), set.by};
   const int begin = s * slice, end = min(begin + slice, a.vocab);
   const void* x = static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes;
   unsigned long long sum = 0;
+#pragma unroll 2
   for (int i = begin + PIECE * threadIdx.x; i < end; i += PIECE * SLICE_THREADS) {
     float v[PIECE];
     load_piece<TYPE>(x, i, end, v);
 #pragma unroll
     for (int e = 0; e < PIECE; ++e) {
-      const uint32_t key = key_of(v[e]);
-      if (v[e] == NEG_INF || key < cut.key || (key == cut.key && i + e > cut.at)) continue;
-      const double p = weigh(v[e]);
-      sum += p >= set.least ? fixed(p) : 0;
+      const int b = plan.mode == CUT_NONE ? 0 : bin(v[e]);
+      if (plan.mode != CUT_FEW && b < plan.bin) {
+        const double p = weigh(v[e]);
+        sum += p >= set.least ? fixed(p) : 0;
+      }
+      if (plan.mode != CUT_NONE && (plan.mode == CUT_FEW ? b <= plan.bin : b == plan.bin) && v[e] != NEG_INF) {
+        const int at = atomicAdd(&w.listed[row], 1);
+        if (at < CAP) w.list[(int64_t)row * CAP + at] = (unsigned long long)~key_of(v[e]) << 32 | (uint32_t)(i + e);
+      }
     }
   }
   sum = wave_scan64(sum);
@@ -375,40 +449,75 @@ __device__ __forceinline__ unsigned long long target_of(float u, unsigned long l
   return t < (double)total ? (unsigned long long)t : total - 1;
 }
 
-// Sorts list[0 .. n) (n a power of two) upwards; the whole workgroup.
-__device__ __forceinline__ void sort(unsigned long long* list, int n) {
-  for (int k = 2; k <= n; k <<= 1)
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      __syncthreads();
-      for (int t = threadIdx.x; t < n / 2; t += THREADS) {
-        const int i = ((t & ~(j - 1)) << 1) | (t & (j - 1)), o = i | j;
-        const unsigned long long x = list[i], y = list[o];
-        if ((x > y) == ((i & k) == 0)) list[i] = y, list[o] = x;
-      }
-    }
-  __syncthreads();
-}
 __device__ __forceinline__ int power_of_two(int n) { return n < 2 ? 1 : 1 << (32 - __builtin_clz(n - 1)); }
-
-struct Shared {
-  unsigned long long list[CAP];
-  unsigned long long weights[BINS];  // up to and with the bin
-  uint32_t counts[BINS];
-  unsigned long long red[2 * THREADS / 64];
-  unsigned long long found;
-  uint32_t key0, key1;
-  int n, bin;
-};
 
 constexpr int EACH = CAP / THREADS;  // entries of a thread
 
+struct Shared {
+  unsigned long long list[CAP];
+  unsigned long long bins[BINS];  // of counts or weights, up to and with the bin
+  unsigned long long counts[BINS];
+  unsigned long long red[2 * THREADS / 64];
+  unsigned long long found;
+  Plan plan;
+  uint32_t key0, key1;
+  int n, at;
+};
+
+// Sorts list[0 .. n) (n a power of two up to CAP) upwards; the whole workgroup.
+// Up to an entry a thread they stay in registers: partners within a wave change
+// places by lanes, others through the list.
+__device__ __forceinline__ void sort(unsigned long long* list, int n) {
+  __syncthreads();
+  if (n <= THREADS) {
+    const int t = threadIdx.x;
+    unsigned long long v = t < n ? list[t] : 0;
+    for (int k = 2; k <= n; k <<= 1)
+      for (int j = k >> 1; j > 0; j >>= 1) {
+        unsigned long long o;
+        if (j >= 64) {
+          __syncthreads();
+          if (t < n) list[t] = v;
+          __syncthreads();
+          o = t < n ? list[t ^ j] : 0;
+        } else {
+          o = __shfl_xor(v, j);
+        }
+        const bool low = ((t & j) == 0) == ((t & k) == 0);  // this place takes the smaller one
+        v = (o < v) == low ? o : v;
+      }
+    __syncthreads();
+    if (t < n) list[t] = v;
+  } else {
+    for (int k = 2; k <= n; k <<= 1)
+      for (int j = k >> 1; j > 0; j >>= 1) {
+        __syncthreads();
+        for (int t = threadIdx.x; t < n / 2; t += THREADS) {
+          const int i = ((t & ~(j - 1)) << 1) | (t & (j - 1)), o = i | j;
+          const unsigned long long x = list[i], y = list[o];
+          if ((x > y) == ((i & k) == 0)) list[i] = y, list[o] = x;
+        }
+      }
+  }
+  __syncthreads();
+}
+
+// A row with all that its workgroup needs.  List entries: ~key << 32 | index, so
+// rising entries are falling logits, equal ones by index.
 template <int TYPE>
-struct RowCut {
+struct OneRow {
   const SampleArgs& a;
+  const Settings& set;
   Shared& sh;
   const void* x;
   const Binning bin;
   const Weigh weigh;
+
+  __device__ __forceinline__ static uint32_t key_in(unsigned long long entry) { return ~(uint32_t)(entry >> 32); }
+  __device__ __forceinline__ unsigned long long weight_of(uint32_t key) const { return fixed(weigh(logit_of(key))); }
+  __device__ __forceinline__ unsigned long long scan(unsigned long long v, unsigned long long& total) const {
+    return block_scan64<THREADS>(v, total, sh.red);
+  }
 
   // f(logit, index) for the row's elements that are not -infinity
   template <typename F>
@@ -422,51 +531,12 @@ struct RowCut {
         if (v[e] != NEG_INF) f(v[e], i + e);
     }
   }
-  // Sorted entries: ~key << 32 | index, so falling logits, rising indexes.
-  __device__ __forceinline__ static uint32_t key_in(unsigned long long entry) { return ~(uint32_t)(entry >> 32); }
-  __device__ __forceinline__ unsigned long long weight_in(unsigned long long entry) const {
-    return fixed(weigh(logit_of(key_in(entry))));
-  }
 
-  // The first bin up to which sums(bin) reaches what is wanted (reaches: false,
-  // ..., false, true, ...), or the last one.
-  template <typename F>
-  __device__ __forceinline__ int first_bin(F&& reaches) const {
-    if (threadIdx.x == 0) sh.bin = BINS - 1;
-    __syncthreads();
-    const int b = threadIdx.x;
-    if (reaches(b) && (b == 0 || !reaches(b - 1))) sh.bin = b;
-    __syncthreads();
-    const int r = sh.bin;
-    __syncthreads();
-    return r;
-  }
-  // Turns the bins' own counts and weights (a bin a thread) into sums up to them.
-  __device__ __forceinline__ void sum_bins(uint32_t count, unsigned long long weight) const {
-    unsigned long long all;
-    const unsigned long long c = block_scan64(count, all, sh.red), s = block_scan64(weight, all, sh.red);
-    sh.counts[threadIdx.x] = (uint32_t)c;
-    sh.weights[threadIdx.x] = s;
-    __syncthreads();
-  }
-
-  // Puts the elements that `in` accepts into the list (at most CAP) and sorts
-  // them; the entries behind them are the largest.
-  template <typename F>
-  __device__ __forceinline__ int gather(F&& in) const {
-    if (threadIdx.x == 0) sh.n = 0;
-    __syncthreads();
-    each([&](float l, int i) {
-      if (in(l)) {
-        const int at = atomicAdd(&sh.n, 1);
-        if (at < CAP) sh.list[at] = (unsigned long long)~key_of(l) << 32 | (uint32_t)i;
-      }
-    });
-    __syncthreads();
-    const int n = min(sh.n, CAP), m = power_of_two(n);
+  // Sorts the n entries that are in the list.
+  __device__ __forceinline__ void order(int n) const {
+    const int m = power_of_two(n);
     for (int i = n + threadIdx.x; i < m; i += THREADS) sh.list[i] = ~0ull;
     sort(sh.list, m);
-    return n;
   }
   // the weights of a thread's entries EACH * t .. and the sum in front of them
   __device__ __forceinline__ unsigned long long scan_list(int n, unsigned long long (&w)[EACH], unsigned long long& total) const {
@@ -474,96 +544,124 @@ struct RowCut {
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
       const int j = EACH * threadIdx.x + e;
-      w[e] = j < n ? weight_in(sh.list[j]) : 0;
+      w[e] = j < n ? weight_of(key_in(sh.list[j])) : 0;
       mine += w[e];
     }
-    return block_scan64(mine, total, sh.red) - mine;
+    return scan(mine, total) - mine;
+  }
+  // The last of the n sorted entries that stays.  By count: the `want`th (from
+  // 1).  By weight: the last with less than `goal` in front of it, `before` of
+  // that in front of the list (the first one, if none has).  `upto`: the weights
+  // up to and with it.
+  __device__ __forceinline__ int last_of(int n, bool by_weight, uint32_t want, unsigned long long before, double goal,
+                                         unsigned long long& upto) const {
+    unsigned long long w[EACH], total, sum = scan_list(n, w, total), at = sum;
+    if (threadIdx.x == 0) sh.at = by_weight ? 0 : max((int)min(want, (uint32_t)n) - 1, 0);
+    __syncthreads();
+    int last = 0;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+      const int j = EACH * threadIdx.x + e;
+      last = j < n && (double)(before + at) < goal ? j : last;
+      at += w[e];
+    }
+    if (by_weight && last) atomicMax(&sh.at, last);
+    __syncthreads();
+    const int j = sh.at;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+      sum += w[e];
+      if (EACH * (int)threadIdx.x + e == j) sh.found = sum;
+    }
+    __syncthreads();
+    upto = sh.found;
+    __syncthreads();
+    return j;
   }
 
-  // The end of a prefix inside bin b.  By count: its `want`th element (from 1).
-  // By weight: the last element in front of which the weights, `before` in front
-  // of the bin, are less than `goal` (the bin's first, where goal is 0).  Returns
-  // the cut and, in `upto`, the bin's weights up to and with it.
-  __device__ __forceinline__ Cut end_in(int b, bool by_weight, uint32_t want, unsigned long long before, double goal,
-                                        unsigned long long& upto) const {
-    uint32_t low = 0, high = ~0u;  // keys looked at
-    uint32_t n = sh.counts[b] - (b ? sh.counts[b - 1] : 0);
-    unsigned long long inside = 0;  // weights of the bin above `high`
+  // The first bin up to which sums reach a goal, as reaches(bin) says (false,
+  // ..., false, true, ...), or the last one.
+  template <typename F>
+  __device__ __forceinline__ int first_bin(F&& reaches) const {
+    if (threadIdx.x == 0) sh.at = BINS - 1;
+    __syncthreads();
+    const int b = threadIdx.x;
+    if (reaches(b) && (b == 0 || !reaches(b - 1))) sh.at = b;
+    __syncthreads();
+    const int r = sh.at;
+    __syncthreads();
+    return r;
+  }
+
+  // The end of a prefix anywhere in the row, by the row itself: where the list
+  // cannot say (thousands of elements in one bin, or both criteria over as many).
+  // Counts and weights by ranges of keys, each 1024th of the last, until the
+  // range in which the prefix ends has few elements, or one key.
+  __device__ __forceinline__ Cut search(bool by_weight, uint32_t want, double goal, unsigned long long& upto) const {
+    uint32_t low = 0, high = ~0u;
+    unsigned long long inside = 0;  // weights above `high`
     auto in = [&](float l) {
       const uint32_t k = key_of(l);
-      return bin(l) == b && k >= low && k <= high;
+      return k >= low && k <= high;
     };
-    while (n > CAP) {
-      // too many: bins of key ranges, until few are left or all are equal
+    uint32_t n = 0;
+    for (;;) {
       __syncthreads();
-      if (threadIdx.x == 0) sh.key0 = ~0u, sh.key1 = 0;
+      if (threadIdx.x == 0) sh.key0 = ~0u, sh.key1 = 0, sh.n = 0;
+      sh.counts[threadIdx.x] = 0;
+      sh.bins[threadIdx.x] = 0;
       __syncthreads();
       uint32_t k0 = ~0u, k1 = 0;
+      int mine = 0;
       each([&](float l, int) {
-        if (in(l)) k0 = min(k0, key_of(l)), k1 = max(k1, key_of(l));
+        if (in(l)) k0 = min(k0, key_of(l)), k1 = max(k1, key_of(l)), ++mine;
       });
-      if (k0 <= k1) atomicMin(&sh.key0, k0), atomicMax(&sh.key1, k1);
+      if (mine) atomicMin(&sh.key0, k0), atomicMax(&sh.key1, k1), atomicAdd(&sh.n, mine);
       __syncthreads();
-      low = sh.key0, high = sh.key1;
-      if (low == high) break;
+      low = sh.key0, high = sh.key1, n = sh.n;
+      want = min(want, n);
+      if (n <= CAP || low == high) break;
       const int shift = max(0, 32 - __builtin_clz(high - low) - 10);
-      sh.counts[threadIdx.x] = 0;
-      sh.weights[threadIdx.x] = 0;
-      __syncthreads();
       each([&](float l, int) {
         if (!in(l)) return;
         const uint32_t r = (high - key_of(l)) >> shift;
-        atomicAdd(&sh.counts[r], 1u);
-        atomicAdd(&sh.weights[r], fixed(weigh(l)));
+        atomicAdd(&sh.counts[r], 1ull);
+        atomicAdd(&sh.bins[r], fixed(weigh(l)));
       });
       __syncthreads();
-      const uint32_t c = sh.counts[threadIdx.x];
-      const unsigned long long s = sh.weights[threadIdx.x];
+      unsigned long long all;
+      const unsigned long long c = scan(sh.counts[threadIdx.x], all), w = scan(sh.bins[threadIdx.x], all);
+      sh.counts[threadIdx.x] = c;
+      sh.bins[threadIdx.x] = w;
       __syncthreads();
-      sum_bins(c, s);
       const int r = first_bin([&](int i) {
-        return by_weight ? (double)(before + inside + sh.weights[i]) >= goal : sh.counts[i] >= want;
+        return by_weight ? (double)(inside + sh.bins[i]) >= goal : sh.counts[i] >= want;
       });
-      n = sh.counts[r] - (r ? sh.counts[r - 1] : 0);
-      want -= r ? sh.counts[r - 1] : 0;
-      inside += r ? sh.weights[r - 1] : 0;
+      want -= r ? (uint32_t)sh.counts[r - 1] : 0;
+      inside += r ? sh.bins[r - 1] : 0;
       const uint32_t h = high - ((uint32_t)r << shift), l = h - ((1u << shift) - 1);
       high = h;
       low = l > h || l < low ? low : l;
     }
     if (n <= CAP) {
-      n = gather(in);
-      unsigned long long w[EACH], total;
-      unsigned long long sum = scan_list(n, w, total);
-      if (threadIdx.x == 0) sh.bin = by_weight ? 0 : (int)min(want, n) - 1;
+      if (threadIdx.x == 0) sh.n = 0;
       __syncthreads();
-      int last = 0;  // the last entry that the weights in front of it leave in
-      unsigned long long at = sum;
-#pragma unroll
-      for (int e = 0; e < EACH; ++e) {
-        const int j = EACH * threadIdx.x + e;
-        last = j < (int)n && (double)(before + inside + at) < goal ? j : last;
-        at += w[e];
-      }
-      if (by_weight && last) atomicMax(&sh.bin, last);
+      each([&](float l, int i) {
+        if (in(l)) sh.list[atomicAdd(&sh.n, 1)] = (unsigned long long)~key_of(l) << 32 | (uint32_t)i;
+      });
       __syncthreads();
-      const int j = max(sh.bin, 0);
-#pragma unroll
-      for (int e = 0; e < EACH; ++e) {
-        sum += w[e];
-        if (EACH * (int)threadIdx.x + e == j) sh.found = sum;
-      }
-      __syncthreads();
-      upto = inside + sh.found;
+      order(n);
+      const int j = last_of(n, by_weight, want, inside, goal, upto);
+      upto += inside;
       const unsigned long long entry = sh.list[j];
       __syncthreads();
-      return Cut{key_in(entry), (int)(uint32_t)entry, 0, 0};
+      return Cut{key_in(entry), (int)(uint32_t)entry};
     }
     // all equal: the one of their number `m`, in the order of the vocabulary
-    const unsigned long long w = fixed(weigh(logit_of(high)));
+    const unsigned long long w = weight_of(high);
     uint32_t m = want;
     if (by_weight) {
-      const double need = goal - (double)(before + inside);
+      const double need = goal - (double)inside;
       m = need > 0.0 ? (w ? (uint32_t)fmin(ceil(need / (double)w), (double)n) : n) : 1;
     }
     m = max(1u, min(m, n));
@@ -578,190 +676,149 @@ struct RowCut {
         for (int e = 0; e < PIECE; ++e) mine += v[e] != NEG_INF && key_of(v[e]) == high;
       }
       unsigned long long all;
-      uint32_t at = seen + (uint32_t)block_scan64(mine, all, sh.red) - mine;
+      uint32_t at = seen + (uint32_t)scan(mine, all) - mine;
       if (mine)
 #pragma unroll
         for (int e = 0; e < PIECE; ++e)
-          if (v[e] != NEG_INF && key_of(v[e]) == high && ++at == m) sh.bin = i + e;
+          if (v[e] != NEG_INF && key_of(v[e]) == high && ++at == m) sh.at = i + e;
       seen += (uint32_t)all;
     }
     __syncthreads();
-    const int place = sh.bin;
+    const int place = sh.at;
     __syncthreads();
     upto = inside + (unsigned long long)m * w;
-    return Cut{high, place, 0, 0};
+    return Cut{high, place};
+  }
+
+  // The token, among elements [begin, end): the first up to which the kept
+  // weights, `before` in front, pass t; returns the weights up to the end.  (Where
+  // they do not pass it nothing is written.)
+  __device__ __forceinline__ unsigned long long draw(int begin, int end, Cut cut, unsigned long long before,
+                                                     unsigned long long t, int32_t* out) const {
+    for (int i0 = begin; i0 < end && before <= t; i0 += PIECE * THREADS) {
+      const int i = i0 + PIECE * threadIdx.x;
+      unsigned long long w[PIECE], sum = 0, all;
+      float v[PIECE];
+      if (i < end) load_piece<TYPE>(x, i, end, v);
+#pragma unroll
+      for (int e = 0; e < PIECE; ++e) {
+        w[e] = 0;
+        if (i + e >= end || v[e] == NEG_INF) continue;
+        const uint32_t key = key_of(v[e]);
+        if (key < cut.key || (key == cut.key && i + e > cut.at)) continue;
+        const double p = weigh(v[e]);
+        w[e] = p >= set.least ? fixed(p) : 0;
+        sum += w[e];
+      }
+      unsigned long long at = before + scan(sum, all) - sum;
+#pragma unroll
+      for (int e = 0; e < PIECE; ++e) {
+        if (at <= t && t < at + w[e]) *out = i + e;
+        at += w[e];
+      }
+      before += all;
+    }
+    return before;
   }
 };
 
-// Where the row's prefix ends, or, where it has few elements, its token.
 template <int TYPE>
-__global__ void __launch_bounds__(THREADS) sample_cut_kernel(SampleArgs a, int slices) {
+__global__ void __launch_bounds__(THREADS) sample_draw_kernel(SampleArgs a, int slices, int slice) {
   __shared__ Shared sh;
   const int row = blockIdx.x;
-  const Settings set(a, row);
-  if (set.greedy) return;
   const Work wk(a.ws, a.rows, slices);
-  if (!set.cuts()) {
-    if (threadIdx.x == 0) wk.cuts[row] = Cut{0, 0, 0, 0};
-    return;
-  }
+  const Settings set(a, row);
+  int32_t* out = a.out + row;
+  const float u = a.u[row];
+  const int listed = wk.listed[row];
   const Top top = top_of<THREADS>(wk.parts + (int64_t)row * slices, slices, sh.red);
-  const RowCut<TYPE> r{a, sh, static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes, Binning(top),
-                       Weigh{(double)top.most(), set.by}};
-  r.sum_bins(wk.counts[(int64_t)row * BINS + threadIdx.x], wk.weights[(int64_t)row * BINS + threadIdx.x]);
-  const uint32_t all = sh.counts[BINS - 1];
-  const bool by_count = set.k > 0 && (uint32_t)set.k < all, by_weight = set.p < 1.0;
-  if (!by_count && !by_weight) {
-    if (threadIdx.x == 0) wk.cuts[row] = Cut{0, 0, 0, 0};
+  if (set.greedy || top.most() == NEG_INF) {
+    if (threadIdx.x == 0) *out = top.most() == NEG_INF ? -1 : top.place();
     return;
   }
-  // the last bin that the prefix can reach
-  int last = BINS - 1;
-  if (by_count) last = r.first_bin([&](int b) { return sh.counts[b] >= (uint32_t)set.k; });
-  if (by_weight && !by_count) {
-    const double goal = set.p * (double)sh.weights[BINS - 1];
-    last = r.first_bin([&](int b) { return (double)sh.weights[b] >= goal; });
+  const OneRow<TYPE> r{a, set, sh, static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes, Binning(top),
+                       Weigh{(double)top.most(), set.by}};
+  const Plan plan = plan_of<THREADS>(a, set, wk.bins + (int64_t)row * BINS, sh.red, &sh.plan);
+  const bool by_count = set.by_count(a.vocab), by_weight = set.by_weight();
+  unsigned long long total, upto;
+
+  if (plan.mode == CUT_MANY || (plan.mode != CUT_NONE && listed > CAP)) {
+    // the row alone, from its logits
+    Cut cut{0, 0};
+    double goal = plan.goal;
+    if (by_count) {
+      cut = r.search(false, (uint32_t)set.k, 0.0, upto);
+      goal = set.p * (double)upto;
+    }
+    if (by_weight) cut = r.search(true, 1, goal, upto);
+    total = r.draw(0, a.vocab, cut, 0, ~0ull >> 1, out);
+    r.draw(0, a.vocab, cut, 0, target_of(u, total), out);
+    return;
   }
-  if (sh.counts[last] <= CAP) {
-    // few: all of them in the list, and the token from it
-    const int n = r.gather([&](float l) { return r.bin(l) <= last; });
-    unsigned long long w[EACH], total, sum;
-    if (n == 0) {  // (no logit above -infinity)
-      if (threadIdx.x == 0) wk.cuts[row] = Cut{0, 0, 0, 0};
-      return;
-    }
-    sum = r.scan_list(n, w, total);
-    const int nk = by_count ? min(set.k, n) : n;
-    if (by_count) {  // the sum of the first nk
-      unsigned long long s = sum;
-#pragma unroll
-      for (int e = 0; e < EACH; ++e) {
-        s += w[e];
-        if (EACH * (int)threadIdx.x + e == nk - 1) sh.found = s;
-      }
-      __syncthreads();
-      total = sh.found;
-    } else {
-      total = sh.weights[BINS - 1];  // (of the row, not of the list)
-    }
-    const double goal = set.p * (double)total;
-    if (threadIdx.x == 0) sh.n = 1;
+
+  const int n = plan.mode == CUT_NONE ? 0 : listed;
+  if (n) {
+    for (int i = threadIdx.x; i < n; i += THREADS) sh.list[i] = wk.list[(int64_t)row * CAP + i];
     __syncthreads();
-    int kept = 0;
-#pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-      const int j = EACH * threadIdx.x + e;
-      const bool keep = j < nk && (j == 0 || !by_weight || (double)sum < goal) &&
-                        r.weigh(logit_of(r.key_in(sh.list[j < n ? j : 0]))) >= set.least;
-      kept = keep ? j + 1 : kept;
-      sum += w[e];
-    }
-    if (kept) atomicMax(&sh.n, kept);
-    __syncthreads();
-    const int m = sh.n, m2 = power_of_two(m);
-    // ... in the order of the vocabulary
-    unsigned long long entry[EACH];
+    r.order(n);
+  }
+
+  if (plan.mode == CUT_FEW) {
+    int kept = by_count ? min(set.k, n) : n;
+    r.last_of(n, false, (uint32_t)kept, 0, 0.0, upto);
+    if (by_weight) kept = min(kept, 1 + r.last_of(n, true, 1, 0, set.p * (double)upto, upto));
+    // (min-p keeps a prefix of these; then by index)
+    unsigned long long entry[EACH], w[EACH], mine = 0;
 #pragma unroll
     for (int e = 0; e < EACH; ++e) entry[e] = sh.list[EACH * threadIdx.x + e];
     __syncthreads();
+    const int m = power_of_two(kept);
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
       const int j = EACH * threadIdx.x + e;
-      if (j < m2) sh.list[j] = j < m ? entry[e] << 32 | entry[e] >> 32 : ~0ull;
+      const bool stays = j < kept && (j == 0 || r.weigh(logit_of(r.key_in(entry[e]))) >= set.least);
+      if (j < m) sh.list[j] = stays ? entry[e] << 32 | entry[e] >> 32 : ~0ull;
     }
-    sort(sh.list, m2);
-    unsigned long long mine = 0;
+    sort(sh.list, m);
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
       const int j = EACH * threadIdx.x + e;
-      entry[e] = j < m ? sh.list[j] : 0;
-      w[e] = j < m ? fixed(r.weigh(logit_of(~(uint32_t)entry[e]))) : 0;
+      entry[e] = j < m ? sh.list[j] : ~0ull;
+      w[e] = entry[e] != ~0ull ? r.weight_of(~(uint32_t)entry[e]) : 0;
       mine += w[e];
     }
-    sum = block_scan64(mine, total, sh.red) - mine;
-    const unsigned long long t = target_of(a.u[row], total);
+    unsigned long long sum = r.scan(mine, total) - mine;
+    const unsigned long long t = target_of(u, total);
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
-      if (sum <= t && t < sum + w[e]) a.out[row] = (int)(entry[e] >> 32);
+      if (sum <= t && t < sum + w[e]) *out = (int)(entry[e] >> 32);
       sum += w[e];
     }
-    if (threadIdx.x == 0) wk.cuts[row] = Cut{0, 0, 1, 0};
     return;
   }
-  // many: where the prefix ends
-  Cut cut{0, 0, 0, 0};
-  unsigned long long total = sh.weights[BINS - 1], upto;
-  const unsigned long long upto_last = last ? sh.weights[last - 1] : 0;
-  const unsigned long long mine_w = sh.weights[threadIdx.x];  // (end_in may use the bins for its own)
-  const uint32_t mine_c = sh.counts[threadIdx.x];
-  if (by_count) {
-    cut = r.end_in(last, false, (uint32_t)set.k - (last ? sh.counts[last - 1] : 0), upto_last, 0.0, upto);
-    total = upto_last + upto;
-    sh.weights[threadIdx.x] = mine_w;
-    sh.counts[threadIdx.x] = mine_c;
-    __syncthreads();
-  }
-  if (by_weight) {
-    const double goal = set.p * (double)total;
-    const int b = min(last, r.first_bin([&](int i) { return (double)sh.weights[i] >= goal; }));
-    cut = r.end_in(b, true, 1, b ? sh.weights[b - 1] : 0, goal, upto);
-  }
-  if (threadIdx.x == 0) wk.cuts[row] = cut;
-}
 
-// The token of a row whose prefix is known: the slice in which the draw falls,
-// then the element.
-template <int TYPE>
-__global__ void __launch_bounds__(THREADS) sample_draw_kernel(SampleArgs a, int slices, int slice) {
-  __shared__ unsigned long long red[2 * THREADS / 64];
-  __shared__ unsigned long long before_s;
-  __shared__ int slice_s;
-  const int row = blockIdx.x;
-  const Work wk(a.ws, a.rows, slices);
-  const Settings set(a, row);
-  Cut cut{0, 0, 0, 0};
-  if (!set.greedy && (a.top_k || a.top_p)) cut = wk.cuts[row];
-  if (cut.done) return;
-  if (threadIdx.x == 0) slice_s = 0, before_s = 0;
-  const Top top = top_of<THREADS>(wk.parts + (int64_t)row * slices, slices, red);  // (with barriers)
-  if (set.greedy || top.most() == NEG_INF) {
-    if (threadIdx.x == 0) a.out[row] = top.most() == NEG_INF ? -1 : top.place();
-    return;
+  // the slices' sums, and to each what it keeps of the list (sh.bins: a slice a
+  // thread)
+  sh.bins[threadIdx.x] = (int)threadIdx.x < slices ? wk.sums[(int64_t)row * slices + threadIdx.x] : 0;
+  if (threadIdx.x == 0) sh.key0 = 0, sh.found = 0;
+  Cut cut{0, 0};
+  if (n) {
+    const int last = r.last_of(n, !by_count, by_count ? (uint32_t)(set.k - (int)plan.before) : 1, plan.before, plan.goal, upto);
+    const unsigned long long entry = sh.list[last];
+    cut = Cut{r.key_in(entry), (int)(uint32_t)entry};
+    for (int j = threadIdx.x; j <= last; j += THREADS) {
+      const double p = r.weigh(logit_of(r.key_in(sh.list[j])));
+      const uint32_t i = (uint32_t)sh.list[j];
+      if (p >= set.least) atomicAdd(&sh.bins[i / (uint32_t)slice], fixed(p));
+    }
   }
-  const Weigh weigh{(double)top.most(), set.by};
-  unsigned long long total;
-  const unsigned long long mine = (int)threadIdx.x < slices ? wk.sums[(int64_t)row * slices + threadIdx.x] : 0;
-  const unsigned long long upto = block_scan64(mine, total, red);
-  const unsigned long long t = target_of(a.u[row], total);
-  if (upto - mine <= t && t < upto) slice_s = threadIdx.x, before_s = upto - mine;
   __syncthreads();
-  const int begin = slice_s * slice, end = min(begin + slice, a.vocab);
-  unsigned long long before = before_s;
-  const void* x = static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes;
-  for (int i0 = begin; i0 < end; i0 += PIECE * THREADS) {
-    const int i = i0 + PIECE * threadIdx.x;
-    unsigned long long w[PIECE], sum = 0, all;
-    float v[PIECE];
-    if (i < end) load_piece<TYPE>(x, i, end, v);
-#pragma unroll
-    for (int e = 0; e < PIECE; ++e) {
-      w[e] = 0;
-      if (i + e >= end || v[e] == NEG_INF) continue;
-      const uint32_t key = key_of(v[e]);
-      if (key < cut.key || (key == cut.key && i + e > cut.at)) continue;
-      const double p = weigh(v[e]);
-      w[e] = p >= set.least ? fixed(p) : 0;
-      sum += w[e];
-    }
-    unsigned long long at = before + block_scan64(sum, all, red) - sum;
-#pragma unroll
-    for (int e = 0; e < PIECE; ++e) {
-      if (at <= t && t < at + w[e]) a.out[row] = i + e;
-      at += w[e];
-    }
-    before += all;
-    if (before > t) break;
-  }
+  const unsigned long long mine = sh.bins[threadIdx.x], here = r.scan(mine, total);
+  const unsigned long long t = target_of(u, total);
+  if (here - mine <= t && t < here) sh.key0 = threadIdx.x, sh.found = here - mine;
+  __syncthreads();
+  const int begin = (int)sh.key0 * slice, end = min(begin + slice, a.vocab);
+  r.draw(begin, end, cut, sh.found, t, out);
 }
 
 // Logits of a slice: about 1024 workgroups over all rows, between 2048 and
@@ -780,10 +837,7 @@ hipError_t launch(const SampleArgs& a, hipStream_t s) {
   const int slice = slice_of(a.rows, a.vocab), slices = slices_of(a.rows, a.vocab);
   const dim3 grid((unsigned)a.rows * (unsigned)slices), rows((unsigned)a.rows);
   hipLaunchKernelGGL(sample_scan_kernel<TYPE>, grid, dim3(SLICE_THREADS), 0, s, a, slices, slice);
-  if (a.top_k || a.top_p) {
-    hipLaunchKernelGGL(sample_histogram_kernel<TYPE>, grid, dim3(SLICE_THREADS), 0, s, a, slices, slice);
-    hipLaunchKernelGGL(sample_cut_kernel<TYPE>, rows, dim3(THREADS), 0, s, a, slices);
-  }
+  if (a.top_k || a.top_p) hipLaunchKernelGGL(sample_bins_kernel<TYPE>, grid, dim3(SLICE_THREADS), 0, s, a, slices, slice);
   hipLaunchKernelGGL(sample_sums_kernel<TYPE>, grid, dim3(SLICE_THREADS), 0, s, a, slices, slice);
   hipLaunchKernelGGL(sample_draw_kernel<TYPE>, rows, dim3(THREADS), 0, s, a, slices, slice);
   return hipGetLastError();
