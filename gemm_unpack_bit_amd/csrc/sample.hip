@@ -175,22 +175,48 @@ struct Settings {
   __device__ __forceinline__ bool by_weight() const { return p < 1.0; }
 };
 
-// max over a wave; sums over the wave's lanes up to and with the lane's
-__device__ __forceinline__ unsigned long long wave_max64(unsigned long long v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const unsigned long long o = __shfl_xor(v, d);
-    v = o > v ? o : v;
+// Lane moves of 64-bit values without a detour through LDS: the value of lane
+// ^ J, and sums over the wave's lanes up to and with the lane's.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ uint32_t dpp32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+template <int J>
+__device__ __forceinline__ uint32_t lane_xor32(uint32_t v) {
+  if constexpr (J == 1) return dpp32<DPP_QP_XOR1>(v);
+  else if constexpr (J == 2) return dpp32<DPP_QP_XOR2>(v);
+  else if constexpr (J == 4) return dpp32<0x1B>(dpp32<0x141>(v));  // mirrored in 8 lanes, then in 4
+  else if constexpr (J == 8) return dpp32<DPP_ROR8>(v);
+  else {
+    const auto r = J == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                           : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return threadIdx.x & J ? r[0] : r[1];
   }
-  return v;
+}
+template <int J>
+__device__ __forceinline__ unsigned long long lane_xor(unsigned long long v) {
+  return (unsigned long long)lane_xor32<J>((uint32_t)(v >> 32)) << 32 | lane_xor32<J>((uint32_t)v);
+}
+__device__ __forceinline__ unsigned long long wave_max64(unsigned long long v) {
+  auto most = [](unsigned long long x, unsigned long long y) { return x > y ? x : y; };
+  v = most(v, lane_xor<1>(v));
+  v = most(v, lane_xor<2>(v));
+  v = most(v, lane_xor<4>(v));
+  v = most(v, lane_xor<8>(v));
+  v = most(v, lane_xor<16>(v));
+  return most(v, lane_xor<32>(v));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ unsigned long long dpp64(unsigned long long v) {
+  return (unsigned long long)dpp32<CTRL, ROWS>((uint32_t)(v >> 32)) << 32 | dpp32<CTRL, ROWS>((uint32_t)v);
 }
 __device__ __forceinline__ unsigned long long wave_scan64(unsigned long long v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const unsigned long long o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
+  v += dpp64<0x111, 0xF>(v);  // row_shr:1, 2, 4, 8, then the rows' last lanes
+  v += dpp64<0x112, 0xF>(v);
+  v += dpp64<0x114, 0xF>(v);
+  v += dpp64<0x118, 0xF>(v);
+  v += dpp64<DPP_BCAST15, 0xA>(v);
+  v += dpp64<DPP_BCAST31, 0xC>(v);
   return v;
 }
 
@@ -330,8 +356,7 @@ __global__ void __launch_bounds__(SLICE_THREADS) sample_scan_kernel(SampleArgs a
     least = fminf(least, lo);
   }
   unsigned long long best = wave_max64((unsigned long long)key_of(most) << 32 | (uint32_t)~at);
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) least = fminf(least, __shfl_xor(least, d));
+  least = logit_of(~(uint32_t)wave_max64((uint32_t)~key_of(least)));
   if ((threadIdx.x & 63) == 0) {
     red[threadIdx.x >> 6] = best;
     red[SLICE_THREADS / 64 + (threadIdx.x >> 6)] = __float_as_uint(least);
@@ -398,7 +423,10 @@ template <int TYPE>
 __global__ void __launch_bounds__(SLICE_THREADS) sample_sums_kernel(SampleArgs a, int slices, int slice) {
   __shared__ unsigned long long red[2 * SLICE_THREADS / 64];
   __shared__ Plan plan_s;
+  __shared__ uint16_t list[CAP];  // places in the slice
+  __shared__ int listed, place;
   const int row = blockIdx.x / slices, s = blockIdx.x % slices;
+  if (threadIdx.x == 0) listed = 0;
   const Work w(a.ws, a.rows, slices);
   const Settings set(a, row);
   if (set.greedy) return;
@@ -422,8 +450,8 @@ __global__ void __launch_bounds__(SLICE_THREADS) sample_sums_kernel(SampleArgs a
         sum += p >= set.least ? fixed(p) : 0;
       }
       if (plan.mode != CUT_NONE && (plan.mode == CUT_FEW ? b <= plan.bin : b == plan.bin) && v[e] != NEG_INF) {
-        const int at = atomicAdd(&w.listed[row], 1);
-        if (at < CAP) w.list[(int64_t)row * CAP + at] = (unsigned long long)~key_of(v[e]) << 32 | (uint32_t)(i + e);
+        const int at = atomicAdd(&listed, 1);
+        if (at < CAP) list[at] = (uint16_t)(i + e - begin);
       }
     }
   }
@@ -435,6 +463,13 @@ __global__ void __launch_bounds__(SLICE_THREADS) sample_sums_kernel(SampleArgs a
 #pragma unroll
     for (int i = 0; i < SLICE_THREADS / 64; ++i) sum += red[i];
     w.sums[(int64_t)row * slices + s] = sum;
+    if (listed) place = atomicAdd(&w.listed[row], listed);
+  }
+  __syncthreads();
+  // (more than CAP in all: the list is not used, and not filled past its end)
+  for (int j = threadIdx.x; j < min(listed, CAP) && place + j < CAP; j += SLICE_THREADS) {
+    const int i = begin + list[j];
+    w.list[(int64_t)row * CAP + place + j] = (unsigned long long)~key_of(clean(logit_at<TYPE>(x, i))) << 32 | (uint32_t)i;
   }
 }
 
@@ -472,20 +507,22 @@ __device__ __forceinline__ void sort(unsigned long long* list, int n) {
   if (n <= THREADS) {
     const int t = threadIdx.x;
     unsigned long long v = t < n ? list[t] : 0;
-    for (int k = 2; k <= n; k <<= 1)
-      for (int j = k >> 1; j > 0; j >>= 1) {
-        unsigned long long o;
-        if (j >= 64) {
-          __syncthreads();
-          if (t < n) list[t] = v;
-          __syncthreads();
-          o = t < n ? list[t ^ j] : 0;
-        } else {
-          o = __shfl_xor(v, j);
-        }
-        const bool low = ((t & j) == 0) == ((t & k) == 0);  // this place takes the smaller one
-        v = (o < v) == low ? o : v;
+    for (int k = 2; k <= n; k <<= 1) {
+      // this place takes the smaller one of a pair
+      auto take = [&](unsigned long long o, int j) { v = (o < v) == (((t & j) == 0) == ((t & k) == 0)) ? o : v; };
+      for (int j = k >> 1; j >= 64; j >>= 1) {
+        __syncthreads();
+        if (t < n) list[t] = v;
+        __syncthreads();
+        take(t < n ? list[t ^ j] : 0, j);
       }
+      if (k >= 64) take(lane_xor<32>(v), 32);
+      if (k >= 32) take(lane_xor<16>(v), 16);
+      if (k >= 16) take(lane_xor<8>(v), 8);
+      if (k >= 8) take(lane_xor<4>(v), 4);
+      if (k >= 4) take(lane_xor<2>(v), 2);
+      take(lane_xor<1>(v), 1);
+    }
     __syncthreads();
     if (t < n) list[t] = v;
   } else {
