@@ -30,15 +30,19 @@
 // Bound: for one row the launches; for many the three times that a logit is read
 // (once from memory, then from the caches) and a weight's 20 operations of 64
 // bits, twice with top-p.
+#include <type_traits>
+
 #include "attn_common.hpp"
 #include "step.hpp"
 
 namespace qg {
 namespace {
 
-constexpr int BINS = 1024, THREADS = 1024;  // (of a row's workgroup: a thread a bin)
-constexpr int CAP = 4096;                   // elements listed
-constexpr int SLICE_THREADS = 256, PIECE = 8;
+constexpr int BINS = 1024;  // and at most so many chunks, of which a slice has one per wave
+constexpr int CAP = 4096;   // elements listed
+constexpr int T = 256;      // threads of every workgroup
+constexpr int WAVES = T / 64, PIECE = 8, STEP = PIECE * T, MOST_SLICES = BINS / WAVES;
+constexpr int OWN = BINS / T;  // bins (or chunks) of a thread
 
 // what a slice of a row leaves: its largest logit's key and place (the first
 // one), its smallest finite logit
@@ -66,7 +70,7 @@ struct Cut {
 };
 
 struct Work {
-  unsigned long long *bins, *sums, *list;  // [rows][BINS], [rows][slices], [rows][CAP]
+  unsigned long long *bins, *list, *sums;  // [rows][BINS], [rows][CAP], [rows][slices * WAVES]
   int* listed;                             // [rows]
   Part* parts;                             // [rows][slices]
   __device__ __forceinline__ Work(void* ws, int64_t rows, int slices) {
@@ -74,12 +78,12 @@ struct Work {
     bins = reinterpret_cast<unsigned long long*>(p), p += rows * BINS * 8;
     list = reinterpret_cast<unsigned long long*>(p), p += rows * CAP * 8;
     parts = reinterpret_cast<Part*>(p), p += rows * slices * 16;
-    sums = reinterpret_cast<unsigned long long*>(p), p += rows * slices * 8;
+    sums = reinterpret_cast<unsigned long long*>(p), p += rows * slices * (8 * WAVES);
     listed = reinterpret_cast<int*>(p);
   }
 };
 constexpr size_t work_bytes(int64_t rows, int slices) {
-  return (size_t)(rows * (BINS * 8 + CAP * 8 + 4) + rows * slices * 24);
+  return (size_t)(rows * (BINS * 8 + CAP * 8 + 4) + rows * slices * (16 + 8 * WAVES));
 }
 
 // Keys: floats in their order as unsigned numbers; NaN as -infinity, -0 as 0.
@@ -220,8 +224,7 @@ __device__ __forceinline__ unsigned long long wave_scan64(unsigned long long v) 
   return v;
 }
 
-// A workgroup's T threads: sums up to and with the thread's, and of all.
-template <int T>
+// A workgroup's threads: sums up to and with the thread's, and of all.
 __device__ __forceinline__ unsigned long long block_scan64(unsigned long long v, unsigned long long& total,
                                                            unsigned long long* red) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -230,7 +233,7 @@ __device__ __forceinline__ unsigned long long block_scan64(unsigned long long v,
   __syncthreads();
   unsigned long long before = 0, all = 0;
 #pragma unroll
-  for (int i = 0; i < T / 64; ++i) {
+  for (int i = 0; i < WAVES; ++i) {
     before += i < w ? red[i] : 0;
     all += red[i];
   }
@@ -240,31 +243,26 @@ __device__ __forceinline__ unsigned long long block_scan64(unsigned long long v,
 }
 
 // The row's largest logit's key and first place (as key << 32 | ~place), and
-// its smallest finite logit, from the slices' parts; the whole workgroup.
+// its smallest finite logit, from the slices' parts (a thread each); the whole
+// workgroup.
 struct Top {
   unsigned long long best;
   float least;
   __device__ __forceinline__ float most() const { return logit_of((uint32_t)(best >> 32)); }
   __device__ __forceinline__ int place() const { return (int)~(uint32_t)best; }
 };
-template <int T>
-__device__ __forceinline__ Top top_of(const Part* parts, int slices, unsigned long long* red) {
-  unsigned long long best = 0, low = 0;
-  for (int i = threadIdx.x; i < slices; i += T) {
-    const Part p = parts[i];
-    const unsigned long long b = (unsigned long long)p.key << 32 | (uint32_t)~p.at;
-    best = b > best ? b : best;
-    const unsigned long long l = (uint32_t)~key_of(p.least);
-    low = l > low ? l : low;
-  }
-  best = wave_max64(best);
-  low = wave_max64(low);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = best, red[T / 64 + (threadIdx.x >> 6)] = low;
+__device__ __forceinline__ Part part_of(const Part* parts, int slices) {
+  return (int)threadIdx.x < slices ? parts[threadIdx.x] : Part{0, -1, __builtin_inff(), 0};
+}
+__device__ __forceinline__ Top top_of(const Part& p, unsigned long long* red) {
+  unsigned long long best = wave_max64((unsigned long long)p.key << 32 | (uint32_t)~p.at);
+  unsigned long long low = wave_max64((uint32_t)~key_of(p.least));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = best, red[WAVES + (threadIdx.x >> 6)] = low;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < T / 64; ++i) {
+  for (int i = 0; i < WAVES; ++i) {
     best = red[i] > best ? red[i] : best;
-    low = red[T / 64 + i] > low ? red[T / 64 + i] : low;
+    low = red[WAVES + i] > low ? red[WAVES + i] : low;
   }
   __syncthreads();
   return {best, logit_of(~(uint32_t)low)};
@@ -277,38 +275,40 @@ struct Binning {
     const float width = most - t.least;
     by = width > 0.f && width < 3e38f ? (float)BINS / width : 0.f;
   }
-  __device__ __forceinline__ int operator()(float l) const {
+  // in bins from the largest logit on; past the last one (and NaN, of
+  // infinities) the last one
+  __device__ __forceinline__ float at(float l) const {
     const float d = (most - l) * by;
-    return l == most ? 0 : d < (float)(BINS - 1) ? (int)d : BINS - 1;  // (NaN, of infinities: the last)
+    return l == most ? 0.f : d < (float)BINS - 0.001f ? d : (float)BINS - 0.001f;
+  }
+  __device__ __forceinline__ int operator()(float l) const { return (int)at(l); }
+  // a 1024th part of its bin, the same order
+  __device__ __forceinline__ int part(float l) const {
+    const float d = at(l);
+    return (int)((d - (float)(int)d) * (float)BINS);
   }
 };
 
-// The row's largest and smallest logits and what follows from its histogram, the
-// same in every workgroup of the row; T threads, all of them.
-template <int T>
-__device__ __forceinline__ Plan plan_of(const SampleArgs& a, const Settings& set, const unsigned long long* bins,
+// What follows from a row's histogram (a thread's bins: mine), the same in every
+// workgroup of the row; all threads.
+__device__ __forceinline__ Plan plan_of(const SampleArgs& a, const Settings& set, const unsigned long long (&mine)[OWN],
                                         unsigned long long* red, Plan* shared) {
   const bool by_count = set.by_count(a.vocab), by_weight = set.by_weight();
   if (!by_count && !by_weight) return Plan{CUT_NONE, BINS, 0, 0.0, 0};
-  constexpr int E = BINS / T;
-  unsigned long long mine[E], sum = 0, total;
+  unsigned long long sum = 0, total;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    mine[e] = bins[E * threadIdx.x + e];
-    sum += mine[e];
-  }
-  unsigned long long before = block_scan64<T>(sum, total, red) - sum;
+  for (int e = 0; e < OWN; ++e) sum += mine[e];
+  if (threadIdx.x == 0) *shared = Plan{CUT_NONE, BINS, 0, 0.0, 0};
+  unsigned long long before = block_scan64(sum, total, red) - sum;
   // by count: the first bin with k elements up to it (all may be fewer); by
   // weight: the first up to which the weights reach p S
   const double goal = by_count ? (double)set.k : set.p * (double)total;
-  if (threadIdx.x == 0) *shared = Plan{CUT_NONE, BINS, 0, 0.0, 0};
-  __syncthreads();
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
+  for (int e = 0; e < OWN; ++e) {
     const unsigned long long upto = before + mine[e];
-    const bool first = E * threadIdx.x + e == 0;
-    if ((double)upto >= goal && (first || (double)before < goal)) {
-      Plan p{CUT_BIN, (int)(E * threadIdx.x) + e, before, goal, total};
+    const int b = OWN * threadIdx.x + e;
+    if ((double)upto >= goal && (b == 0 || (double)before < goal)) {
+      Plan p{CUT_BIN, b, before, goal, total};
       if (by_count) p.mode = upto <= CAP ? CUT_FEW : by_weight ? CUT_MANY : CUT_BIN;
       *shared = p;
     }
@@ -320,14 +320,18 @@ __device__ __forceinline__ Plan plan_of(const SampleArgs& a, const Settings& set
   if (by_count && p.mode == CUT_NONE && by_weight) p.mode = total <= CAP ? CUT_FEW : CUT_MANY;
   return p;
 }
+__device__ __forceinline__ void own_bins(const SampleArgs& a, const unsigned long long* bins, unsigned long long (&mine)[OWN]) {
+#pragma unroll
+  for (int e = 0; e < OWN; ++e) mine[e] = a.top_k || a.top_p ? bins[OWN * threadIdx.x + e] : 0;
+}
 
 // ---------------------------------------------------------------------------
 // slices
 // ---------------------------------------------------------------------------
 
 template <int TYPE>
-__global__ void __launch_bounds__(SLICE_THREADS) sample_scan_kernel(SampleArgs a, int slices, int slice) {
-  __shared__ unsigned long long red[2 * SLICE_THREADS / 64];
+__global__ void __launch_bounds__(T) sample_scan_kernel(SampleArgs a, int slices, int slice) {
+  __shared__ unsigned long long red[2 * WAVES];
   const int row = blockIdx.x / slices, s = blockIdx.x % slices;
   const Work w(a.ws, a.rows, slices);
   const int begin = s * slice, end = min(begin + slice, a.vocab);
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(SLICE_THREADS) sample_scan_kernel(SampleArgs a
   float most = NEG_INF, least = __builtin_inff();
   int at = begin;
 #pragma unroll 4
-  for (int i = begin + PIECE * threadIdx.x; i < end; i += PIECE * SLICE_THREADS) {
+  for (int i = begin + PIECE * threadIdx.x; i < end; i += STEP) {
     float v[PIECE];
     load_piece<TYPE>(x, i, end, v);
     float hi = v[0], lo = v[0];
@@ -359,42 +363,42 @@ __global__ void __launch_bounds__(SLICE_THREADS) sample_scan_kernel(SampleArgs a
   least = logit_of(~(uint32_t)wave_max64((uint32_t)~key_of(least)));
   if ((threadIdx.x & 63) == 0) {
     red[threadIdx.x >> 6] = best;
-    red[SLICE_THREADS / 64 + (threadIdx.x >> 6)] = __float_as_uint(least);
+    red[WAVES + (threadIdx.x >> 6)] = __float_as_uint(least);
   }
   __syncthreads();
   if (threadIdx.x == 0) {
 #pragma unroll
-    for (int i = 0; i < SLICE_THREADS / 64; ++i) {
+    for (int i = 0; i < WAVES; ++i) {
       best = red[i] > best ? red[i] : best;
-      least = fminf(least, __uint_as_float((uint32_t)red[SLICE_THREADS / 64 + i]));
+      least = fminf(least, __uint_as_float((uint32_t)red[WAVES + i]));
     }
     w.parts[(int64_t)row * slices + s] = Part{(uint32_t)(best >> 32), (int)~(uint32_t)best, least, 0};
     if (s == 0) w.listed[row] = 0;
   }
   // the row's histogram starts at 0, a part of it by each slice
   if (a.top_k || a.top_p)
-    for (int i = s * SLICE_THREADS + threadIdx.x; i < BINS; i += slices * SLICE_THREADS) w.bins[(int64_t)row * BINS + i] = 0;
+    for (int i = s * T + threadIdx.x; i < BINS; i += slices * T) w.bins[(int64_t)row * BINS + i] = 0;
 }
 
 // Counts (with top-k) or weights (with top-p alone) by bins.
 template <int TYPE>
-__global__ void __launch_bounds__(SLICE_THREADS) sample_bins_kernel(SampleArgs a, int slices, int slice) {
-  __shared__ unsigned long long red[2 * SLICE_THREADS / 64];
+__global__ void __launch_bounds__(T) sample_bins_kernel(SampleArgs a, int slices, int slice) {
+  __shared__ unsigned long long red[2 * WAVES];
   __shared__ unsigned long long bins[BINS];
   const int row = blockIdx.x / slices, s = blockIdx.x % slices;
   const Settings set(a, row);
   const bool by_count = set.by_count(a.vocab);
   if (set.greedy || !(by_count || set.by_weight())) return;
   const Work w(a.ws, a.rows, slices);
-  for (int i = threadIdx.x; i < BINS; i += SLICE_THREADS) bins[i] = 0;
-  const Top top = top_of<SLICE_THREADS>(w.parts + (int64_t)row * slices, slices, red);  // (with barriers)
+  for (int i = threadIdx.x; i < BINS; i += T) bins[i] = 0;
+  const Top top = top_of(part_of(w.parts + (int64_t)row * slices, slices), red);  // (with barriers)
   const Binning bin(top);
   const Weigh weigh{(double)top.most(), set.by};
   const int begin = s * slice, end = min(begin + slice, a.vocab);
   const void* x = static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes;
   uint32_t* counts = reinterpret_cast<uint32_t*>(bins);
 #pragma unroll 2
-  for (int i = begin + PIECE * threadIdx.x; i < end; i += PIECE * SLICE_THREADS) {
+  for (int i = begin + PIECE * threadIdx.x; i < end; i += STEP) {
     float v[PIECE];
     load_piece<TYPE>(x, i, end, v);
     if (by_count) {
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(SLICE_THREADS) sample_bins_kernel(SampleArgs a
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < BINS; i += SLICE_THREADS) {
+  for (int i = threadIdx.x; i < BINS; i += T) {
     const unsigned long long f = by_count ? counts[i] : bins[i];
     if (f) atomicAdd(&w.bins[(int64_t)row * BINS + i], f);
   }
@@ -418,28 +422,32 @@ __global__ void __launch_bounds__(SLICE_THREADS) sample_bins_kernel(SampleArgs a
 
 // The slice's elements of the bin in which the prefix ends go into the list (or
 // those of all bins up to it); the weights that it keeps of the bins in front of
-// it are summed.
+// it are summed, by chunks: a wave has a run of the slice.
 template <int TYPE>
-__global__ void __launch_bounds__(SLICE_THREADS) sample_sums_kernel(SampleArgs a, int slices, int slice) {
-  __shared__ unsigned long long red[2 * SLICE_THREADS / 64];
+__global__ void __launch_bounds__(T) sample_sums_kernel(SampleArgs a, int slices, int slice) {
+  __shared__ unsigned long long red[2 * WAVES];
   __shared__ Plan plan_s;
   __shared__ uint16_t list[CAP];  // places in the slice
   __shared__ int listed, place;
   const int row = blockIdx.x / slices, s = blockIdx.x % slices;
   if (threadIdx.x == 0) listed = 0;
   const Work w(a.ws, a.rows, slices);
+  const Part part = part_of(w.parts + (int64_t)row * slices, slices);
+  unsigned long long mine[OWN];
+  own_bins(a, w.bins + (int64_t)row * BINS, mine);
   const Settings set(a, row);
   if (set.greedy) return;
-  const Plan plan = plan_of<SLICE_THREADS>(a, set, w.bins + (int64_t)row * BINS, red, &plan_s);
+  const Plan plan = plan_of(a, set, mine, red, &plan_s);
   if (plan.mode == CUT_MANY) return;
-  const Top top = top_of<SLICE_THREADS>(w.parts + (int64_t)row * slices, slices, red);
+  const Top top = top_of(part, red);  // (with barriers)
   const Binning bin(top);
   const Weigh weigh{(double)top.most(), set.by};
-  const int begin = s * slice, end = min(begin + slice, a.vocab);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int first = s * slice, begin = first + wave * (slice / WAVES), end = min(begin + slice / WAVES, a.vocab);
   const void* x = static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes;
   unsigned long long sum = 0;
 #pragma unroll 2
-  for (int i = begin + PIECE * threadIdx.x; i < end; i += PIECE * SLICE_THREADS) {
+  for (int i = begin + PIECE * lane; i < end; i += PIECE * 64) {
     float v[PIECE];
     load_piece<TYPE>(x, i, end, v);
 #pragma unroll
@@ -451,24 +459,19 @@ __global__ void __launch_bounds__(SLICE_THREADS) sample_sums_kernel(SampleArgs a
       }
       if (plan.mode != CUT_NONE && (plan.mode == CUT_FEW ? b <= plan.bin : b == plan.bin) && v[e] != NEG_INF) {
         const int at = atomicAdd(&listed, 1);
-        if (at < CAP) list[at] = (uint16_t)(i + e - begin);
+        if (at < CAP) list[at] = (uint16_t)(i + e - first);
       }
     }
   }
   sum = wave_scan64(sum);
-  if ((threadIdx.x & 63) == 63) red[threadIdx.x >> 6] = sum;
+  if (lane == 63) w.sums[((int64_t)row * slices + s) * WAVES + wave] = sum;
+  if (plan.mode == CUT_NONE) return;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    sum = 0;
-#pragma unroll
-    for (int i = 0; i < SLICE_THREADS / 64; ++i) sum += red[i];
-    w.sums[(int64_t)row * slices + s] = sum;
-    if (listed) place = atomicAdd(&w.listed[row], listed);
-  }
+  if (threadIdx.x == 0 && listed) place = atomicAdd(&w.listed[row], listed);
   __syncthreads();
   // (more than CAP in all: the list is not used, and not filled past its end)
-  for (int j = threadIdx.x; j < min(listed, CAP) && place + j < CAP; j += SLICE_THREADS) {
-    const int i = begin + list[j];
+  for (int j = threadIdx.x; j < min(listed, CAP) && place + j < CAP; j += T) {
+    const int i = first + list[j];
     w.list[(int64_t)row * CAP + place + j] = (unsigned long long)~key_of(clean(logit_at<TYPE>(x, i))) << 32 | (uint32_t)i;
   }
 }
@@ -486,50 +489,84 @@ __device__ __forceinline__ unsigned long long target_of(float u, unsigned long l
 
 __device__ __forceinline__ int power_of_two(int n) { return n < 2 ? 1 : 1 << (32 - __builtin_clz(n - 1)); }
 
-constexpr int EACH = CAP / THREADS;  // entries of a thread
-
 struct Shared {
   unsigned long long list[CAP];
-  unsigned long long bins[BINS];  // of counts or weights, up to and with the bin
-  unsigned long long counts[BINS];
-  unsigned long long red[2 * THREADS / 64];
+  unsigned long long bins[BINS];  // of counts, weights or chunks' sums
+  uint32_t counts[BINS];
+  unsigned long long red[2 * WAVES];
   unsigned long long found;
   Plan plan;
   uint32_t key0, key1;
   int n, at;
 };
 
-// Sorts list[0 .. n) (n a power of two up to CAP) upwards; the whole workgroup.
-// Up to an entry a thread they stay in registers: partners within a wave change
-// places by lanes, others through the list.
+// Sorts E entries a thread upwards (entry T e + thread, n of them, a power of
+// two): partners within a wave change places by lanes, others within a thread or
+// through the list.
+template <int E>
+__device__ __forceinline__ void sort_held(unsigned long long* list, int n) {
+  const int t = threadIdx.x;
+  unsigned long long v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = T * e + t < n ? list[T * e + t] : 0;
+  for (int k = 2; k <= n; k <<= 1) {
+    // a place takes the smaller one of a pair, or the larger
+    auto take = [&](int e, unsigned long long o, int j) {
+      const int i = T * e + t;
+      v[e] = (o < v[e]) == (((i & j) == 0) == ((i & k) == 0)) ? o : v[e];
+    };
+    auto lanes = [&](auto by) {
+      constexpr int J = decltype(by)::value;
+#pragma unroll
+      for (int e = 0; e < E; ++e) take(e, lane_xor<J>(v[e]), J);
+    };
+#pragma unroll
+    for (int j = E / 2; j > 0; j >>= 1)
+      if (k > T * j) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (!(e & j)) {
+            const unsigned long long x = v[e], y = v[e | j];
+            take(e, y, T * j);
+            take(e | j, x, T * j);
+          }
+      }
+    for (int j = min(k, T) >> 1; j >= 64; j >>= 1) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (T * e + t < n) list[T * e + t] = v[e];
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (T * e + t < n) take(e, list[(T * e + t) ^ j], j);
+    }
+    if (k >= 64) lanes(std::integral_constant<int, 32>{});
+    if (k >= 32) lanes(std::integral_constant<int, 16>{});
+    if (k >= 16) lanes(std::integral_constant<int, 8>{});
+    if (k >= 8) lanes(std::integral_constant<int, 4>{});
+    if (k >= 4) lanes(std::integral_constant<int, 2>{});
+    lanes(std::integral_constant<int, 1>{});
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (T * e + t < n) list[T * e + t] = v[e];
+}
+
+// Sorts list[0 .. n) (n a power of two up to CAP) upwards; the whole workgroup,
+// barriers on both sides.
 __device__ __forceinline__ void sort(unsigned long long* list, int n) {
   __syncthreads();
-  if (n <= THREADS) {
-    const int t = threadIdx.x;
-    unsigned long long v = t < n ? list[t] : 0;
-    for (int k = 2; k <= n; k <<= 1) {
-      // this place takes the smaller one of a pair
-      auto take = [&](unsigned long long o, int j) { v = (o < v) == (((t & j) == 0) == ((t & k) == 0)) ? o : v; };
-      for (int j = k >> 1; j >= 64; j >>= 1) {
-        __syncthreads();
-        if (t < n) list[t] = v;
-        __syncthreads();
-        take(t < n ? list[t ^ j] : 0, j);
-      }
-      if (k >= 64) take(lane_xor<32>(v), 32);
-      if (k >= 32) take(lane_xor<16>(v), 16);
-      if (k >= 16) take(lane_xor<8>(v), 8);
-      if (k >= 8) take(lane_xor<4>(v), 4);
-      if (k >= 4) take(lane_xor<2>(v), 2);
-      take(lane_xor<1>(v), 1);
-    }
-    __syncthreads();
-    if (t < n) list[t] = v;
+  if (n <= T) {
+    sort_held<1>(list, n);
+  } else if (n <= 4 * T) {
+    sort_held<4>(list, n);
   } else {
     for (int k = 2; k <= n; k <<= 1)
       for (int j = k >> 1; j > 0; j >>= 1) {
         __syncthreads();
-        for (int t = threadIdx.x; t < n / 2; t += THREADS) {
+        for (int t = threadIdx.x; t < n / 2; t += T) {
           const int i = ((t & ~(j - 1)) << 1) | (t & (j - 1)), o = i | j;
           const unsigned long long x = list[i], y = list[o];
           if ((x > y) == ((i & k) == 0)) list[i] = y, list[o] = x;
@@ -553,14 +590,14 @@ struct OneRow {
   __device__ __forceinline__ static uint32_t key_in(unsigned long long entry) { return ~(uint32_t)(entry >> 32); }
   __device__ __forceinline__ unsigned long long weight_of(uint32_t key) const { return fixed(weigh(logit_of(key))); }
   __device__ __forceinline__ unsigned long long scan(unsigned long long v, unsigned long long& total) const {
-    return block_scan64<THREADS>(v, total, sh.red);
+    return block_scan64(v, total, sh.red);
   }
 
   // f(logit, index) for the row's elements that are not -infinity
   template <typename F>
   __device__ __forceinline__ void each(F&& f) const {
 #pragma unroll 2
-    for (int i = PIECE * threadIdx.x; i < a.vocab; i += PIECE * THREADS) {
+    for (int i = PIECE * threadIdx.x; i < a.vocab; i += STEP) {
       float v[PIECE];
       load_piece<TYPE>(x, i, a.vocab, v);
 #pragma unroll
@@ -572,19 +609,8 @@ struct OneRow {
   // Sorts the n entries that are in the list.
   __device__ __forceinline__ void order(int n) const {
     const int m = power_of_two(n);
-    for (int i = n + threadIdx.x; i < m; i += THREADS) sh.list[i] = ~0ull;
+    for (int i = n + threadIdx.x; i < m; i += T) sh.list[i] = ~0ull;
     sort(sh.list, m);
-  }
-  // the weights of a thread's entries EACH * t .. and the sum in front of them
-  __device__ __forceinline__ unsigned long long scan_list(int n, unsigned long long (&w)[EACH], unsigned long long& total) const {
-    unsigned long long mine = 0;
-#pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-      const int j = EACH * threadIdx.x + e;
-      w[e] = j < n ? weight_of(key_in(sh.list[j])) : 0;
-      mine += w[e];
-    }
-    return scan(mine, total) - mine;
   }
   // The last of the n sorted entries that stays.  By count: the `want`th (from
   // 1).  By weight: the last with less than `goal` in front of it, `before` of
@@ -592,38 +618,53 @@ struct OneRow {
   // up to and with it.
   __device__ __forceinline__ int last_of(int n, bool by_weight, uint32_t want, unsigned long long before, double goal,
                                          unsigned long long& upto) const {
-    unsigned long long w[EACH], total, sum = scan_list(n, w, total), at = sum;
+    const int each = (n + T - 1) / T, j0 = each * (int)threadIdx.x, j1 = min(j0 + each, n);  // a thread's entries
+    unsigned long long total, sum = 0;
+    for (int j = j0; j < j1; ++j) sum += weight_of(key_in(sh.list[j]));
     if (threadIdx.x == 0) sh.at = by_weight ? 0 : max((int)min(want, (uint32_t)n) - 1, 0);
-    __syncthreads();
-    int last = 0;
-#pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-      const int j = EACH * threadIdx.x + e;
-      last = j < n && (double)(before + at) < goal ? j : last;
-      at += w[e];
+    sum = scan(sum, total) - sum;
+    if (by_weight) {
+      int last = 0;
+      unsigned long long at = before + sum;
+      for (int j = j0; j < j1; ++j) {
+        last = (double)at < goal ? j : last;
+        at += weight_of(key_in(sh.list[j]));
+      }
+      if (last) atomicMax(&sh.at, last);
+      __syncthreads();
     }
-    if (by_weight && last) atomicMax(&sh.at, last);
-    __syncthreads();
-    const int j = sh.at;
-#pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-      sum += w[e];
-      if (EACH * (int)threadIdx.x + e == j) sh.found = sum;
+    const int l = sh.at;
+    if (j0 <= l && l < j1) {
+      for (int j = j0; j <= l; ++j) sum += weight_of(key_in(sh.list[j]));
+      sh.found = sum;
     }
     __syncthreads();
-    upto = sh.found;
+    upto = n ? sh.found : 0;
     __syncthreads();
-    return j;
+    return l;
   }
 
+  // Sums over sh.bins (a thread's OWN ones side by side), in place.
+  __device__ __forceinline__ void sum_bins() const {
+    unsigned long long mine[OWN], sum = 0, total;
+#pragma unroll
+    for (int e = 0; e < OWN; ++e) mine[e] = sum += sh.bins[OWN * threadIdx.x + e];
+    const unsigned long long before = scan(sum, total) - sum;
+#pragma unroll
+    for (int e = 0; e < OWN; ++e) sh.bins[OWN * threadIdx.x + e] = before + mine[e];
+    __syncthreads();
+  }
   // The first bin up to which sums reach a goal, as reaches(bin) says (false,
   // ..., false, true, ...), or the last one.
   template <typename F>
   __device__ __forceinline__ int first_bin(F&& reaches) const {
     if (threadIdx.x == 0) sh.at = BINS - 1;
     __syncthreads();
-    const int b = threadIdx.x;
-    if (reaches(b) && (b == 0 || !reaches(b - 1))) sh.at = b;
+#pragma unroll
+    for (int e = 0; e < OWN; ++e) {
+      const int b = OWN * threadIdx.x + e;
+      if (reaches(b) && (b == 0 || !reaches(b - 1))) sh.at = b;
+    }
     __syncthreads();
     const int r = sh.at;
     __syncthreads();
@@ -632,8 +673,8 @@ struct OneRow {
 
   // The end of a prefix anywhere in the row, by the row itself: where the list
   // cannot say (thousands of elements in one bin, or both criteria over as many).
-  // Counts and weights by ranges of keys, each 1024th of the last, until the
-  // range in which the prefix ends has few elements, or one key.
+  // Counts or weights by ranges of keys, each about a 1000th of the last, until
+  // the range in which the prefix ends has few elements, or one key.
   __device__ __forceinline__ Cut search(bool by_weight, uint32_t want, double goal, unsigned long long& upto) const {
     uint32_t low = 0, high = ~0u;
     unsigned long long inside = 0;  // weights above `high`
@@ -645,8 +686,7 @@ struct OneRow {
     for (;;) {
       __syncthreads();
       if (threadIdx.x == 0) sh.key0 = ~0u, sh.key1 = 0, sh.n = 0;
-      sh.counts[threadIdx.x] = 0;
-      sh.bins[threadIdx.x] = 0;
+      for (int i = threadIdx.x; i < BINS; i += T) sh.counts[i] = 0, sh.bins[i] = 0;
       __syncthreads();
       uint32_t k0 = ~0u, k1 = 0;
       int mine = 0;
@@ -662,19 +702,25 @@ struct OneRow {
       each([&](float l, int) {
         if (!in(l)) return;
         const uint32_t r = (high - key_of(l)) >> shift;
-        atomicAdd(&sh.counts[r], 1ull);
+        atomicAdd(&sh.counts[r], 1u);
         atomicAdd(&sh.bins[r], fixed(weigh(l)));
       });
       __syncthreads();
-      unsigned long long all;
-      const unsigned long long c = scan(sh.counts[threadIdx.x], all), w = scan(sh.bins[threadIdx.x], all);
-      sh.counts[threadIdx.x] = c;
-      sh.bins[threadIdx.x] = w;
-      __syncthreads();
+      sum_bins();
+      {  // counts likewise
+        uint32_t mine[OWN], sum = 0;
+#pragma unroll
+        for (int e = 0; e < OWN; ++e) mine[e] = sum += sh.counts[OWN * threadIdx.x + e];
+        unsigned long long total;
+        const uint32_t before = (uint32_t)scan(sum, total) - sum;
+#pragma unroll
+        for (int e = 0; e < OWN; ++e) sh.counts[OWN * threadIdx.x + e] = before + mine[e];
+        __syncthreads();
+      }
       const int r = first_bin([&](int i) {
         return by_weight ? (double)(inside + sh.bins[i]) >= goal : sh.counts[i] >= want;
       });
-      want -= r ? (uint32_t)sh.counts[r - 1] : 0;
+      want -= r ? sh.counts[r - 1] : 0;
       inside += r ? sh.bins[r - 1] : 0;
       const uint32_t h = high - ((uint32_t)r << shift), l = h - ((1u << shift) - 1);
       high = h;
@@ -703,7 +749,7 @@ struct OneRow {
     }
     m = max(1u, min(m, n));
     uint32_t seen = 0;
-    for (int i0 = 0; i0 < a.vocab && seen < m; i0 += PIECE * THREADS) {
+    for (int i0 = 0; i0 < a.vocab && seen < m; i0 += STEP) {
       const int i = i0 + PIECE * threadIdx.x;
       float v[PIECE];
       uint32_t mine = 0;
@@ -727,12 +773,53 @@ struct OneRow {
     return Cut{high, place};
   }
 
+  // The end of a prefix among the n listed elements of one bin, `before` (counts
+  // or weights) in front of them: first by 1024 parts of the bin, then by the
+  // sorted elements of one part.  The entries that stay are those up to the cut.
+  __device__ __forceinline__ Cut end_in_bin(int n, bool by_weight, unsigned long long before, double goal) const {
+    for (int i = threadIdx.x; i < BINS; i += T) sh.bins[i] = 0;
+    if (threadIdx.x == 0) sh.n = 0;
+    __syncthreads();
+    for (int j = threadIdx.x; j < n; j += T) {
+      const uint32_t key = key_in(sh.list[j]);
+      atomicAdd(&sh.bins[bin.part(logit_of(key))], by_weight ? weight_of(key) : 1ull);
+    }
+    __syncthreads();
+    sum_bins();
+    const int r = first_bin([&](int i) { return (double)(before + sh.bins[i]) >= goal; });
+    before += r ? sh.bins[r - 1] : 0;
+    // that part's entries in front of the others (which stay where they are
+    // listed in global memory)
+    constexpr int MORE = CAP / T;
+    unsigned long long mine[MORE];
+    uint32_t are = 0;
+#pragma unroll
+    for (int e = 0; e < MORE; ++e) {
+      const int j = T * e + threadIdx.x;
+      if (T * e >= n) break;
+      mine[e] = j < n ? sh.list[j] : 0;
+      are |= j < n && bin.part(logit_of(key_in(mine[e]))) == r ? 1u << e : 0u;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < MORE; ++e)
+      if (are >> e & 1) sh.list[atomicAdd(&sh.n, 1)] = mine[e];
+    __syncthreads();
+    const int m = sh.n;
+    order(m);
+    unsigned long long upto;
+    const int l = last_of(m, by_weight, by_weight ? 1 : (uint32_t)(goal - (double)before), before, goal, upto);
+    const unsigned long long entry = sh.list[l];
+    __syncthreads();
+    return Cut{key_in(entry), (int)(uint32_t)entry};
+  }
+
   // The token, among elements [begin, end): the first up to which the kept
   // weights, `before` in front, pass t; returns the weights up to the end.  (Where
   // they do not pass it nothing is written.)
   __device__ __forceinline__ unsigned long long draw(int begin, int end, Cut cut, unsigned long long before,
                                                      unsigned long long t, int32_t* out) const {
-    for (int i0 = begin; i0 < end && before <= t; i0 += PIECE * THREADS) {
+    for (int i0 = begin; i0 < end && before <= t; i0 += STEP) {
       const int i = i0 + PIECE * threadIdx.x;
       unsigned long long w[PIECE], sum = 0, all;
       float v[PIECE];
@@ -760,23 +847,35 @@ struct OneRow {
 };
 
 template <int TYPE>
-__global__ void __launch_bounds__(THREADS) sample_draw_kernel(SampleArgs a, int slices, int slice) {
+__global__ void __launch_bounds__(T) sample_draw_kernel(SampleArgs a, int slices, int slice) {
   __shared__ Shared sh;
   const int row = blockIdx.x;
   const Work wk(a.ws, a.rows, slices);
+  // (all that is needed of memory is asked for at once)
+  const Part part = part_of(wk.parts + (int64_t)row * slices, slices);
+  unsigned long long mine[OWN], sums[OWN];
+  own_bins(a, wk.bins + (int64_t)row * BINS, mine);
+#pragma unroll
+  for (int e = 0; e < OWN; ++e) {
+    const int c = OWN * threadIdx.x + e;
+    sums[e] = c < slices * WAVES ? wk.sums[(int64_t)row * slices * WAVES + c] : 0;
+  }
+  const int listed = wk.listed[row];
+  const unsigned long long* list = wk.list + (int64_t)row * CAP;
   const Settings set(a, row);
   int32_t* out = a.out + row;
   const float u = a.u[row];
-  const int listed = wk.listed[row];
-  const Top top = top_of<THREADS>(wk.parts + (int64_t)row * slices, slices, sh.red);
+  const Top top = top_of(part, sh.red);
   if (set.greedy || top.most() == NEG_INF) {
     if (threadIdx.x == 0) *out = top.most() == NEG_INF ? -1 : top.place();
     return;
   }
   const OneRow<TYPE> r{a, set, sh, static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes, Binning(top),
                        Weigh{(double)top.most(), set.by}};
-  const Plan plan = plan_of<THREADS>(a, set, wk.bins + (int64_t)row * BINS, sh.red, &sh.plan);
   const bool by_count = set.by_count(a.vocab), by_weight = set.by_weight();
+  if (by_count || by_weight)
+    for (int j = threadIdx.x; j < min(listed, CAP); j += T) sh.list[j] = list[j];
+  const Plan plan = plan_of(a, set, mine, sh.red, &sh.plan);  // (with barriers)
   unsigned long long total, upto;
 
   if (plan.mode == CUT_MANY || (plan.mode != CUT_NONE && listed > CAP)) {
@@ -794,75 +893,75 @@ __global__ void __launch_bounds__(THREADS) sample_draw_kernel(SampleArgs a, int 
   }
 
   const int n = plan.mode == CUT_NONE ? 0 : listed;
-  if (n) {
-    for (int i = threadIdx.x; i < n; i += THREADS) sh.list[i] = wk.list[(int64_t)row * CAP + i];
-    __syncthreads();
-    r.order(n);
-  }
-
   if (plan.mode == CUT_FEW) {
+    r.order(n);
     int kept = by_count ? min(set.k, n) : n;
-    r.last_of(n, false, (uint32_t)kept, 0, 0.0, upto);
-    if (by_weight) kept = min(kept, 1 + r.last_of(n, true, 1, 0, set.p * (double)upto, upto));
+    if (by_weight) {
+      r.last_of(n, false, (uint32_t)kept, 0, 0.0, upto);
+      kept = min(kept, 1 + r.last_of(n, true, 1, 0, set.p * (double)upto, upto));
+    }
     // (min-p keeps a prefix of these; then by index)
-    unsigned long long entry[EACH], w[EACH], mine = 0;
-#pragma unroll
-    for (int e = 0; e < EACH; ++e) entry[e] = sh.list[EACH * threadIdx.x + e];
-    __syncthreads();
     const int m = power_of_two(kept);
-#pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-      const int j = EACH * threadIdx.x + e;
-      const bool stays = j < kept && (j == 0 || r.weigh(logit_of(r.key_in(entry[e]))) >= set.least);
-      if (j < m) sh.list[j] = stays ? entry[e] << 32 | entry[e] >> 32 : ~0ull;
+    __syncthreads();
+    for (int j = threadIdx.x; j < m; j += T) {
+      const unsigned long long entry = sh.list[j];
+      const bool stays = j < kept && (j == 0 || r.weigh(logit_of(r.key_in(entry))) >= set.least);
+      sh.list[j] = stays ? entry << 32 | entry >> 32 : ~0ull;
     }
     sort(sh.list, m);
-#pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-      const int j = EACH * threadIdx.x + e;
-      entry[e] = j < m ? sh.list[j] : ~0ull;
-      w[e] = entry[e] != ~0ull ? r.weight_of(~(uint32_t)entry[e]) : 0;
-      mine += w[e];
-    }
-    unsigned long long sum = r.scan(mine, total) - mine;
+    const int each = (m + T - 1) / T, j0 = min(each * (int)threadIdx.x, m), j1 = min(j0 + each, m);
+    unsigned long long sum = 0;
+    auto weight_at = [&](int j) { return sh.list[j] == ~0ull ? 0ull : r.weight_of(~(uint32_t)sh.list[j]); };
+    for (int j = j0; j < j1; ++j) sum += weight_at(j);
+    sum = r.scan(sum, total) - sum;
     const unsigned long long t = target_of(u, total);
-#pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-      if (sum <= t && t < sum + w[e]) *out = (int)(entry[e] >> 32);
-      sum += w[e];
+    for (int j = j0; j < j1; ++j) {
+      const unsigned long long w = weight_at(j);
+      if (sum <= t && t < sum + w) *out = (int)(sh.list[j] >> 32);
+      sum += w;
     }
     return;
   }
 
-  // the slices' sums, and to each what it keeps of the list (sh.bins: a slice a
-  // thread)
-  sh.bins[threadIdx.x] = (int)threadIdx.x < slices ? wk.sums[(int64_t)row * slices + threadIdx.x] : 0;
-  if (threadIdx.x == 0) sh.key0 = 0, sh.found = 0;
+  // the chunks' sums, and to each what it keeps of the list
   Cut cut{0, 0};
-  if (n) {
-    const int last = r.last_of(n, !by_count, by_count ? (uint32_t)(set.k - (int)plan.before) : 1, plan.before, plan.goal, upto);
-    const unsigned long long entry = sh.list[last];
-    cut = Cut{r.key_in(entry), (int)(uint32_t)entry};
-    for (int j = threadIdx.x; j <= last; j += THREADS) {
-      const double p = r.weigh(logit_of(r.key_in(sh.list[j])));
-      const uint32_t i = (uint32_t)sh.list[j];
-      if (p >= set.least) atomicAdd(&sh.bins[i / (uint32_t)slice], fixed(p));
-    }
+  if (n) cut = r.end_in_bin(n, !by_count, plan.before, plan.goal);
+#pragma unroll
+  for (int e = 0; e < OWN; ++e) sh.bins[OWN * threadIdx.x + e] = sums[e];
+  __syncthreads();
+  const int chunk = slice / WAVES;
+  for (int j = threadIdx.x; j < n; j += T) {
+    const unsigned long long entry = list[j];
+    const uint32_t key = r.key_in(entry), i = (uint32_t)entry;
+    if (key < cut.key || (key == cut.key && (int)i > cut.at)) continue;
+    const double p = r.weigh(logit_of(key));
+    if (p >= set.least) atomicAdd(&sh.bins[i / (uint32_t)chunk], fixed(p));
   }
   __syncthreads();
-  const unsigned long long mine = sh.bins[threadIdx.x], here = r.scan(mine, total);
+  unsigned long long sum = 0, own[OWN];
+#pragma unroll
+  for (int e = 0; e < OWN; ++e) sum += own[e] = sh.bins[OWN * threadIdx.x + e];
+  unsigned long long at = r.scan(sum, total) - sum;
   const unsigned long long t = target_of(u, total);
-  if (here - mine <= t && t < here) sh.key0 = threadIdx.x, sh.found = here - mine;
+  if (threadIdx.x == 0) sh.key0 = 0, sh.found = 0;
   __syncthreads();
-  const int begin = (int)sh.key0 * slice, end = min(begin + slice, a.vocab);
+#pragma unroll
+  for (int e = 0; e < OWN; ++e) {
+    if (at <= t && t < at + own[e]) sh.key0 = OWN * threadIdx.x + e, sh.found = at;
+    at += own[e];
+  }
+  __syncthreads();
+  const int begin = (int)sh.key0 * chunk, end = min(begin + chunk, a.vocab);
   r.draw(begin, end, cut, sh.found, t, out);
 }
 
 // Logits of a slice: about 1024 workgroups over all rows, between 2048 and
 // 16384 of them each.
 int slice_of(int64_t rows, int vocab) {
-  const int64_t step = PIECE * SLICE_THREADS, each = rows * vocab / (1024 * step) * step;
-  return (int)(each < step ? step : each > 8 * step ? 8 * step : each);
+  const int64_t each = rows * vocab / (1024 * STEP) * STEP;
+  const int64_t least = ((int64_t)vocab + MOST_SLICES * STEP - 1) / (MOST_SLICES * STEP) * STEP;
+  const int64_t s = each < 8 * STEP ? each : 8 * STEP;
+  return (int)(s < least ? least : s);
 }
 int slices_of(int64_t rows, int vocab) {
   const int s = slice_of(rows, vocab);
@@ -872,11 +971,11 @@ int slices_of(int64_t rows, int vocab) {
 template <int TYPE>
 hipError_t launch(const SampleArgs& a, hipStream_t s) {
   const int slice = slice_of(a.rows, a.vocab), slices = slices_of(a.rows, a.vocab);
-  const dim3 grid((unsigned)a.rows * (unsigned)slices), rows((unsigned)a.rows);
-  hipLaunchKernelGGL(sample_scan_kernel<TYPE>, grid, dim3(SLICE_THREADS), 0, s, a, slices, slice);
-  if (a.top_k || a.top_p) hipLaunchKernelGGL(sample_bins_kernel<TYPE>, grid, dim3(SLICE_THREADS), 0, s, a, slices, slice);
-  hipLaunchKernelGGL(sample_sums_kernel<TYPE>, grid, dim3(SLICE_THREADS), 0, s, a, slices, slice);
-  hipLaunchKernelGGL(sample_draw_kernel<TYPE>, rows, dim3(THREADS), 0, s, a, slices, slice);
+  const dim3 grid((unsigned)a.rows * (unsigned)slices), rows((unsigned)a.rows), threads(T);
+  hipLaunchKernelGGL(sample_scan_kernel<TYPE>, grid, threads, 0, s, a, slices, slice);
+  if (a.top_k || a.top_p) hipLaunchKernelGGL(sample_bins_kernel<TYPE>, grid, threads, 0, s, a, slices, slice);
+  hipLaunchKernelGGL(sample_sums_kernel<TYPE>, grid, threads, 0, s, a, slices, slice);
+  hipLaunchKernelGGL(sample_draw_kernel<TYPE>, rows, threads, 0, s, a, slices, slice);
   return hipGetLastError();
 }
 
