@@ -30,8 +30,6 @@
 // Bound: for one row the launches; for many the three times that a logit is read
 // (once from memory, then from the caches) and a weight's 20 operations of 64
 // bits, twice with top-p.
-#include <type_traits>
-
 #include "attn_common.hpp"
 #include "step.hpp"
 
@@ -39,7 +37,7 @@ namespace qg {
 namespace {
 
 constexpr int BINS = 1024;  // and at most so many chunks, of which a slice has one per wave
-constexpr int CAP = 4096;   // elements listed
+constexpr int CAP = 2048;   // elements listed
 constexpr int T = 256;      // threads of every workgroup
 constexpr int WAVES = T / 64, PIECE = 8, STEP = PIECE * T, MOST_SLICES = BINS / WAVES;
 constexpr int OWN = BINS / T;  // bins (or chunks) of a thread
@@ -102,31 +100,69 @@ __device__ __forceinline__ float logit_at(const void* row, int64_t i) {
   else if constexpr (TYPE == 1) return BF16::value(static_cast<const uint16_t*>(row)[i]);
   else return static_cast<const float*>(row)[i];
 }
-// PIECE logits from i on; those from `end` on are -infinity.  (Rows may begin at
-// any element.)
+// PIECE logits from i on, as they are in memory, and as floats.  (Rows may begin
+// at any element.)
+template <int TYPE>
+struct Raw {
+  u4 w[TYPE == 2 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* row, int i) {
+    if constexpr (TYPE == 2) {
+      typedef uint32_t loose __attribute__((ext_vector_type(4), aligned(4)));
+      const uint32_t* p = static_cast<const uint32_t*>(row) + i;
+      w[0] = *reinterpret_cast<const loose*>(p);
+      w[1] = *reinterpret_cast<const loose*>(p + 4);
+    } else {
+      typedef uint32_t loose __attribute__((ext_vector_type(4), aligned(2)));
+      w[0] = *reinterpret_cast<const loose*>(static_cast<const uint16_t*>(row) + i);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[PIECE]) const {
+#pragma unroll
+    for (int e = 0; e < PIECE; ++e) {
+      if constexpr (TYPE == 2) {
+        v[e] = clean(__uint_as_float(w[e / 4][e & 3]));
+      } else {
+        const uint16_t h = (uint16_t)(w[0][e / 2] >> (16 * (e & 1)));
+        v[e] = clean(TYPE == 0 ? F16::value(h) : BF16::value(h));
+      }
+    }
+  }
+};
+// the same where the row may end inside the piece: those from `end` on are
+// -infinity
 template <int TYPE>
 __device__ __forceinline__ void load_piece(const void* row, int i, int end, float (&v)[PIECE]) {
   if (i + PIECE <= end) {
-    if constexpr (TYPE == 2) {
-      typedef float loose4 __attribute__((ext_vector_type(4), aligned(4)));
-      const float* p = static_cast<const float*>(row) + i;
-      const f4 a = *reinterpret_cast<const loose4*>(p), b = *reinterpret_cast<const loose4*>(p + 4);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
-    } else {
-      typedef uint32_t loose __attribute__((ext_vector_type(4), aligned(2)));
-      const u4 a = *reinterpret_cast<const loose*>(static_cast<const uint16_t*>(row) + i);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint16_t h = (uint16_t)(a[e / 2] >> (16 * (e & 1)));
-        v[e] = TYPE == 0 ? F16::value(h) : BF16::value(h);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < PIECE; ++e) v[e] = clean(v[e]);
+    Raw<TYPE> r;
+    r.load(row, i);
+    r.get(v);
   } else {
 #pragma unroll
     for (int e = 0; e < PIECE; ++e) v[e] = i + e < end ? clean(logit_at<TYPE>(row, i + e)) : NEG_INF;
+  }
+}
+// f(piece, its first index) for the pieces of [begin, end), THREADS at a time,
+// this one's first at begin + PIECE * thread; four are on their way at once.
+template <int TYPE, int THREADS, typename F>
+__device__ __forceinline__ void pieces(const void* row, int begin, int end, int thread, F&& f) {
+  constexpr int AT_ONCE = 4, ROUND = PIECE * THREADS;
+  int i = begin + PIECE * thread, at = begin;
+  for (; at + AT_ONCE * ROUND <= end; at += AT_ONCE * ROUND) {
+    Raw<TYPE> r[AT_ONCE];
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) r[k].load(row, i + k * ROUND);
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) {
+      float v[PIECE];
+      r[k].get(v);
+      f(v, i + k * ROUND);
+    }
+    i += AT_ONCE * ROUND;
+  }
+  for (; i < end; i += ROUND) {
+    float v[PIECE];
+    load_piece<TYPE>(row, i, end, v);
+    f(v, i);
   }
 }
 
@@ -268,12 +304,18 @@ __device__ __forceinline__ Top top_of(const Part& p, unsigned long long* red) {
   return {best, logit_of(~(uint32_t)low)};
 }
 
-// The bin of a logit l <= M: the same or a later one for every smaller l.
+// The bin of a logit l <= M: the same or a later one for every smaller l.  Bins
+// go from the largest logit to the smallest, or to where weights are 0 (2^-44 of
+// the largest; `ends`: the last bin then has no weights), so that a row masked
+// with large negative numbers has fine bins too.
 struct Binning {
   float most, by;
-  __device__ __forceinline__ Binning(const Top& t) : most(t.most()) {
-    const float width = most - t.least;
-    by = width > 0.f && width < 3e38f ? (float)BINS / width : 0.f;
+  bool ends;
+  __device__ __forceinline__ Binning(const Top& t, const Settings& set) : most(t.most()) {
+    const float width = most - t.least, all = (float)fmin(44.0 / set.by, 3e38);
+    ends = !(width <= all);
+    const float used = ends ? all : width;
+    by = used > 0.f ? (float)BINS / used : 0.f;
   }
   // in bins from the largest logit on; past the last one (and NaN, of
   // infinities) the last one
@@ -282,17 +324,17 @@ struct Binning {
     return l == most ? 0.f : d < (float)BINS - 0.001f ? d : (float)BINS - 0.001f;
   }
   __device__ __forceinline__ int operator()(float l) const { return (int)at(l); }
-  // a 1024th part of its bin, the same order
-  __device__ __forceinline__ int part(float l) const {
-    const float d = at(l);
-    return (int)((d - (float)(int)d) * (float)BINS);
+  // one of 1024 parts of the bins [first, last], the same order, for l in them
+  __device__ __forceinline__ int part(float l, int first, int last) const {
+    const float d = (at(l) - (float)first) * ((float)BINS / (float)(last + 1 - first));
+    return d < (float)(BINS - 1) ? (int)d : BINS - 1;
   }
 };
 
 // What follows from a row's histogram (a thread's bins: mine), the same in every
 // workgroup of the row; all threads.
 __device__ __forceinline__ Plan plan_of(const SampleArgs& a, const Settings& set, const unsigned long long (&mine)[OWN],
-                                        unsigned long long* red, Plan* shared) {
+                                        bool ends, unsigned long long* red, Plan* shared) {
   const bool by_count = set.by_count(a.vocab), by_weight = set.by_weight();
   if (!by_count && !by_weight) return Plan{CUT_NONE, BINS, 0, 0.0, 0};
   unsigned long long sum = 0, total;
@@ -300,8 +342,9 @@ __device__ __forceinline__ Plan plan_of(const SampleArgs& a, const Settings& set
   for (int e = 0; e < OWN; ++e) sum += mine[e];
   if (threadIdx.x == 0) *shared = Plan{CUT_NONE, BINS, 0, 0.0, 0};
   unsigned long long before = block_scan64(sum, total, red) - sum;
-  // by count: the first bin with k elements up to it (all may be fewer); by
-  // weight: the first up to which the weights reach p S
+  // by count: the first bin with k elements up to it (all may be fewer; among
+  // elements without weight it does not matter which stay); by weight: the first
+  // up to which the weights reach p S
   const double goal = by_count ? (double)set.k : set.p * (double)total;
 #pragma unroll
   for (int e = 0; e < OWN; ++e) {
@@ -309,7 +352,7 @@ __device__ __forceinline__ Plan plan_of(const SampleArgs& a, const Settings& set
     const int b = OWN * threadIdx.x + e;
     if ((double)upto >= goal && (b == 0 || (double)before < goal)) {
       Plan p{CUT_BIN, b, before, goal, total};
-      if (by_count) p.mode = upto <= CAP ? CUT_FEW : by_weight ? CUT_MANY : CUT_BIN;
+      if (by_count) p.mode = upto <= CAP ? CUT_FEW : by_weight ? CUT_MANY : ends && b == BINS - 1 ? CUT_NONE : CUT_BIN;
       *shared = p;
     }
     before = upto;
@@ -338,10 +381,7 @@ __global__ void __launch_bounds__(T) sample_scan_kernel(SampleArgs a, int slices
   const void* x = static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes;
   float most = NEG_INF, least = __builtin_inff();
   int at = begin;
-#pragma unroll 4
-  for (int i = begin + PIECE * threadIdx.x; i < end; i += STEP) {
-    float v[PIECE];
-    load_piece<TYPE>(x, i, end, v);
+  pieces<TYPE, T>(x, begin, end, threadIdx.x, [&](const float (&v)[PIECE], int i) {
     float hi = v[0], lo = v[0];
 #pragma unroll
     for (int e = 1; e < PIECE; ++e) hi = fmaxf(hi, v[e]), lo = fminf(lo, v[e]);
@@ -358,7 +398,7 @@ __global__ void __launch_bounds__(T) sample_scan_kernel(SampleArgs a, int slices
       for (int e = 0; e < PIECE; ++e) lo = v[e] > NEG_INF ? fminf(lo, v[e]) : lo;
     }
     least = fminf(least, lo);
-  }
+  });
   unsigned long long best = wave_max64((unsigned long long)key_of(most) << 32 | (uint32_t)~at);
   least = logit_of(~(uint32_t)wave_max64((uint32_t)~key_of(least)));
   if ((threadIdx.x & 63) == 0) {
@@ -392,15 +432,12 @@ __global__ void __launch_bounds__(T) sample_bins_kernel(SampleArgs a, int slices
   const Work w(a.ws, a.rows, slices);
   for (int i = threadIdx.x; i < BINS; i += T) bins[i] = 0;
   const Top top = top_of(part_of(w.parts + (int64_t)row * slices, slices), red);  // (with barriers)
-  const Binning bin(top);
+  const Binning bin(top, set);
   const Weigh weigh{(double)top.most(), set.by};
   const int begin = s * slice, end = min(begin + slice, a.vocab);
   const void* x = static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes;
   uint32_t* counts = reinterpret_cast<uint32_t*>(bins);
-#pragma unroll 2
-  for (int i = begin + PIECE * threadIdx.x; i < end; i += STEP) {
-    float v[PIECE];
-    load_piece<TYPE>(x, i, end, v);
+  pieces<TYPE, T>(x, begin, end, threadIdx.x, [&](const float (&v)[PIECE], int) {
     if (by_count) {
 #pragma unroll
       for (int e = 0; e < PIECE; ++e)
@@ -412,7 +449,7 @@ __global__ void __launch_bounds__(T) sample_bins_kernel(SampleArgs a, int slices
         if (f) atomicAdd(&bins[bin(v[e])], f);
       }
     }
-  }
+  });
   __syncthreads();
   for (int i = threadIdx.x; i < BINS; i += T) {
     const unsigned long long f = by_count ? counts[i] : bins[i];
@@ -437,19 +474,16 @@ __global__ void __launch_bounds__(T) sample_sums_kernel(SampleArgs a, int slices
   own_bins(a, w.bins + (int64_t)row * BINS, mine);
   const Settings set(a, row);
   if (set.greedy) return;
-  const Plan plan = plan_of(a, set, mine, red, &plan_s);
-  if (plan.mode == CUT_MANY) return;
   const Top top = top_of(part, red);  // (with barriers)
-  const Binning bin(top);
+  const Binning bin(top, set);
+  const Plan plan = plan_of(a, set, mine, bin.ends, red, &plan_s);
+  if (plan.mode == CUT_MANY) return;
   const Weigh weigh{(double)top.most(), set.by};
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int first = s * slice, begin = first + wave * (slice / WAVES), end = min(begin + slice / WAVES, a.vocab);
   const void* x = static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes;
   unsigned long long sum = 0;
-#pragma unroll 2
-  for (int i = begin + PIECE * lane; i < end; i += PIECE * 64) {
-    float v[PIECE];
-    load_piece<TYPE>(x, i, end, v);
+  pieces<TYPE, 64>(x, begin, end, lane, [&](const float (&v)[PIECE], int i) {
 #pragma unroll
     for (int e = 0; e < PIECE; ++e) {
       const int b = plan.mode == CUT_NONE ? 0 : bin(v[e]);
@@ -462,7 +496,7 @@ __global__ void __launch_bounds__(T) sample_sums_kernel(SampleArgs a, int slices
         if (at < CAP) list[at] = (uint16_t)(i + e - first);
       }
     }
-  }
+  });
   sum = wave_scan64(sum);
   if (lane == 63) w.sums[((int64_t)row * slices + s) * WAVES + wave] = sum;
   if (plan.mode == CUT_NONE) return;
@@ -490,7 +524,7 @@ __device__ __forceinline__ unsigned long long target_of(float u, unsigned long l
 __device__ __forceinline__ int power_of_two(int n) { return n < 2 ? 1 : 1 << (32 - __builtin_clz(n - 1)); }
 
 struct Shared {
-  unsigned long long list[CAP];
+  unsigned long long list[CAP], few[CAP];
   unsigned long long bins[BINS];  // of counts, weights or chunks' sums
   uint32_t counts[BINS];
   unsigned long long red[2 * WAVES];
@@ -500,68 +534,32 @@ struct Shared {
   int n, at;
 };
 
-// Sorts E entries a thread upwards (entry T e + thread, n of them, a power of
-// two): partners within a wave change places by lanes, others within a thread or
-// through the list.
-template <int E>
-__device__ __forceinline__ void sort_held(unsigned long long* list, int n) {
-  const int t = threadIdx.x;
-  unsigned long long v[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = T * e + t < n ? list[T * e + t] : 0;
-  for (int k = 2; k <= n; k <<= 1) {
-    // a place takes the smaller one of a pair, or the larger
-    auto take = [&](int e, unsigned long long o, int j) {
-      const int i = T * e + t;
-      v[e] = (o < v[e]) == (((i & j) == 0) == ((i & k) == 0)) ? o : v[e];
-    };
-    auto lanes = [&](auto by) {
-      constexpr int J = decltype(by)::value;
-#pragma unroll
-      for (int e = 0; e < E; ++e) take(e, lane_xor<J>(v[e]), J);
-    };
-#pragma unroll
-    for (int j = E / 2; j > 0; j >>= 1)
-      if (k > T * j) {
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (!(e & j)) {
-            const unsigned long long x = v[e], y = v[e | j];
-            take(e, y, T * j);
-            take(e | j, x, T * j);
-          }
-      }
-    for (int j = min(k, T) >> 1; j >= 64; j >>= 1) {
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (T * e + t < n) list[T * e + t] = v[e];
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (T * e + t < n) take(e, list[(T * e + t) ^ j], j);
-    }
-    if (k >= 64) lanes(std::integral_constant<int, 32>{});
-    if (k >= 32) lanes(std::integral_constant<int, 16>{});
-    if (k >= 16) lanes(std::integral_constant<int, 8>{});
-    if (k >= 8) lanes(std::integral_constant<int, 4>{});
-    if (k >= 4) lanes(std::integral_constant<int, 2>{});
-    lanes(std::integral_constant<int, 1>{});
-  }
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    if (T * e + t < n) list[T * e + t] = v[e];
-}
-
 // Sorts list[0 .. n) (n a power of two up to CAP) upwards; the whole workgroup,
-// barriers on both sides.
+// barriers on both sides.  Up to an entry a thread they stay in registers:
+// partners within a wave change places by lanes, others through the list.
 __device__ __forceinline__ void sort(unsigned long long* list, int n) {
   __syncthreads();
   if (n <= T) {
-    sort_held<1>(list, n);
-  } else if (n <= 4 * T) {
-    sort_held<4>(list, n);
+    const int t = threadIdx.x;
+    unsigned long long v = t < n ? list[t] : 0;
+    for (int k = 2; k <= n; k <<= 1) {
+      // this place takes the smaller one of a pair, or the larger
+      auto take = [&](unsigned long long o, int j) { v = (o < v) == (((t & j) == 0) == ((t & k) == 0)) ? o : v; };
+      for (int j = k >> 1; j >= 64; j >>= 1) {
+        __syncthreads();
+        if (t < n) list[t] = v;
+        __syncthreads();
+        if (t < n) take(list[t ^ j], j);
+      }
+      if (k >= 64) take(lane_xor<32>(v), 32);
+      if (k >= 32) take(lane_xor<16>(v), 16);
+      if (k >= 16) take(lane_xor<8>(v), 8);
+      if (k >= 8) take(lane_xor<4>(v), 4);
+      if (k >= 4) take(lane_xor<2>(v), 2);
+      take(lane_xor<1>(v), 1);
+    }
+    __syncthreads();
+    if (t < n) list[t] = v;
   } else {
     for (int k = 2; k <= n; k <<= 1)
       for (int j = k >> 1; j > 0; j >>= 1) {
@@ -596,31 +594,28 @@ struct OneRow {
   // f(logit, index) for the row's elements that are not -infinity
   template <typename F>
   __device__ __forceinline__ void each(F&& f) const {
-#pragma unroll 2
-    for (int i = PIECE * threadIdx.x; i < a.vocab; i += STEP) {
-      float v[PIECE];
-      load_piece<TYPE>(x, i, a.vocab, v);
+    pieces<TYPE, T>(x, 0, a.vocab, threadIdx.x, [&](const float (&v)[PIECE], int i) {
 #pragma unroll
       for (int e = 0; e < PIECE; ++e)
         if (v[e] != NEG_INF) f(v[e], i + e);
-    }
+    });
   }
 
-  // Sorts the n entries that are in the list.
+  // Sorts the n entries that are in `few`.
   __device__ __forceinline__ void order(int n) const {
     const int m = power_of_two(n);
-    for (int i = n + threadIdx.x; i < m; i += T) sh.list[i] = ~0ull;
-    sort(sh.list, m);
+    for (int i = n + threadIdx.x; i < m; i += T) sh.few[i] = ~0ull;
+    sort(sh.few, m);
   }
-  // The last of the n sorted entries that stays.  By count: the `want`th (from
+  // The last of the n sorted entries of `few` that stays.  By count: the `want`th (from
   // 1).  By weight: the last with less than `goal` in front of it, `before` of
-  // that in front of the list (the first one, if none has).  `upto`: the weights
+  // that in front of them (the first one, if none has).  `upto`: the weights
   // up to and with it.
   __device__ __forceinline__ int last_of(int n, bool by_weight, uint32_t want, unsigned long long before, double goal,
                                          unsigned long long& upto) const {
     const int each = (n + T - 1) / T, j0 = each * (int)threadIdx.x, j1 = min(j0 + each, n);  // a thread's entries
     unsigned long long total, sum = 0;
-    for (int j = j0; j < j1; ++j) sum += weight_of(key_in(sh.list[j]));
+    for (int j = j0; j < j1; ++j) sum += weight_of(key_in(sh.few[j]));
     if (threadIdx.x == 0) sh.at = by_weight ? 0 : max((int)min(want, (uint32_t)n) - 1, 0);
     sum = scan(sum, total) - sum;
     if (by_weight) {
@@ -628,14 +623,14 @@ struct OneRow {
       unsigned long long at = before + sum;
       for (int j = j0; j < j1; ++j) {
         last = (double)at < goal ? j : last;
-        at += weight_of(key_in(sh.list[j]));
+        at += weight_of(key_in(sh.few[j]));
       }
       if (last) atomicMax(&sh.at, last);
       __syncthreads();
     }
     const int l = sh.at;
     if (j0 <= l && l < j1) {
-      for (int j = j0; j <= l; ++j) sum += weight_of(key_in(sh.list[j]));
+      for (int j = j0; j <= l; ++j) sum += weight_of(key_in(sh.few[j]));
       sh.found = sum;
     }
     __syncthreads();
@@ -644,14 +639,15 @@ struct OneRow {
     return l;
   }
 
-  // Sums over sh.bins (a thread's OWN ones side by side), in place.
-  __device__ __forceinline__ void sum_bins() const {
+  // Sums over sh.bins or sh.counts (a thread's OWN ones side by side), in place.
+  template <typename N>
+  __device__ __forceinline__ void sum_up(N* bins) const {
     unsigned long long mine[OWN], sum = 0, total;
 #pragma unroll
-    for (int e = 0; e < OWN; ++e) mine[e] = sum += sh.bins[OWN * threadIdx.x + e];
+    for (int e = 0; e < OWN; ++e) mine[e] = sum += bins[OWN * threadIdx.x + e];
     const unsigned long long before = scan(sum, total) - sum;
 #pragma unroll
-    for (int e = 0; e < OWN; ++e) sh.bins[OWN * threadIdx.x + e] = before + mine[e];
+    for (int e = 0; e < OWN; ++e) bins[OWN * threadIdx.x + e] = (N)(before + mine[e]);
     __syncthreads();
   }
   // The first bin up to which sums reach a goal, as reaches(bin) says (false,
@@ -706,17 +702,8 @@ struct OneRow {
         atomicAdd(&sh.bins[r], fixed(weigh(l)));
       });
       __syncthreads();
-      sum_bins();
-      {  // counts likewise
-        uint32_t mine[OWN], sum = 0;
-#pragma unroll
-        for (int e = 0; e < OWN; ++e) mine[e] = sum += sh.counts[OWN * threadIdx.x + e];
-        unsigned long long total;
-        const uint32_t before = (uint32_t)scan(sum, total) - sum;
-#pragma unroll
-        for (int e = 0; e < OWN; ++e) sh.counts[OWN * threadIdx.x + e] = before + mine[e];
-        __syncthreads();
-      }
+      sum_up(sh.bins);
+      sum_up(sh.counts);
       const int r = first_bin([&](int i) {
         return by_weight ? (double)(inside + sh.bins[i]) >= goal : sh.counts[i] >= want;
       });
@@ -730,13 +717,13 @@ struct OneRow {
       if (threadIdx.x == 0) sh.n = 0;
       __syncthreads();
       each([&](float l, int i) {
-        if (in(l)) sh.list[atomicAdd(&sh.n, 1)] = (unsigned long long)~key_of(l) << 32 | (uint32_t)i;
+        if (in(l)) sh.few[atomicAdd(&sh.n, 1)] = (unsigned long long)~key_of(l) << 32 | (uint32_t)i;
       });
       __syncthreads();
       order(n);
       const int j = last_of(n, by_weight, want, inside, goal, upto);
       upto += inside;
-      const unsigned long long entry = sh.list[j];
+      const unsigned long long entry = sh.few[j];
       __syncthreads();
       return Cut{key_in(entry), (int)(uint32_t)entry};
     }
@@ -773,45 +760,76 @@ struct OneRow {
     return Cut{high, place};
   }
 
-  // The end of a prefix among the n listed elements of one bin, `before` (counts
-  // or weights) in front of them: first by 1024 parts of the bin, then by the
-  // sorted elements of one part.  The entries that stay are those up to the cut.
-  __device__ __forceinline__ Cut end_in_bin(int n, bool by_weight, unsigned long long before, double goal) const {
-    for (int i = threadIdx.x; i < BINS; i += T) sh.bins[i] = 0;
-    if (threadIdx.x == 0) sh.n = 0;
+  // Counts and weights of the n listed elements, which are in the bins [first,
+  // last], up to each of 1024 parts of these.
+  __device__ __forceinline__ void parts(int n, int first, int last) const {
+    for (int i = threadIdx.x; i < BINS; i += T) sh.bins[i] = 0, sh.counts[i] = 0;
     __syncthreads();
     for (int j = threadIdx.x; j < n; j += T) {
       const uint32_t key = key_in(sh.list[j]);
-      atomicAdd(&sh.bins[bin.part(logit_of(key))], by_weight ? weight_of(key) : 1ull);
+      const int p = bin.part(logit_of(key), first, last);
+      atomicAdd(&sh.bins[p], weight_of(key));
+      atomicAdd(&sh.counts[p], 1u);
     }
     __syncthreads();
-    sum_bins();
-    const int r = first_bin([&](int i) { return (double)(before + sh.bins[i]) >= goal; });
-    before += r ? sh.bins[r - 1] : 0;
-    // that part's entries in front of the others (which stay where they are
-    // listed in global memory)
-    constexpr int MORE = CAP / T;
-    unsigned long long mine[MORE];
-    uint32_t are = 0;
-#pragma unroll
-    for (int e = 0; e < MORE; ++e) {
-      const int j = T * e + threadIdx.x;
-      if (T * e >= n) break;
-      mine[e] = j < n ? sh.list[j] : 0;
-      are |= j < n && bin.part(logit_of(key_in(mine[e]))) == r ? 1u << e : 0u;
-    }
+    sum_up(sh.bins);
+    sum_up(sh.counts);
+  }
+  // Puts those of the n listed elements that `in` accepts into `few`, made into
+  // entries by `as`, and sorts them; how many.
+  template <typename F, typename G>
+  __device__ __forceinline__ int pick(int n, F&& in, G&& as) const {
+    if (threadIdx.x == 0) sh.n = 0;
     __syncthreads();
-#pragma unroll
-    for (int e = 0; e < MORE; ++e)
-      if (are >> e & 1) sh.list[atomicAdd(&sh.n, 1)] = mine[e];
+    for (int j = threadIdx.x; j < n; j += T) {
+      const unsigned long long entry = sh.list[j];
+      if (in(entry)) sh.few[atomicAdd(&sh.n, 1)] = as(entry);
+    }
     __syncthreads();
     const int m = sh.n;
     order(m);
-    unsigned long long upto;
-    const int l = last_of(m, by_weight, by_weight ? 1 : (uint32_t)(goal - (double)before), before, goal, upto);
-    const unsigned long long entry = sh.list[l];
+    return m;
+  }
+  // The end of a prefix among them: the part in which it lies, then its sorted
+  // elements.  By count: the `want`th (from 1); by weight: as last_of, `before` in
+  // front of all.  `upto`: the weights up to and with it.
+  __device__ __forceinline__ Cut end_in(int n, int first, int last, bool by_weight, uint32_t want, unsigned long long before,
+                                        double goal, unsigned long long& upto) const {
+    const int r = first_bin([&](int i) { return by_weight ? (double)(before + sh.bins[i]) >= goal : sh.counts[i] >= want; });
+    const unsigned long long inside = r ? sh.bins[r - 1] : 0;
+    want -= r ? min(sh.counts[r - 1], want) : 0;
+    const int m = pick(n, [&](unsigned long long e) { return bin.part(logit_of(key_in(e)), first, last) == r; },
+                       [](unsigned long long e) { return e; });
+    const int l = last_of(m, by_weight, want, before + inside, goal, upto);
+    upto += inside;
+    const unsigned long long entry = sh.few[l];
     __syncthreads();
     return Cut{key_in(entry), (int)(uint32_t)entry};
+  }
+  // The weight that an entry adds to what is kept.
+  __device__ __forceinline__ unsigned long long kept(unsigned long long entry, Cut cut) const {
+    const uint32_t key = key_in(entry);
+    if (key < cut.key || (key == cut.key && (int)(uint32_t)entry > cut.at)) return 0;
+    const double p = weigh(logit_of(key));
+    return p >= set.least ? fixed(p) : 0;
+  }
+  // The chunk (of sh.bins, a thread's OWN ones side by side) in which the draw
+  // falls, its place there and what is in front of it.
+  __device__ __forceinline__ int chunk_of(float u, unsigned long long& before, unsigned long long& t) const {
+    unsigned long long sum = 0, own[OWN], total;
+#pragma unroll
+    for (int e = 0; e < OWN; ++e) sum += own[e] = sh.bins[OWN * threadIdx.x + e];
+    if (threadIdx.x == 0) sh.at = 0, sh.found = 0;
+    unsigned long long at = scan(sum, total) - sum;
+    t = target_of(u, total);
+#pragma unroll
+    for (int e = 0; e < OWN; ++e) {
+      if (at <= t && t < at + own[e]) sh.at = OWN * threadIdx.x + e, sh.found = at;
+      at += own[e];
+    }
+    __syncthreads();
+    before = sh.found;
+    return sh.at;
   }
 
   // The token, among elements [begin, end): the first up to which the kept
@@ -870,13 +888,13 @@ __global__ void __launch_bounds__(T) sample_draw_kernel(SampleArgs a, int slices
     if (threadIdx.x == 0) *out = top.most() == NEG_INF ? -1 : top.place();
     return;
   }
-  const OneRow<TYPE> r{a, set, sh, static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes, Binning(top),
+  const OneRow<TYPE> r{a, set, sh, static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes, Binning(top, set),
                        Weigh{(double)top.most(), set.by}};
   const bool by_count = set.by_count(a.vocab), by_weight = set.by_weight();
   if (by_count || by_weight)
     for (int j = threadIdx.x; j < min(listed, CAP); j += T) sh.list[j] = list[j];
-  const Plan plan = plan_of(a, set, mine, sh.red, &sh.plan);  // (with barriers)
-  unsigned long long total, upto;
+  const Plan plan = plan_of(a, set, mine, r.bin.ends, sh.red, &sh.plan);  // (with barriers)
+  unsigned long long total, upto, before, t;
 
   if (plan.mode == CUT_MANY || (plan.mode != CUT_NONE && listed > CAP)) {
     // the row alone, from its logits
@@ -893,66 +911,51 @@ __global__ void __launch_bounds__(T) sample_draw_kernel(SampleArgs a, int slices
   }
 
   const int n = plan.mode == CUT_NONE ? 0 : listed;
+  Cut cut{0, 0};
   if (plan.mode == CUT_FEW) {
-    r.order(n);
-    int kept = by_count ? min(set.k, n) : n;
-    if (by_weight) {
-      r.last_of(n, false, (uint32_t)kept, 0, 0.0, upto);
-      kept = min(kept, 1 + r.last_of(n, true, 1, 0, set.p * (double)upto, upto));
-    }
-    // (min-p keeps a prefix of these; then by index)
-    const int m = power_of_two(kept);
+    // everything from the list: the ends, then the draw by chunks of the
+    // vocabulary
+    const int last = min(plan.bin, BINS - 1);
+    r.parts(n, 0, last);
+    cut = r.end_in(n, 0, last, false, (uint32_t)min(set.k, n), 0, 0.0, upto);
+    if (by_weight) cut = r.end_in(n, 0, last, true, 1, 0, set.p * (double)upto, upto);
+    const uint32_t chunk = (uint32_t)(a.vocab + BINS - 1) / BINS;
+    for (int i = threadIdx.x; i < BINS; i += T) sh.bins[i] = 0;
     __syncthreads();
-    for (int j = threadIdx.x; j < m; j += T) {
-      const unsigned long long entry = sh.list[j];
-      const bool stays = j < kept && (j == 0 || r.weigh(logit_of(r.key_in(entry))) >= set.least);
-      sh.list[j] = stays ? entry << 32 | entry >> 32 : ~0ull;
+    for (int j = threadIdx.x; j < n; j += T) {
+      const unsigned long long w = r.kept(sh.list[j], cut);
+      if (w) atomicAdd(&sh.bins[(uint32_t)sh.list[j] / chunk], w);
     }
-    sort(sh.list, m);
-    const int each = (m + T - 1) / T, j0 = min(each * (int)threadIdx.x, m), j1 = min(j0 + each, m);
-    unsigned long long sum = 0;
-    auto weight_at = [&](int j) { return sh.list[j] == ~0ull ? 0ull : r.weight_of(~(uint32_t)sh.list[j]); };
-    for (int j = j0; j < j1; ++j) sum += weight_at(j);
-    sum = r.scan(sum, total) - sum;
-    const unsigned long long t = target_of(u, total);
-    for (int j = j0; j < j1; ++j) {
-      const unsigned long long w = weight_at(j);
-      if (sum <= t && t < sum + w) *out = (int)(sh.list[j] >> 32);
-      sum += w;
-    }
+    __syncthreads();
+    const uint32_t c = (uint32_t)r.chunk_of(u, before, t);
+    const int m = r.pick(n, [&](unsigned long long e) { return (uint32_t)e / chunk == c && r.kept(e, cut); },
+                         [](unsigned long long e) { return e << 32 | e >> 32; });
+    if (threadIdx.x == 0)
+      for (int j = 0; j < m; ++j) {  // (a chunk has few)
+        const unsigned long long w = r.weight_of(~(uint32_t)sh.few[j]);
+        if (before <= t && t < before + w) *out = (int)(sh.few[j] >> 32);
+        before += w;
+      }
     return;
   }
 
   // the chunks' sums, and to each what it keeps of the list
-  Cut cut{0, 0};
-  if (n) cut = r.end_in_bin(n, !by_count, plan.before, plan.goal);
+  if (n) {
+    r.parts(n, plan.bin, plan.bin);
+    cut = r.end_in(n, plan.bin, plan.bin, !by_count, by_count ? (uint32_t)(set.k - (int)plan.before) : 1,
+                   by_count ? 0 : plan.before, plan.goal, upto);
+  }
 #pragma unroll
   for (int e = 0; e < OWN; ++e) sh.bins[OWN * threadIdx.x + e] = sums[e];
   __syncthreads();
   const int chunk = slice / WAVES;
   for (int j = threadIdx.x; j < n; j += T) {
-    const unsigned long long entry = list[j];
-    const uint32_t key = r.key_in(entry), i = (uint32_t)entry;
-    if (key < cut.key || (key == cut.key && (int)i > cut.at)) continue;
-    const double p = r.weigh(logit_of(key));
-    if (p >= set.least) atomicAdd(&sh.bins[i / (uint32_t)chunk], fixed(p));
+    const unsigned long long w = r.kept(sh.list[j], cut);
+    if (w) atomicAdd(&sh.bins[(uint32_t)sh.list[j] / (uint32_t)chunk], w);
   }
   __syncthreads();
-  unsigned long long sum = 0, own[OWN];
-#pragma unroll
-  for (int e = 0; e < OWN; ++e) sum += own[e] = sh.bins[OWN * threadIdx.x + e];
-  unsigned long long at = r.scan(sum, total) - sum;
-  const unsigned long long t = target_of(u, total);
-  if (threadIdx.x == 0) sh.key0 = 0, sh.found = 0;
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < OWN; ++e) {
-    if (at <= t && t < at + own[e]) sh.key0 = OWN * threadIdx.x + e, sh.found = at;
-    at += own[e];
-  }
-  __syncthreads();
-  const int begin = (int)sh.key0 * chunk, end = min(begin + chunk, a.vocab);
-  r.draw(begin, end, cut, sh.found, t, out);
+  const int begin = r.chunk_of(u, before, t) * chunk;
+  r.draw(begin, min(begin + chunk, a.vocab), cut, before, t, out);
 }
 
 // Logits of a slice: about 1024 workgroups over all rows, between 2048 and
