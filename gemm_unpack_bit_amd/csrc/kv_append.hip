@@ -18,6 +18,10 @@
 // (row, position, page, exponent).  A lane has 16 elements: two pieces of 8,
 // whose pairs turn by the same eight angles in every head, so a wave works out
 // the sines of its token once for all heads that it takes.
+//
+// Measured: 48 tokens of 32 heads over 8 into 16 bits 4.2 us, into 8 bits 5;
+// 8192 tokens of 64 heads over 8 into 16 bits 65 us (335 MB, 5.2 TB/s), into 8
+// bits 63; 10000 tokens read back out of 8 bits 14 us.
 #include "e4m3.hpp"
 
 namespace qg {
@@ -93,11 +97,27 @@ __device__ __forceinline__ int64_t pool_place(const KvArgs& c, int b, int64_t p)
 }
 
 // Heads of one token by one wave: `n` heads from `h0` on of the queries, then
-// keys, then values (a cache of 8 bits: of the queries).
+// keys, then values (a cache of 8 bits: of the queries).  2 H of them are on
+// their way at any time, the first ones while their place is found.
 template <typename E, int D, bool TURN>
 __device__ __forceinline__ void token_heads(const KvAppendArgs& a, int t, int h0, int n) {
   constexpr int U = D / 16, H = 64 / U;  // units of a head, heads at a time
   const int lane = threadIdx.x & 63, u = lane % U;
+  const Unit<D> unit(a, u);
+  u4 next[2][2];
+  auto load = [&](int i) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (i + H * x >= n) continue;
+      const int h = h0 + i + H * x, hk = h - a.heads, hv = hk - a.c.heads_kv;
+      const uint16_t* from = hk < 0   ? a.q + (int64_t)t * a.q_token + h * a.q_head
+                             : hv < 0 ? a.k + (int64_t)t * a.k_token + hk * a.k_head
+                                      : a.v + (int64_t)t * a.v_token + hv * a.v_head;
+      next[x][0] = *reinterpret_cast<const u4*>(from + unit.first);
+      next[x][1] = *reinterpret_cast<const u4*>(from + unit.second);
+    }
+  };
+  load(lane / U);
   const Place w = place_of(a.cu, a.c.rows, t);
   if (w.b < 0) return;
   const int p0 = a.pos[w.b];
@@ -105,34 +125,37 @@ __device__ __forceinline__ void token_heads(const KvAppendArgs& a, int t, int h0
   const int64_t p = (int64_t)p0 + w.i;
   const int64_t at = h0 + n > a.heads ? pool_place(a.c, w.b, p) : -1;
   const int64_t row = (int64_t)a.c.heads_kv * D;
-  const Unit<D> unit(a, u);
   Angles ang;
   if (TURN && unit.turns) ang.set(a, u, a.at ? a.at[t] : (int)p);
-#pragma unroll 2
-  for (int i = lane / U; i < n; i += H) {
-    const int h = h0 + i, hk = h - a.heads, hv = hk - a.c.heads_kv;
-    const uint16_t* from;
-    uint16_t* to;
-    if (hk < 0) {
-      from = a.q + (int64_t)t * a.q_token + h * a.q_head;
-      to = a.o + (int64_t)t * a.o_token + h * a.o_head;
-    } else {
-      if (at < 0) continue;
-      from = hv < 0 ? a.k + (int64_t)t * a.k_token + hk * a.k_head : a.v + (int64_t)t * a.v_token + hv * a.v_head;
-      const int64_t in_layer = ((int64_t)a.layer * a.c.pages << a.c.page_shift) + at;
-      to = (hv < 0 ? a.c.k : a.c.v) + in_layer * row + (hv < 0 ? hk : hv) * D;
+  for (int i = lane / U; i < n; i += 2 * H) {
+    u4 now[2][2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) now[x][0] = next[x][0], now[x][1] = next[x][1];
+    load(i + 2 * H);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (i + H * x >= n) continue;
+      const int h = h0 + i + H * x, hk = h - a.heads, hv = hk - a.c.heads_kv;
+      uint16_t* to;
+      if (hk < 0) {
+        to = a.o + (int64_t)t * a.o_token + h * a.o_head;
+      } else {
+        if (at < 0) continue;
+        const int64_t in_layer = ((int64_t)a.layer * a.c.pages << a.c.page_shift) + at;
+        to = (hv < 0 ? a.c.k : a.c.v) + in_layer * row + (hv < 0 ? hk : hv) * D;
+      }
+      u4 lo = now[x][0], hi = now[x][1];
+      if (TURN && unit.turns && hv < 0) {
+        float v[16];
+        unpack16<E>(lo, hi, v);
+        if (a.interleaved) ang.turn(v, true);
+        else ang.turn(v, false);
+        lo = pack8<E>(v);
+        hi = pack8<E>(v + 8);
+      }
+      *reinterpret_cast<u4*>(to + unit.first) = lo;
+      *reinterpret_cast<u4*>(to + unit.second) = hi;
     }
-    u4 lo = *reinterpret_cast<const u4*>(from + unit.first), hi = *reinterpret_cast<const u4*>(from + unit.second);
-    if (TURN && unit.turns && hv < 0) {
-      float x[16];
-      unpack16<E>(lo, hi, x);
-      if (a.interleaved) ang.turn(x, true);
-      else ang.turn(x, false);
-      lo = pack8<E>(x);
-      hi = pack8<E>(x + 8);
-    }
-    *reinterpret_cast<u4*>(to + unit.first) = lo;
-    *reinterpret_cast<u4*>(to + unit.second) = hi;
   }
 }
 
@@ -144,18 +167,31 @@ __device__ __forceinline__ void block_heads(const KvAppendArgs& a, int b, int p0
                                             int h1) {
   constexpr int U = D / 16, TP = 64 / U, PASSES = KV_BLOCK / TP;
   const int lane = threadIdx.x & 63, u = lane % U;
-  const int64_t place = pool_place(a.c, b, first);  // (a block lies in one page)
-  if (place < 0) return;
   const Unit<D> unit(a, u);
   const bool turn = TURN && which == 0 && unit.turns;
   const uint16_t* src = which ? a.v : a.k;
   const int64_t token = which ? a.v_token : a.k_token, head = which ? a.v_head : a.k_head;
-  const int64_t in_layer = ((int64_t)a.layer * a.c.pages << a.c.page_shift) + place;
-  uint8_t* codes = reinterpret_cast<uint8_t*>(which ? a.c.v : a.c.k) + in_layer * a.c.heads_kv * D;
-  uint8_t* exps = (which ? a.c.v_exps : a.c.k_exps) + in_layer / KV_BLOCK * a.c.heads_kv;
   const int64_t end = (int64_t)p0 + n;
   const int i0 = p0 > first ? (int)(p0 - first) : 0, i1 = end - first < KV_BLOCK ? (int)(end - first) : KV_BLOCK;  // new ones
   const int64_t t0 = a.cu[b] + (first - p0);  // the token at the block's first place
+  // (a head's pieces are on their way while the one before it is written)
+  u4 next[PASSES][2];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int x = 0; x < PASSES; ++x) {
+      const int i = TP * x + lane / U;
+      if (i < i0 || i >= i1) continue;
+      const uint16_t* from = src + (t0 + i) * token + h * head;
+      next[x][0] = *reinterpret_cast<const u4*>(from + unit.first);
+      next[x][1] = *reinterpret_cast<const u4*>(from + unit.second);
+    }
+  };
+  load(h0);
+  const int64_t place = pool_place(a.c, b, first);  // (a block lies in one page)
+  if (place < 0) return;
+  const int64_t in_layer = ((int64_t)a.layer * a.c.pages << a.c.page_shift) + place;
+  uint8_t* codes = reinterpret_cast<uint8_t*>(which ? a.c.v : a.c.k) + in_layer * a.c.heads_kv * D;
+  uint8_t* exps = (which ? a.c.v_exps : a.c.k_exps) + in_layer / KV_BLOCK * a.c.heads_kv;
   Angles ang[PASSES];
   if (turn)
 #pragma unroll
@@ -167,12 +203,15 @@ __device__ __forceinline__ void block_heads(const KvAppendArgs& a, int b, int p0
     float v[PASSES][16];
     float most = 0.f;
     const int had = i0 ? exps[h] : 0;
+    u4 raw[PASSES][2];
+#pragma unroll
+    for (int x = 0; x < PASSES; ++x) raw[x][0] = next[x][0], raw[x][1] = next[x][1];
+    if (h + 1 < h1) load(h + 1);
 #pragma unroll
     for (int x = 0; x < PASSES; ++x) {
       const int i = TP * x + lane / U;
       if (i < i0 || i >= i1) continue;
-      const uint16_t* from = src + (t0 + i) * token + h * head;
-      unpack16<E>(*reinterpret_cast<const u4*>(from + unit.first), *reinterpret_cast<const u4*>(from + unit.second), v[x]);
+      unpack16<E>(raw[x][0], raw[x][1], v[x]);
       if (turn) {
         if (a.interleaved) ang[x].turn(v[x], true);
         else ang[x].turn(v[x], false);
@@ -216,31 +255,31 @@ __device__ __forceinline__ void block_heads(const KvAppendArgs& a, int b, int p0
   }
 }
 
-// Work of a wave: first the tokens' heads, `slice` of them at a time, then (8
-// bits) the blocks.  Row b's blocks have the numbers from cu[b] / 16 + 2 b on,
-// which is at least as many as it touches and needs no sum over the rows.
+// Work of a wave: first (8 bits) the blocks, whose waves have more to do, then
+// the tokens' heads, `slice` of them at a time.  Row b's blocks have the numbers
+// from cu[b] / 16 + 2 b on, which is at least as many as it touches and needs no
+// sum over the rows.
 template <typename E, int D, bool TURN, bool Q8>
 __global__ void __launch_bounds__(64 * WAVES) kv_append_kernel(KvAppendArgs a, int slices, int slice, int group) {
-  const int64_t wave = (int64_t)blockIdx.x * WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t heads = (int64_t)a.tokens * slices;
-  if (wave < heads) {
-    const int t = (int)(wave / slices), h0 = (int)(wave % slices) * slice;
-    const int all = Q8 ? a.heads : a.heads + 2 * a.c.heads_kv;
-    token_heads<E, D, TURN>(a, t, h0, min(slice, all - h0));
-    return;
-  }
+  int64_t wave = (int64_t)blockIdx.x * WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if constexpr (Q8) {
     const int parts = 2 * ((a.c.heads_kv + group - 1) / group);
-    const int64_t x = wave - heads, blocks = (int64_t)a.tokens / KV_BLOCK + 2 * (int64_t)a.c.rows;
-    const int slot = (int)(x / parts), part = (int)(x % parts), which = part & 1, h0 = part / 2 * group;
-    if (slot >= blocks) return;
-    const int b = find_row(a.c.rows, slot, [&](int r) { return clamp_cu(a.cu[r], a.tokens) / KV_BLOCK + 2 * r; });
-    const int c0 = clamp_cu(a.cu[b], a.tokens), n = clamp_cu(a.cu[b + 1], a.tokens) - c0, p0 = a.pos[b];
-    if (n <= 0 || p0 < 0 || a.cu[b] != c0) return;
-    const int64_t first = ((int64_t)(p0 / KV_BLOCK) + slot - (c0 / KV_BLOCK + 2 * b)) * KV_BLOCK;
-    if (first < p0 - KV_BLOCK + 1 || first >= (int64_t)p0 + n) return;
-    block_heads<E, D, TURN>(a, b, p0, n, first, which, h0, min(h0 + group, a.c.heads_kv));
+    const int64_t blocks = (int64_t)a.tokens / KV_BLOCK + 2 * (int64_t)a.c.rows;
+    if (wave < blocks * parts) {
+      const int slot = (int)(wave / parts), part = (int)(wave % parts), which = part & 1, h0 = part / 2 * group;
+      const int b = find_row(a.c.rows, slot, [&](int r) { return clamp_cu(a.cu[r], a.tokens) / KV_BLOCK + 2 * r; });
+      const int c0 = clamp_cu(a.cu[b], a.tokens), n = clamp_cu(a.cu[b + 1], a.tokens) - c0, p0 = a.pos[b];
+      if (n <= 0 || p0 < 0 || a.cu[b] != c0) return;
+      const int64_t first = ((int64_t)(p0 / KV_BLOCK) + slot - (c0 / KV_BLOCK + 2 * b)) * KV_BLOCK;
+      if (first < p0 - KV_BLOCK + 1 || first >= (int64_t)p0 + n) return;
+      block_heads<E, D, TURN>(a, b, p0, n, first, which, h0, min(h0 + group, a.c.heads_kv));
+      return;
+    }
+    wave -= blocks * parts;
   }
+  const int t = (int)(wave / slices), h0 = (int)(wave % slices) * slice;
+  const int all = Q8 ? a.heads : a.heads + 2 * a.c.heads_kv;
+  if (wave < (int64_t)a.tokens * slices) token_heads<E, D, TURN>(a, t, h0, min(slice, all - h0));
 }
 
 // One wave per token: units of its keys, then of its values.
@@ -284,12 +323,18 @@ template <typename E, int D, bool TURN, bool Q8>
 hipError_t append(const KvAppendArgs& a, hipStream_t s) {
   constexpr int H = 64 / (D / 16);
   const int all = Q8 ? a.heads : a.heads + 2 * a.c.heads_kv, kv = a.c.heads_kv;
-  const int slice = 2 * H, slices = (all + slice - 1) / slice;
+  // heads of a token that one wave takes with the same sines: 2 H, or twice as
+  // many where enough waves are left (64 + 16 heads of 128, 16 bits: 256 tokens
+  // 5.4 us with 2 H, 5.9 with 4 H, 6.5 with 8 H, 1024 tokens 11.8, 10.5, 10.7,
+  // 8192 tokens 69, 65, 67)
+  int slice = 4 * H;
+  if ((int64_t)a.tokens * ((all + slice - 1) / slice) < 1536) slice = 2 * H;
+  const int slices = (all + slice - 1) / slice;
   const int64_t blocks = Q8 ? (int64_t)a.tokens / KV_BLOCK + 2 * (int64_t)a.c.rows : 0;
-  // heads of a block that one wave takes with the same sines: as many as leave
-  // enough waves
+  // ... and heads of a block (64 heads over 8 of 128: 512 tokens 8.6 us with 1
+  // head, 11.4 with 4, 15.6 with 8, 8192 tokens 68, 63, 63)
   int group = 1;
-  while (group < 8 && group < kv && blocks * 2 * kv / (2 * group) >= 4096) group *= 2;
+  while (group < 8 && group < kv && blocks * 2 * kv / (2 * group) >= 1024) group *= 2;
   const int64_t waves = (int64_t)a.tokens * slices + blocks * 2 * ((kv + group - 1) / group);
   hipLaunchKernelGGL((kv_append_kernel<E, D, TURN, Q8>), dim3((unsigned)((waves + WAVES - 1) / WAVES)), dim3(64 * WAVES), 0, s,
                      a, slices, slice, group);
