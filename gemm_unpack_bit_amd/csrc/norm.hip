@@ -15,7 +15,7 @@
 namespace qg {
 namespace {
 
-constexpr int HELD = 4;
+constexpr int HELD = 2;
 
 __device__ __forceinline__ float wave_sum(float v) { return quarter_sum(group_sum<16>(v)); }
 __device__ __forceinline__ float wave_max(float v) {
@@ -27,6 +27,10 @@ __device__ __forceinline__ float wave_max(float v) {
 }
 
 __device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7F800000u) != 0x7F800000u; }
+
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0C0C0400u), __builtin_amdgcn_perm(b, a, 0x0C0C0400u), 0x05040100u);
+}
 
 // PW: elements of a piece, 8 (one 16-byte access) or 1 (any alignment).
 // A workgroup has 16 waves or fewer: one row (WAVES > 1) or four (WAVES = 1).
@@ -105,15 +109,12 @@ __global__ void __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) rms_norm_kernel
 
     float step = 0.f;
     if constexpr (Q8) {
-      // (NaN, from infinities too, is counted apart: maxima pass over it)
-      float most = 0.f, bad = 0.f;
+      // (as whole numbers, magnitudes order alike, and infinities and NaN stand
+      // above them all)
+      uint32_t top = 0;
       auto look = [&](const float (&v)[PW], const float (&wt)[PW]) {
 #pragma unroll
-        for (int e = 0; e < PW; ++e) {
-          const float y = v[e] * inv * wt[e];
-          most = fmaxf(most, fabsf(y));
-          bad = finite(y) ? bad : 1.f;
-        }
+        for (int e = 0; e < PW; ++e) top = max(top, __float_as_uint(v[e] * inv * wt[e]) & 0x7FFFFFFFu);
       };
 #pragma unroll
       for (int i = 0; i < HELD; ++i)
@@ -124,28 +125,40 @@ __global__ void __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) rms_norm_kernel
         load(a.weight, p, wt);
         look(y, wt);
       }
-      most = wave_max(bad != 0.f ? __builtin_inff() : most);
+      float most = wave_max(__uint_as_float(min(top, 0x7F800000u)));
       most = join(most, 1, [](float p, float q) { return fmaxf(p, q); });
       step = most / 127.0f;  // correctly rounded
       if (!finite(most)) step = __builtin_nanf("");
       if (tid == 0) a.step[row] = step;
     }
+    // 1 / step, where the quotients below can be had from it
+    const float by = Q8 && step > 0x1p-100f && step < 0x1p100f ? 1.f / step : 0.f;
 
     auto finish = [&](int piece, float (&v)[PW], const float (&wt)[PW]) {
       if (a.sum) store(a.sum + row * a.sum_row, piece, v);
 #pragma unroll
       for (int e = 0; e < PW; ++e) v[e] = v[e] * inv * wt[e];
       if constexpr (Q8) {
+        // y / step correctly rounded, so codes are those of the definition.  With the
+        // correctly rounded reciprocal, the product and one correction by the
+        // remainder give that (where the remainder would be subnormal, the code is
+        // 0 with any rounding); adding 1.5 * 2^23 rounds to a whole number, which
+        // then stands in the low byte.
         uint32_t c[PW];
+        if (by != 0.f) {
 #pragma unroll
-        for (int e = 0; e < PW; ++e) {
-          // correctly rounded division, so codes are those of the definition
-          const float q = step > 0.f ? fminf(fmaxf(rintf(v[e] / step), -127.f), 127.f) : 0.f;
-          c[e] = (uint32_t)(int)q & 0xFFu;
+          for (int e = 0; e < PW; ++e) {
+            const float q = v[e] * by, exact = fmaf(fmaf(-q, step, v[e]), by, q);
+            c[e] = __float_as_uint(fminf(fmaxf(exact, -127.f), 127.f) + 12582912.f);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < PW; ++e)
+            c[e] = step > 0.f ? (uint32_t)(int)rintf(fminf(fmaxf(v[e] / step, -127.f), 127.f)) : 0u;
         }
         int8_t* to = a.y8 + row * a.dim + (int64_t)piece * PW;
         if constexpr (PW == 8)
-          *reinterpret_cast<u2*>(to) = u2{c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24};
+          *reinterpret_cast<u2*>(to) = u2{low_bytes(c[0], c[1], c[2], c[3]), low_bytes(c[4], c[5], c[6], c[7])};
         else
           *to = (int8_t)c[0];
       } else {
@@ -178,8 +191,13 @@ hipError_t launch(const NormArgs& a, hipStream_t s) {
 template <typename E, int PW, bool Q8>
 hipError_t launch_w(const NormArgs& a, hipStream_t s) {
   const int pieces = (a.dim + PW - 1) / PW;
-  if (pieces <= 64 * HELD && a.rows > 64) return launch<E, PW, 1, Q8>(a, s);
-  if (pieces <= 256 * HELD && (a.rows > 64 || pieces <= 256)) return launch<E, PW, 4, Q8>(a, s);
+  // Measured (fp16, with a residual, 16-bit results): 4096 rows of 1024 8.8 us with
+  // one wave and 10.8 with 4, 128 rows 3.8 and 3.4; of 2048 13.8 with 4 and 16.8
+  // with 8; of 4096 30 with either, one row 3.7 and 3.5; of 8192 56 with 8, 63 with
+  // 4, 58 with 16; of 16384 114 with 8 and 106 with 16.
+  if (pieces <= 128 && a.rows > 512) return launch<E, PW, 1, Q8>(a, s);
+  if (pieces <= 256) return launch<E, PW, 4, Q8>(a, s);
+  if (pieces <= 1024) return launch<E, PW, 8, Q8>(a, s);
   return launch<E, PW, 16, Q8>(a, s);
 }
 
