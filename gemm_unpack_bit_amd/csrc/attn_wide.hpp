@@ -174,15 +174,22 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
     codes_t c[CL];
     uint32_t e;
   };
-  auto fetch = [&](const uint16_t* pool, const uint8_t* exps, int u, Raw& raw) {
-    const int64_t tok = tok_of(u);
-    const int last = (u + 1) * KB <= r.keys ? T::RW - 1 : r.keys - 1 - min(u * KB + T::RW * wave, top);
-    const uint8_t* p = reinterpret_cast<const uint8_t*>(pool) + tok * a.k_token + (int64_t)g.h * a.k_head;
+  typedef __attribute__((address_space(1))) const uint8_t* global8;
+  // (off: the lane's place in the wave's rows)
+  auto fetch_at = [&](const uint16_t* pool, const uint8_t* exps, int64_t tok, uint32_t off, int last, Raw& raw) {
+    global8 p = (global8)reinterpret_cast<const uint8_t*>(pool) + tok * a.k_token + (int64_t)g.h * a.k_head;
 #pragma unroll
-    for (int i = 0; i < CL; ++i)
-      raw.c[i] = *reinterpret_cast<const codes_t*>(p + (uint32_t)min(RC * i + lane / (D / CB), last) * (uint32_t)a.k_token +
-                                                   CB * (lane % (D / CB)));
-    raw.e = exps[tok / KV_BLOCK * a.heads_kv + g.h];
+    for (int i = 0; i < CL; ++i) {
+      const uint32_t at = last < T::RW - 1 ? (uint32_t)min(RC * i + lane / (D / CB), last) * (uint32_t)a.k_token + CB * (lane % (D / CB))
+                                           : off + (uint32_t)(RC * i) * (uint32_t)a.k_token;
+      raw.c[i] = *(__attribute__((address_space(1))) const codes_t*)(p + at);
+    }
+    raw.e = ((global8)exps)[tok / KV_BLOCK * a.heads_kv + g.h];
+  };
+  const uint32_t code_off = (uint32_t)(lane / (D / CB)) * (uint32_t)a.k_token + CB * (lane % (D / CB));
+  auto fetch = [&](const uint16_t* pool, const uint8_t* exps, int u, Raw& raw) {
+    fetch_at(pool, exps, tok_of(u), code_off,
+             (u + 1) * KB <= r.keys ? T::RW - 1 : r.keys - 1 - min(u * KB + T::RW * wave, top), raw);
   };
   auto decode = [&](const Raw& raw, Buffers<D>& buf) {
     const float by = exp_scale(raw.e);
@@ -438,12 +445,18 @@ __device__ __forceinline__ void run_segment(const Segment& g, int64_t slots, Buf
       // steps whose tile every row sees in full, and that have three behind them
       const int uf = u0 + ((max(min(common / KB, u1 - 3), u0) - u0) & ~1);
       int u = u0;
+      // (the tokens of the next loads are looked up a step ahead)
+      int64_t tok2 = tok_of(u + 2), tok3 = tok_of(u + 3);
+      uint32_t off = code_off;
       auto fast = [&](Buffers<D>& k_now, Buffers<D>& k_next, Buffers<D>& v_now, Buffers<D>& v_next) {
         lds_barrier();
         decode(kr, k_now);
         decode(vr, v_next);
-        fetch(a.k, a.k_exps, u + 3, kr);
-        fetch(a.v, a.v_exps, u + 2, vr);
+        asm volatile("" : "+v"(off));  // (kept as a 32-bit offset of a scalar base)
+        fetch_at(a.k, a.k_exps, tok3, off, T::RW - 1, kr);
+        fetch_at(a.v, a.v_exps, tok2, off, T::RW - 1, vr);
+        tok2 = tok3;
+        tok3 = tok_of(u + 4);
         ++u;
         weigh(std::false_type{});
         gather(v_now);
