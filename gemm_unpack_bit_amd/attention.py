@@ -232,6 +232,10 @@ def kv_write(cache, layer, k, v, cu, pos):
                                                 _ints(pos, "pos", rows, dev), _raw_stream(dev)))
 
 
+_APPEND = [(name, getattr(_lib, name)) for name in ("qgemv_kv_append", "qgemv_kv8_append")]
+_READ = [(name, getattr(_lib, name)) for name in ("qgemv_kv_read", "qgemv_kv8_read")]
+
+
 def kv_append(cache, layer, k, v, cu, pos, q=None, freqs=None, at=None, interleaved=False, out=None):
     """kv_write with the position rotation: keys (and queries) turn by the angles
     position * freqs[i], fp32 [rot / 2], in pairs of elements i and i + rot / 2,
@@ -244,17 +248,19 @@ def kv_append(cache, layer, k, v, cu, pos, q=None, freqs=None, at=None, interlea
     rows, dev = cache.rows, cache._dev
     dtype = cache._type(k, "k")
     hk, hv = _heads(k, "k", dtype, dev), _heads(v, "v", dtype, dev)
-    tokens, heads_kv, dim = k.shape
-    if v.shape != k.shape or heads_kv != cache.heads_kv or dim != cache.head_dim:
+    shape = k.shape
+    tokens, heads_kv, dim = shape
+    if v.shape != shape or heads_kv != cache.heads_kv or dim != cache.head_dim:
         raise ValueError("k and v must be [tokens, heads_kv, head_dim] of the cache")
     heads, hq, ho = 0, None, None
     if q is not None:
-        hq, heads = _heads(q, "q", dtype, dev), q.shape[1]
-        if q.shape[0] != tokens or q.shape[2] != dim:
+        hq, shape = _heads(q, "q", dtype, dev), q.shape
+        if shape[0] != tokens or shape[2] != dim:
             raise ValueError("q must be [tokens, heads, head_dim] with k's tokens and head_dim")
+        heads = shape[1]
         if out is None:
-            out = torch.empty(q.shape, dtype=dtype, device=q.device)
-        elif out.shape != q.shape:
+            out = torch.empty(shape, dtype=dtype, device=q.device)
+        elif out.shape != shape:
             raise ValueError("out must have q's shape")
         ho = _heads(out, "out", dtype, dev)
     elif out is not None:
@@ -270,8 +276,8 @@ def kv_append(cache, layer, k, v, cu, pos, q=None, freqs=None, at=None, interlea
             pa = _ints(at, "at", tokens, dev)
     elif at is not None:
         raise ValueError("at goes with freqs")
-    name = "qgemv_kv8_append" if cache._eight else "qgemv_kv_append"
-    _done(name, getattr(_lib, name)(
+    name, call = _APPEND[cache._eight]
+    _done(name, call(
         _DTYPES[dtype], cache._ref, layer, tokens, heads, hq, hk, hv, _ints(cu, "cu", rows + 1, dev),
         _ints(pos, "pos", rows, dev), pf, rot, int(interleaved), pa, ho, _raw_stream(dev)))
     return out
@@ -294,13 +300,13 @@ def kv_read(cache, layer, cu, start, tokens=None, dtype=None, out=None):
     k, v = out
     dtype = cache._type(k, "k")
     hk, hv = _heads(k, "k", dtype, dev), _heads(v, "v", dtype, dev)
-    if v.shape != k.shape or k.shape[1:] != (cache.heads_kv, cache.head_dim) or (tokens is not None and k.shape[0] != tokens):
+    shape = k.shape
+    if (v.shape != shape or shape[1] != cache.heads_kv or shape[2] != cache.head_dim
+            or (tokens is not None and shape[0] != tokens)):
         raise ValueError("out must be two arrays [tokens, heads_kv, head_dim] of the cache")
     pc, ps = _ints(cu, "cu", rows + 1, dev), _ints(start, "start", rows, dev)
-    if cache._eight:
-        _done("qgemv_kv8_read", _lib.qgemv_kv8_read(_DTYPES[dtype], cache._ref, layer, k.shape[0], pc, ps, hk, hv, _raw_stream(dev)))
-    else:
-        _done("qgemv_kv_read", _lib.qgemv_kv_read(cache._ref, layer, k.shape[0], pc, ps, hk, hv, _raw_stream(dev)))
+    name, call = _READ[cache._eight]
+    _done(name, call(*((_DTYPES[dtype],) if cache._eight else ()), cache._ref, layer, shape[0], pc, ps, hk, hv, _raw_stream(dev)))
     return k, v
 
 

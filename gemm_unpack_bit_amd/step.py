@@ -25,9 +25,12 @@ def _rows(t, name, shape, dtype, dev):
         raise TypeError(f"{name} must be a CUDA tensor on the same device as the others")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape or (t.stride(1) != 1 and shape[1] > 1):
-        raise ValueError(f"{name} must be {list(shape)} with a contiguous last dimension")
-    return _pack(t.data_ptr() or 16, t.stride(0))  # (an empty tensor has no data)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    row, last = t.stride()
+    if last != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return _pack(t.data_ptr() or 16, row)  # (an empty tensor has no data)
 
 
 def _flat(t, name, n, dtype, dev):
@@ -41,19 +44,19 @@ def _flat(t, name, n, dtype, dev):
 
 
 def _norm_inputs(x, weight, residual, residual_out):
-    dtype, dev = _kind(x, "x"), x.get_device()
-    if x.dim() != 2:
+    dtype, dev, shape = _kind(x, "x"), x.get_device(), x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [rows, dim]")
-    hx = _rows(x, "x", x.shape, dtype, dev)
-    pw = _flat(weight, "weight", x.shape[1], dtype, dev)
+    hx = _rows(x, "x", shape, dtype, dev)
+    pw = _flat(weight, "weight", shape[1], dtype, dev)
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out goes with residual")
-        return dtype, dev, hx, pw, None, None, None
+        return dtype, dev, shape, hx, pw, None, None, None
     if residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=dtype, device=x.device)
-    return (dtype, dev, hx, pw, _rows(residual, "residual", x.shape, dtype, dev),
-            _rows(residual_out, "residual_out", x.shape, dtype, dev), residual_out)
+        residual_out = torch.empty(shape, dtype=dtype, device=x.device)
+    return (dtype, dev, shape, hx, pw, _rows(residual, "residual", shape, dtype, dev),
+            _rows(residual_out, "residual_out", shape, dtype, dev), residual_out)
 
 
 def rms_norm(x, weight, eps=1e-6, residual=None, out=None, residual_out=None):
@@ -62,23 +65,22 @@ def rms_norm(x, weight, eps=1e-6, residual=None, out=None, residual_out=None):
     x, residual [rows, dim], fp16 or bf16, any row strides; weight [dim].
     Returns y, or with a residual (y, h): h rounded once, in ``residual_out``
     (which may be ``residual``, as ``out`` may be ``x``)."""
-    dtype, dev, hx, pw, hr, hs, total = _norm_inputs(x, weight, residual, residual_out)
+    dtype, dev, shape, hx, pw, hr, hs, total = _norm_inputs(x, weight, residual, residual_out)
     if out is None:
-        out = torch.empty(x.shape, dtype=dtype, device=x.device)
-    rows, dim = x.shape
-    _done("qgemv_rms_norm", _lib.qgemv_rms_norm(_DTYPES[dtype], rows, dim, eps, hx, hr, pw, hs,
-                                                _rows(out, "out", x.shape, dtype, dev), _raw_stream(dev)))
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+    _done("qgemv_rms_norm", _lib.qgemv_rms_norm(_DTYPES[dtype], *shape, eps, hx, hr, pw, hs,
+                                                _rows(out, "out", shape, dtype, dev), _raw_stream(dev)))
     return out if residual is None else (out, total)
 
 
 def rms_norm_q8(x, weight, eps=1e-6, residual=None, out=None, scales=None, residual_out=None):
     """rms_norm with y in 8 bits for w4a8_rows: int8 codes rint(y / scale) [rows, dim] and fp32 scales [rows], a
     row's max |y| / 127.  Returns (codes, scales), or with a residual (codes, scales, h)."""
-    dtype, dev, hx, pw, hr, hs, total = _norm_inputs(x, weight, residual, residual_out)
-    rows, dim = x.shape
+    dtype, dev, shape, hx, pw, hr, hs, total = _norm_inputs(x, weight, residual, residual_out)
+    rows, dim = shape
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-    elif out.shape != x.shape:
+        out = torch.empty(shape, dtype=torch.int8, device=x.device)
+    elif out.shape != shape:
         raise ValueError("out must have x's shape")
     if scales is None:
         scales = torch.empty(rows, dtype=torch.float32, device=x.device)
@@ -92,14 +94,14 @@ def w4a8_rows(x8, row_scales, wq, scales, zeros, out=None):
     """The product of w4a8 for activations in 8 bits (rms_norm_q8's): y = (x8 * row_scales) . dequant(Wq)^T, fp16.
 
     x8 int8 [M, K], M up to 16; row_scales fp32 [M]; wq, scales and zeros as w4a16."""
-    dev = x8.get_device()
-    if x8.dim() != 2:
+    dev, shape = x8.get_device(), x8.shape
+    if len(shape) != 2:
         raise ValueError("x8 must be [M, K]")
-    M, K = x8.shape
+    M, K = shape
     N = scales.shape[0]
     px, pr = _flat(x8, "x8", M * K, torch.int8, dev), _flat(row_scales, "row_scales", M, torch.float32, dev)
     groups = K // _q.GROUP
-    need = _q.packed_words(4, N, K)  # 0 for shapes the library rejects itself
+    need = _lib.qgemv_packed_words(4, _q.LAYOUT_DEVICE, N, K)  # 0 for shapes the library rejects itself
     pq = _flat(wq, "wq", need or wq.numel(), torch.int32, dev)
     ps = _flat(scales, "scales", N * groups, torch.float16, dev)
     pz = _flat(zeros, "zeros", N * -(-groups // 8), torch.int32, dev)
