@@ -5,14 +5,17 @@
 The weights are random 4-bit codes, so what the tokens say means nothing; the
 calls and their order are those of a serving loop:
 
-- prompts      kv_reserve once, then per layer kv_write and attn_prompt;
-- a decode step  the same with attn_tree, one token per row;
+- prompts      kv_reserve once, then per layer rms_norm, kv_append (rotation and
+               the cache in one), kv_read and attn_prompt;
+- a decode step  the same with attn_tree over the cache, one token per row, and
+               sample (here the largest logit) at its end;
 - scouting     kv_fork gives every row a twin that decodes a few tokens ahead,
                and a second kv_fork drops the twins (their pages go back);
 - verification attn_tree over each row's drafted tree (the scouted tokens and
                wrong guesses beside them), every node seeing its ancestors;
 - acceptance   kv_compact keeps the nodes that the layers agree with.
 
+The cache is of 16 bits, or with ``main(cache_type=torch.float8_e4m3fn)`` of 8.
 At the end the next token's logits over the cache are compared with those of
 one prompt that holds all the kept tokens.
 """
@@ -46,19 +49,6 @@ class Linear:
         return f(x.contiguous(), self.wq, self.scales, self.zeros, BITS)
 
 
-def norm(x):
-    f = x.float()
-    return (f * torch.rsqrt(f.square().mean(-1, keepdim=True) + 1e-6)).half()
-
-
-def rotate(x, at):
-    """Rotary positions: x [tokens, heads, DIM], at [tokens]."""
-    half = DIM // 2
-    angle = at[:, None, None].float() * 10000.0 ** (-torch.arange(half, device=x.device) / half)
-    a, b = x[..., :half].float(), x[..., half:].float()
-    return torch.cat([a * angle.cos() - b * angle.sin(), a * angle.sin() + b * angle.cos()], -1).half()
-
-
 def ints(values):
     return torch.tensor(values, dtype=torch.int32, device="cuda")
 
@@ -78,25 +68,38 @@ class Model:
         self.layers = [dict(qkv=Linear(gen, (HEADS + 2 * HEADS_KV) * DIM, HIDDEN), out=Linear(gen, HIDDEN, HEADS * DIM),
                             up=Linear(gen, 2 * FFN, HIDDEN), down=Linear(gen, HIDDEN, FFN)) for _ in range(LAYERS)]
         self.head = Linear(gen, VOCAB, HIDDEN)
+        self.weight = torch.ones(HIDDEN, device="cuda").half()  # of every norm
+        self.freqs = 10000.0 ** (-torch.arange(DIM // 2, device="cuda") / (DIM // 2))
 
     def run(self, tokens, at, cache, cu, mask=None, prompt=False):
-        """Logits of ``tokens`` (packed rows, ``cu``) at the positions ``at``; the rows of the cache grow by them.
+        """Logits of ``tokens`` (packed rows, ``cu``) at the positions ``at`` (int32); the rows of the cache grow by them.
         Returns the logits and where each row's tokens begin in its row."""
-        x = self.embed[tokens]
+        x, more = self.embed[tokens], None  # the sum so far, and what the last product adds to it
         pos = q.kv_reserve(cache, cu)
+
+        def norm():
+            if more is None:
+                return q.rms_norm(x, self.weight), x
+            return q.rms_norm(more, self.weight, residual=x, residual_out=x)
+
         for n, layer in enumerate(self.layers):
-            qkv = layer["qkv"](norm(x)).view(-1, HEADS + 2 * HEADS_KV, DIM)
-            qh, kh = rotate(qkv[:, :HEADS], at), rotate(qkv[:, HEADS:HEADS + HEADS_KV], at)
-            vh = qkv[:, HEADS + HEADS_KV:]  # a view: its token stride is the product's row
-            q.kv_write(cache, n, kh, vh, cu, pos)
-            o = q.attn_prompt(qh, kh, vh, cu) if prompt else q.attn_tree(qh, cache, n, cu, pos, mask)
-            x = x + layer["out"](o.view(-1, HEADS * DIM))
-            gate, up = layer["up"](norm(x)).chunk(2, -1)
-            x = x + layer["down"](torch.nn.functional.silu(gate) * up)
-        return self.head(norm(x)).float(), pos
+            y, x = norm()
+            qkv = layer["qkv"](y).view(-1, HEADS + 2 * HEADS_KV, DIM)
+            qh, kh, vh = qkv.split([HEADS, HEADS_KV, HEADS_KV], 1)  # views: their token stride is the product's row
+            q.kv_append(cache, n, kh, vh, cu, pos, q=qh, freqs=self.freqs, at=at, out=qh)
+            if prompt:
+                kh, vh = q.kv_read(cache, n, cu, pos, tokens=len(tokens))
+                o = q.attn_prompt(qh, kh, vh, cu)
+            else:
+                o = q.attn_tree(qh, cache, n, cu, pos, mask)
+            more = layer["out"](o.view(-1, HEADS * DIM))
+            y, x = norm()
+            gate, up = layer["up"](y).chunk(2, -1)
+            more = layer["down"](torch.nn.functional.silu(gate) * up)
+        return self.head(norm()[0]), pos
 
     def prompts(self, texts, cache):
-        at = torch.cat([torch.arange(len(t), device="cuda") for t in texts])
+        at = torch.cat([torch.arange(len(t), dtype=torch.int32, device="cuda") for t in texts])
         cu = offsets([len(t) for t in texts])
         logits, _ = self.run(torch.cat(texts), at, cache, cu, prompt=True)
         return logits[cu[1:].long() - 1]
@@ -105,8 +108,14 @@ class Model:
         return self.run(tokens, cache.lens.clone(), cache, offsets([1] * cache.rows))[0]
 
 
-def new_cache(rows):
-    return q.KvCache.empty(LAYERS, 64, PAGE, HEADS_KV, DIM, rows, 24)
+def new_cache(rows, kind):
+    return q.KvCache.empty(LAYERS, 64, PAGE, HEADS_KV, DIM, rows, 24, dtype=kind)
+
+
+def largest(logits):
+    """The tokens that sampling at a temperature of 0 takes."""
+    none = torch.zeros(len(logits), device="cuda")
+    return q.sample(logits, none, temperature=none).long()
 
 
 def tree_of(chain, gen):
@@ -121,12 +130,12 @@ def tree_of(chain, gen):
     return tokens, parents
 
 
-def main(seed=1, lengths=(37, 5, 120), ahead=4, rounds=2):
+def main(seed=1, lengths=(37, 5, 120), ahead=4, rounds=2, cache_type=torch.float16):
     model, gen = Model(seed), torch.Generator().manual_seed(seed)
     texts = [torch.randint(0, VOCAB, (n,), generator=gen).cuda() for n in lengths]
     rows = len(texts)
-    cache = new_cache(rows)
-    pending = model.prompts(texts, cache).argmax(-1)  # of every row: chosen, not in the cache yet
+    cache = new_cache(rows, cache_type)
+    pending = largest(model.prompts(texts, cache))  # of every row: chosen, not in the cache yet
     accepted = []
     for _ in range(rounds):
         # scout: twins decode `ahead` tokens, then their rows end
@@ -135,7 +144,7 @@ def main(seed=1, lengths=(37, 5, 120), ahead=4, rounds=2):
         idle = ints([0] * (2 * rows))
         for _ in range(ahead):
             logits = model.step(t, twins)
-            t = logits.argmax(-1).view(rows, 2)[:, :1].repeat(1, 2).flatten()
+            t = largest(logits).view(rows, 2)[:, :1].repeat(1, 2).flatten()
             for b in range(rows):
                 chains[b].append(int(t[2 * b]))
         # the twin at 2 b + 1 goes back to where the row was (it stepped along), the scout at 2 b ends
@@ -153,9 +162,9 @@ def main(seed=1, lengths=(37, 5, 120), ahead=4, rounds=2):
             at += [lens[b] + d for d in depth]
             mask += [[s] for s in seen]
         cu = offsets([len(tok) for tok, _ in trees])
-        logits, pos = model.run(torch.tensor(tokens, device="cuda"), torch.tensor(at, device="cuda"), cache, cu,
+        logits, pos = model.run(torch.tensor(tokens, device="cuda"), ints(at), cache, cu,
                                 torch.tensor(mask, device="cuda"))
-        best, first = logits.argmax(-1).tolist(), cu.tolist()
+        best, first = largest(logits).tolist(), cu.tolist()
         # accept from each root on, as long as a child is what the layers would say next
         keep = []
         for b, (tok, par) in enumerate(trees):
@@ -170,16 +179,17 @@ def main(seed=1, lengths=(37, 5, 120), ahead=4, rounds=2):
         most = max(map(len, keep))
         q.kv_compact(cache, pos, ints([p + [0] * (most - len(p)) for p in keep]), ints([len(p) for p in keep]))
         accepted.append([len(p) for p in keep])
-    over_cache = model.step(pending, cache)
+    over_cache = model.step(pending, cache).float()
     texts = [torch.cat([t, p[None]]) for t, p in zip(texts, pending)]
-    at_once = model.prompts(texts, new_cache(rows))
+    at_once = model.prompts(texts, new_cache(rows, cache_type)).float()
     return dict(accepted=accepted, lens=cache.lens.tolist(), texts=[len(t) for t in texts],
                 status=int(cache.status), pages=int((cache.refs > 0).sum()), refs=int(cache.refs.sum()),
                 difference=float((over_cache - at_once).norm() / at_once.norm()))
 
 
 if __name__ == "__main__":
-    r = main()
-    print("tokens accepted per round and row:", r["accepted"])
-    print("tokens in the rows:", r["lens"], "in", r["pages"], "pages")
-    print(f"logits over the cache against one prompt: relative difference {r['difference']:.2e}")
+    for kind in (torch.float16, torch.float8_e4m3fn):
+        r = main(cache_type=kind)
+        print(f"cache of {kind}: tokens accepted per round and row:", r["accepted"])
+        print("tokens in the rows:", r["lens"], "in", r["pages"], "pages")
+        print(f"logits over the cache against one prompt: relative difference {r['difference']:.2e}")
