@@ -277,9 +277,10 @@ __global__ void __launch_bounds__(64 * WAVES) kv_append_kernel(KvAppendArgs a, i
     }
     wave -= blocks * parts;
   }
+  if (wave >= (int64_t)a.tokens * slices) return;  // (8 bits without queries: no slices)
   const int t = (int)(wave / slices), h0 = (int)(wave % slices) * slice;
   const int all = Q8 ? a.heads : a.heads + 2 * a.c.heads_kv;
-  if (wave < (int64_t)a.tokens * slices) token_heads<E, D, TURN>(a, t, h0, min(slice, all - h0));
+  token_heads<E, D, TURN>(a, t, h0, min(slice, all - h0));
 }
 
 // One wave per token: units of its keys, then of its values.
