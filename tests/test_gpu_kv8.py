@@ -174,6 +174,62 @@ def test_long_rows_are_split_and_agree_with_16_bits(dtype):
         c.check(got, "tree8 long", only={sum(new[:2]), sum(new) - 1})
 
 
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("heads,kv,dim", [(8, 2, 64), (40, 2, 128)])
+def test_many_long_rows_on_the_same_pages(heads, kv, dim, dtype):
+    """So many keys that a wave takes more than 32 steps of one row in a go; every row reads the same pages."""
+    rows, n = 300, 9001
+    say("tree8 many long", heads, kv, dim, dtype)
+    c = Case([n], [1], heads, kv, dim, 32, dtype, seed=dim)
+    c.lens, c.new, c.tables = [n] * rows, [1] * rows, c.tables * rows
+    c.cache = q.KvCache(c.cache.k, c.cache.v, ints(c.tables), ints([n + 1] * rows), c.cache.refs, k_exps=c.cache.k_exps,
+                        v_exps=c.cache.v_exps)
+    c.q = c.q.repeat(rows, 1, 1)
+    c.q[1::2] *= -0.5
+    c.cu, c.pos = cu_of(c.new), ints(c.lens)
+    got = c.run()
+    c.check(got, "tree8 many long", only={0, 1, 2, 151, rows - 1})
+    # the others: the same queries, with other borders between the parts
+    vmax, u = float(max(abs(x).max() for x in c.values())), 2.0 ** -11 if dtype == "float16" else 2.0 ** -8
+    for i in (0, 1):
+        assert bool(((got[i::2].double() - got[i].double()).abs() <= (4 * u + n * 2.0 ** -23) * vmax).all())
+
+
+def test_offsets_past_32_bits():
+    """The same calls on the last pages of the last layer of 6 GiB pools as on a small cache: the same bits."""
+    t = torch()
+    say("kv8 offsets past 32 bits")
+    kv, heads, dim, page, rows, layers = 8, 32, 128, 256, 3, 3
+    lens, more = [300, 1, 511], [1, 40, 2]
+    g = t.Generator(device="cuda").manual_seed(3)
+    first = [t.randn((sum(lens), kv, dim), generator=g, device="cuda").half() for _ in range(2)]
+    new = [t.randn((sum(more), kv, dim), generator=g, device="cuda").half() for _ in range(2)]
+    x = t.randn((sum(more), heads, dim), generator=g, device="cuda").half()
+    results = []
+    for pages in (16, 8192):
+        shape = (layers, pages, page, kv, dim)
+        k, v = (t.empty(shape, dtype=t.float8_e4m3fn, device="cuda") for _ in range(2))
+        ke, ve = (t.empty((layers, pages, page // 16, kv), dtype=t.uint8, device="cuda") for _ in range(2))
+        refs = t.ones(pages, dtype=t.int32, device="cuda")
+        refs[-16:] = 0  # (only the last ones are free)
+        cache = q.KvCache(k, v, t.full((rows, 4), -1, dtype=t.int32, device="cuda"), ints([0] * rows), refs, k_exps=ke, v_exps=ve)
+        q.kv_append(cache, 2, *first, cu_of(lens), q.kv_reserve(cache, cu_of(lens)))
+        pos = q.kv_reserve(cache, cu_of(more))
+        q.kv_append(cache, 2, *new, cu_of(more), pos)
+        assert int(cache.status) == 0 and int(cache.tables.max()) < pages and pos.tolist() == lens
+        out = [q.attn_tree(x, cache, 2, cu_of(more), pos), q.attn_tree(x[:3], cache, 2, cu_of([1, 1, 1]), pos)]
+        out += q.kv_read(cache, 2, cu_of(lens), ints([0] * rows), tokens=sum(lens))
+        twin = q.kv_fork(cache, ints([2, 2, 1]))
+        q.kv_compact(twin, pos[[2, 2, 1]], ints([[1, 0], [1, 0], [0, 30]]), ints([1, 1, 2]))
+        # (token 511 of the first two lies in a full page, which both have, so they are left alone)
+        assert int(cache.status) == q.KV_SHARED and twin.lens.tolist() == [513, 513, 3]
+        out += q.kv_read(twin, 2, cu_of([513, 513, 3]), ints([0] * rows), tokens=1029)
+        results.append(out)
+        del k, v, cache, twin
+    for a, b in zip(*results):
+        assert t.equal(a, b)
+
+
 def test_rows_at_minus_one_scale_and_strides():
     t = torch()
     say("tree8: rows at -1, scale, strides")

@@ -175,6 +175,37 @@ def test_strided_rows_other_streams_and_graphs():
         assert t.equal(out, want)
 
 
+def test_graphs_that_share_a_workspace():
+    """Two captured calls of different shapes and settings, replayed in turn with eager calls between, all in one
+    workspace."""
+    t = torch()
+    g = t.Generator(device="cuda").manual_seed(5)
+    ws = t.full((q.sample_workspace_bytes(9, 40000),), 0xA5, dtype=t.uint8, device="cuda")
+    calls = []
+    for rows, vocab, dtype in ((9, 40000, t.float32), (4, 1003, t.float16)):
+        say("sample, shared workspace", rows, vocab)
+        x = (t.randn((rows, vocab), generator=g, device="cuda") * 3).to(dtype)
+        more = dict(temperature=t.rand(rows, generator=g, device="cuda") + 0.5,
+                    top_k=t.randint(0, 60, (rows,), generator=g, device="cuda", dtype=t.int32),
+                    top_p=t.rand(rows, generator=g, device="cuda") * 0.5 + 0.5, ws=ws)
+        calls.append((x, t.rand(rows, generator=g, device="cuda"), more, t.empty(rows, dtype=t.int32, device="cuda")))
+    want = [q.sample(x, u, **more) for x, u, more, _ in calls]
+    graphs = []
+    for x, u, more, out in calls:
+        q.sample(x, u, out=out, **more)
+        t.cuda.synchronize()
+        graphs.append(t.cuda.CUDAGraph())
+        with t.cuda.graph(graphs[-1]):
+            q.sample(x, u, out=out, **more)
+    for turn in range(3):
+        for i in (0, 1, 1, 0):
+            calls[i][3].fill_(-7)
+            graphs[i].replay()
+            x, u, more, out = calls[1 - i]
+            assert t.equal(q.sample(x, u, **more), want[1 - i])
+            assert t.equal(calls[i][3], want[i])
+
+
 def test_the_same_call_gives_the_same_tokens():
     t = torch()
     x = logits(64, 50000, "float32", 31)
