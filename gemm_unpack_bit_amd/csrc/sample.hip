@@ -41,6 +41,7 @@ constexpr int CAP = 2048;   // elements listed
 constexpr int T = 256;      // threads of every workgroup
 constexpr int WAVES = T / 64, PIECE = 8, STEP = PIECE * T, MOST_SLICES = BINS / WAVES;
 constexpr int OWN = BINS / T;  // bins (or chunks) of a thread
+constexpr float LOWEST = -3.402823466e38f;
 
 // what a slice of a row leaves: its largest logit's key and place (the first
 // one), its smallest finite logit
@@ -69,7 +70,7 @@ struct Cut {
 
 struct Work {
   unsigned long long *bins, *list, *sums;  // [rows][BINS], [rows][CAP], [rows][slices * WAVES]
-  int* listed;                             // [rows]
+  int *listed, *done;                      // [rows]
   Part* parts;                             // [rows][slices]
   __device__ __forceinline__ Work(void* ws, int64_t rows, int slices) {
     char* p = reinterpret_cast<char*>(ws);
@@ -77,11 +78,12 @@ struct Work {
     list = reinterpret_cast<unsigned long long*>(p), p += rows * CAP * 8;
     parts = reinterpret_cast<Part*>(p), p += rows * slices * 16;
     sums = reinterpret_cast<unsigned long long*>(p), p += rows * slices * (8 * WAVES);
-    listed = reinterpret_cast<int*>(p);
+    listed = reinterpret_cast<int*>(p), p += rows * 4;
+    done = reinterpret_cast<int*>(p);
   }
 };
 constexpr size_t work_bytes(int64_t rows, int slices) {
-  return (size_t)(rows * (BINS * 8 + CAP * 8 + 4) + rows * slices * (16 + 8 * WAVES));
+  return (size_t)(rows * (BINS * 8 + CAP * 8 + 8) + rows * slices * (16 + 8 * WAVES));
 }
 
 // Keys: floats in their order as unsigned numbers; NaN as -infinity, -0 as 0.
@@ -116,15 +118,17 @@ struct Raw {
       w[0] = *reinterpret_cast<const loose*>(static_cast<const uint16_t*>(row) + i);
     }
   }
+  template <bool CLEAN>
   __device__ __forceinline__ void get(float (&v)[PIECE]) const {
 #pragma unroll
     for (int e = 0; e < PIECE; ++e) {
       if constexpr (TYPE == 2) {
-        v[e] = clean(__uint_as_float(w[e / 4][e & 3]));
+        v[e] = __uint_as_float(w[e / 4][e & 3]);
       } else {
         const uint16_t h = (uint16_t)(w[0][e / 2] >> (16 * (e & 1)));
-        v[e] = clean(TYPE == 0 ? F16::value(h) : BF16::value(h));
+        v[e] = TYPE == 0 ? F16::value(h) : BF16::value(h);
       }
+      if constexpr (CLEAN) v[e] = clean(v[e]);
     }
   }
 };
@@ -135,36 +139,48 @@ __device__ __forceinline__ void load_piece(const void* row, int i, int end, floa
   if (i + PIECE <= end) {
     Raw<TYPE> r;
     r.load(row, i);
-    r.get(v);
+    r.template get<true>(v);
   } else {
 #pragma unroll
     for (int e = 0; e < PIECE; ++e) v[e] = i + e < end ? clean(logit_at<TYPE>(row, i + e)) : NEG_INF;
   }
 }
-// f(piece, its first index) for the pieces of [begin, end), THREADS at a time,
-// this one's first at begin + PIECE * thread; four are on their way at once.
-template <int TYPE, int THREADS, typename F>
-__device__ __forceinline__ void pieces(const void* row, int begin, int end, int thread, F&& f) {
-  constexpr int AT_ONCE = 4, ROUND = PIECE * THREADS;
-  int i = begin + PIECE * thread, at = begin;
-  for (; at + AT_ONCE * ROUND <= end; at += AT_ONCE * ROUND) {
-    Raw<TYPE> r[AT_ONCE];
+// The pieces of [begin, end), THREADS at a time, this one's first at begin + PIECE
+// * thread; four of a thread are on their way at once, the first ones from the
+// construction on.  Without CLEAN they may hold NaN and -0.
+template <int TYPE, int THREADS, bool CLEAN>
+struct Pieces {
+  static constexpr int AT_ONCE = 4, ROUND = PIECE * THREADS;
+  const void* row;
+  int i, end;
+  Raw<TYPE> raw[AT_ONCE];
+  __device__ __forceinline__ Pieces(const void* row, int begin, int end, int thread)
+      : row(row), i(begin + PIECE * thread), end(end) {
 #pragma unroll
-    for (int k = 0; k < AT_ONCE; ++k) r[k].load(row, i + k * ROUND);
+    for (int k = 0; k < AT_ONCE; ++k)
+      if (i + k * ROUND + PIECE <= end) raw[k].load(row, i + k * ROUND);
+  }
+  // f(piece, its first index)
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) {
+    while (i + PIECE <= end) {
 #pragma unroll
-    for (int k = 0; k < AT_ONCE; ++k) {
-      float v[PIECE];
-      r[k].get(v);
-      f(v, i + k * ROUND);
+      for (int k = 0; k < AT_ONCE; ++k) {
+        if (i + PIECE > end) continue;
+        float v[PIECE];
+        raw[k].template get<CLEAN>(v);
+        if (i + AT_ONCE * ROUND + PIECE <= end) raw[k].load(row, i + AT_ONCE * ROUND);
+        f(v, i);
+        i += ROUND;
+      }
     }
-    i += AT_ONCE * ROUND;
+    if (i < end) {  // (the last one)
+      float v[PIECE];
+      load_piece<TYPE>(row, i, end, v);
+      f(v, i);
+    }
   }
-  for (; i < end; i += ROUND) {
-    float v[PIECE];
-    load_piece<TYPE>(row, i, end, v);
-    f(v, i);
-  }
-}
+};
 
 // Weights.  x = (l - M) log2(e) / T <= 0 is split into its nearest whole number
 // n and f; 2^f is a polynomial through 2^f at the ten Chebyshev points of
@@ -317,13 +333,19 @@ struct Binning {
     const float used = ends ? all : width;
     by = used > 0.f ? (float)BINS / used : 0.f;
   }
-  // in bins from the largest logit on; past the last one (and NaN, of
-  // infinities) the last one
+  // in bins from the largest logit on; past the last one the last one
   __device__ __forceinline__ float at(float l) const {
-    const float d = (most - l) * by;
-    return l == most ? 0.f : d < (float)BINS - 0.001f ? d : (float)BINS - 0.001f;
+    // (NaN, of infinities: the middle one of three numbers is then the least of
+    // the other two)
+    return __builtin_amdgcn_fmed3f((most - l) * by, 0.f, (float)BINS - 0.001f);
   }
   __device__ __forceinline__ int operator()(float l) const { return (int)at(l); }
+  // finite, and at most as large as every logit in the bins up to `last` that is
+  // not -infinity (half a bin lower: more than the roundings)
+  __device__ __forceinline__ float under(int last) const {
+    const float l = most - ((float)last + 1.5f) / by;
+    return last < BINS - 1 && fabsf(l) < __builtin_inff() ? l : LOWEST;
+  }
   // one of 1024 parts of the bins [first, last], the same order, for l in them
   __device__ __forceinline__ int part(float l, int first, int last) const {
     const float d = (at(l) - (float)first) * ((float)BINS / (float)(last + 1 - first));
@@ -381,7 +403,8 @@ __global__ void __launch_bounds__(T) sample_scan_kernel(SampleArgs a, int slices
   const void* x = static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes;
   float most = NEG_INF, least = __builtin_inff();
   int at = begin;
-  pieces<TYPE, T>(x, begin, end, threadIdx.x, [&](const float (&v)[PIECE], int i) {
+  // (maxima and minima pass over NaN)
+  Pieces<TYPE, T, false>(x, begin, end, threadIdx.x).each([&](const float (&v)[PIECE], int i) {
     float hi = v[0], lo = v[0];
 #pragma unroll
     for (int e = 1; e < PIECE; ++e) hi = fmaxf(hi, v[e]), lo = fminf(lo, v[e]);
@@ -399,7 +422,7 @@ __global__ void __launch_bounds__(T) sample_scan_kernel(SampleArgs a, int slices
     }
     least = fminf(least, lo);
   });
-  unsigned long long best = wave_max64((unsigned long long)key_of(most) << 32 | (uint32_t)~at);
+  unsigned long long best = wave_max64((unsigned long long)key_of(clean(most)) << 32 | (uint32_t)~at);
   least = logit_of(~(uint32_t)wave_max64((uint32_t)~key_of(least)));
   if ((threadIdx.x & 63) == 0) {
     red[threadIdx.x >> 6] = best;
@@ -413,7 +436,7 @@ __global__ void __launch_bounds__(T) sample_scan_kernel(SampleArgs a, int slices
       least = fminf(least, __uint_as_float((uint32_t)red[WAVES + i]));
     }
     w.parts[(int64_t)row * slices + s] = Part{(uint32_t)(best >> 32), (int)~(uint32_t)best, least, 0};
-    if (s == 0) w.listed[row] = 0;
+    if (s == 0) w.listed[row] = w.done[row] = 0;
   }
   // the row's histogram starts at 0, a part of it by each slice
   if (a.top_k || a.top_p)
@@ -430,18 +453,18 @@ __global__ void __launch_bounds__(T) sample_bins_kernel(SampleArgs a, int slices
   const bool by_count = set.by_count(a.vocab);
   if (set.greedy || !(by_count || set.by_weight())) return;
   const Work w(a.ws, a.rows, slices);
+  const int begin = s * slice, end = min(begin + slice, a.vocab);
+  Pieces<TYPE, T, false> pieces(static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes, begin, end, threadIdx.x);
   for (int i = threadIdx.x; i < BINS; i += T) bins[i] = 0;
   const Top top = top_of(part_of(w.parts + (int64_t)row * slices, slices), red);  // (with barriers)
   const Binning bin(top, set);
   const Weigh weigh{(double)top.most(), set.by};
-  const int begin = s * slice, end = min(begin + slice, a.vocab);
-  const void* x = static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes;
   uint32_t* counts = reinterpret_cast<uint32_t*>(bins);
-  pieces<TYPE, T>(x, begin, end, threadIdx.x, [&](const float (&v)[PIECE], int) {
+  pieces.each([&](const float (&v)[PIECE], int) {
     if (by_count) {
 #pragma unroll
       for (int e = 0; e < PIECE; ++e)
-        if (v[e] != NEG_INF) atomicAdd(&counts[bin(v[e])], 1u);
+        if (v[e] > NEG_INF) atomicAdd(&counts[bin(v[e])], 1u);
     } else {
 #pragma unroll
       for (int e = 0; e < PIECE; ++e) {
@@ -454,59 +477,6 @@ __global__ void __launch_bounds__(T) sample_bins_kernel(SampleArgs a, int slices
   for (int i = threadIdx.x; i < BINS; i += T) {
     const unsigned long long f = by_count ? counts[i] : bins[i];
     if (f) atomicAdd(&w.bins[(int64_t)row * BINS + i], f);
-  }
-}
-
-// The slice's elements of the bin in which the prefix ends go into the list (or
-// those of all bins up to it); the weights that it keeps of the bins in front of
-// it are summed, by chunks: a wave has a run of the slice.
-template <int TYPE>
-__global__ void __launch_bounds__(T) sample_sums_kernel(SampleArgs a, int slices, int slice) {
-  __shared__ unsigned long long red[2 * WAVES];
-  __shared__ Plan plan_s;
-  __shared__ uint16_t list[CAP];  // places in the slice
-  __shared__ int listed, place;
-  const int row = blockIdx.x / slices, s = blockIdx.x % slices;
-  if (threadIdx.x == 0) listed = 0;
-  const Work w(a.ws, a.rows, slices);
-  const Part part = part_of(w.parts + (int64_t)row * slices, slices);
-  unsigned long long mine[OWN];
-  own_bins(a, w.bins + (int64_t)row * BINS, mine);
-  const Settings set(a, row);
-  if (set.greedy) return;
-  const Top top = top_of(part, red);  // (with barriers)
-  const Binning bin(top, set);
-  const Plan plan = plan_of(a, set, mine, bin.ends, red, &plan_s);
-  if (plan.mode == CUT_MANY) return;
-  const Weigh weigh{(double)top.most(), set.by};
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int first = s * slice, begin = first + wave * (slice / WAVES), end = min(begin + slice / WAVES, a.vocab);
-  const void* x = static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes;
-  unsigned long long sum = 0;
-  pieces<TYPE, 64>(x, begin, end, lane, [&](const float (&v)[PIECE], int i) {
-#pragma unroll
-    for (int e = 0; e < PIECE; ++e) {
-      const int b = plan.mode == CUT_NONE ? 0 : bin(v[e]);
-      if (plan.mode != CUT_FEW && b < plan.bin) {
-        const double p = weigh(v[e]);
-        sum += p >= set.least ? fixed(p) : 0;
-      }
-      if (plan.mode != CUT_NONE && (plan.mode == CUT_FEW ? b <= plan.bin : b == plan.bin) && v[e] != NEG_INF) {
-        const int at = atomicAdd(&listed, 1);
-        if (at < CAP) list[at] = (uint16_t)(i + e - first);
-      }
-    }
-  });
-  sum = wave_scan64(sum);
-  if (lane == 63) w.sums[((int64_t)row * slices + s) * WAVES + wave] = sum;
-  if (plan.mode == CUT_NONE) return;
-  __syncthreads();
-  if (threadIdx.x == 0 && listed) place = atomicAdd(&w.listed[row], listed);
-  __syncthreads();
-  // (more than CAP in all: the list is not used, and not filled past its end)
-  for (int j = threadIdx.x; j < min(listed, CAP) && place + j < CAP; j += T) {
-    const int i = first + list[j];
-    w.list[(int64_t)row * CAP + place + j] = (unsigned long long)~key_of(clean(logit_at<TYPE>(x, i))) << 32 | (uint32_t)i;
   }
 }
 
@@ -594,7 +564,7 @@ struct OneRow {
   // f(logit, index) for the row's elements that are not -infinity
   template <typename F>
   __device__ __forceinline__ void each(F&& f) const {
-    pieces<TYPE, T>(x, 0, a.vocab, threadIdx.x, [&](const float (&v)[PIECE], int i) {
+    Pieces<TYPE, T, true>(x, 0, a.vocab, threadIdx.x).each([&](const float (&v)[PIECE], int i) {
 #pragma unroll
       for (int e = 0; e < PIECE; ++e)
         if (v[e] != NEG_INF) f(v[e], i + e);
@@ -862,55 +832,122 @@ struct OneRow {
     }
     return before;
   }
+
+  // The token, from the row's logits alone.  goal: where the prefix by weight ends,
+  // if that is the only one.
+  __device__ __forceinline__ void alone(bool by_count, bool by_weight, double goal, float u, int32_t* out) const {
+    Cut cut{0, 0};
+    unsigned long long upto = 0;
+    if (by_count) {
+      cut = search(false, (uint32_t)set.k, 0.0, upto);
+      goal = set.p * (double)upto;
+    }
+    if (by_weight) cut = search(true, 1, goal, upto);
+    const unsigned long long total = draw(0, a.vocab, cut, 0, ~0ull >> 1, out);
+    draw(0, a.vocab, cut, 0, target_of(u, total), out);
+  }
 };
 
+// Across the workgroups of a row, which sit on different XCDs whose caches do not
+// see each other: past these.
+template <typename V>
+__device__ __forceinline__ void put(V* p, V v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename V>
+__device__ __forceinline__ V get(const V* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The slice's elements of the bin in which the prefix ends go into the list (or
+// those of all bins up to it); the weights that it keeps of the bins in front of
+// it are summed, by chunks: a wave has a run of the slice.  The row's workgroup
+// that is the last one with this then finds the token; none waits for another.
 template <int TYPE>
 __global__ void __launch_bounds__(T) sample_draw_kernel(SampleArgs a, int slices, int slice) {
   __shared__ Shared sh;
-  const int row = blockIdx.x;
-  const Work wk(a.ws, a.rows, slices);
-  // (all that is needed of memory is asked for at once)
-  const Part part = part_of(wk.parts + (int64_t)row * slices, slices);
-  unsigned long long mine[OWN], sums[OWN];
-  own_bins(a, wk.bins + (int64_t)row * BINS, mine);
-#pragma unroll
-  for (int e = 0; e < OWN; ++e) {
-    const int c = OWN * threadIdx.x + e;
-    sums[e] = c < slices * WAVES ? wk.sums[(int64_t)row * slices * WAVES + c] : 0;
-  }
-  const int listed = wk.listed[row];
-  const unsigned long long* list = wk.list + (int64_t)row * CAP;
+  __shared__ int mine_s, place_s;
+  const int row = blockIdx.x / slices, s = blockIdx.x % slices;
+  if (threadIdx.x == 0) mine_s = 0;
+  const Work w(a.ws, a.rows, slices);
+  const Part part = part_of(w.parts + (int64_t)row * slices, slices);
+  unsigned long long mine[OWN];
+  own_bins(a, w.bins + (int64_t)row * BINS, mine);
   const Settings set(a, row);
   int32_t* out = a.out + row;
   const float u = a.u[row];
-  const Top top = top_of(part, sh.red);
+  const void* x = static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int begin = s * slice + wave * (slice / WAVES), end = min(begin + slice / WAVES, a.vocab);
+  Pieces<TYPE, 64, false> pieces(x, begin, end, lane);
+  const Top top = top_of(part, sh.red);  // (with barriers)
   if (set.greedy || top.most() == NEG_INF) {
-    if (threadIdx.x == 0) *out = top.most() == NEG_INF ? -1 : top.place();
+    if (s == 0 && threadIdx.x == 0) *out = top.most() == NEG_INF ? -1 : top.place();
     return;
   }
-  const OneRow<TYPE> r{a, set, sh, static_cast<const char*>(a.logits) + (int64_t)row * a.row_bytes, Binning(top, set),
-                       Weigh{(double)top.most(), set.by}};
+  const Weigh weigh{(double)top.most(), set.by};
+  const Binning bin(top, set);
+  const OneRow<TYPE> r{a, set, sh, x, bin, weigh};
   const bool by_count = set.by_count(a.vocab), by_weight = set.by_weight();
-  if (by_count || by_weight)
-    for (int j = threadIdx.x; j < min(listed, CAP); j += T) sh.list[j] = list[j];
-  const Plan plan = plan_of(a, set, mine, r.bin.ends, sh.red, &sh.plan);  // (with barriers)
-  unsigned long long total, upto, before, t;
-
-  if (plan.mode == CUT_MANY || (plan.mode != CUT_NONE && listed > CAP)) {
-    // the row alone, from its logits
-    Cut cut{0, 0};
-    double goal = plan.goal;
-    if (by_count) {
-      cut = r.search(false, (uint32_t)set.k, 0.0, upto);
-      goal = set.p * (double)upto;
-    }
-    if (by_weight) cut = r.search(true, 1, goal, upto);
-    total = r.draw(0, a.vocab, cut, 0, ~0ull >> 1, out);
-    r.draw(0, a.vocab, cut, 0, target_of(u, total), out);
+  const Plan plan = plan_of(a, set, mine, bin.ends, sh.red, &sh.plan);
+  if (plan.mode == CUT_MANY) {
+    if (s == 0) r.alone(by_count, by_weight, plan.goal, u, out);
     return;
   }
 
-  const int n = plan.mode == CUT_NONE ? 0 : listed;
+  // (the logits up to the plan's bin are above this, and few others: most pieces are
+  // passed over)
+  const float near = plan.mode == CUT_NONE ? LOWEST : bin.under(plan.bin);
+  unsigned long long sum = 0;
+  pieces.each([&](const float (&v)[PIECE], int i) {
+    const float hi = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+    if (!(hi >= near)) return;
+#pragma unroll
+    for (int e = 0; e < PIECE; ++e) {
+      if (!(v[e] >= near)) continue;
+      const int b = plan.mode == CUT_NONE ? 0 : bin(v[e]);
+      if (plan.mode != CUT_FEW && b < plan.bin) {
+        const double p = weigh(v[e]);
+        sum += p >= set.least ? fixed(p) : 0;
+      } else if (b <= plan.bin) {
+        const int at = atomicAdd(&mine_s, 1);
+        if (at < CAP) sh.few[at] = (unsigned long long)~key_of(clean(v[e])) << 32 | (uint32_t)(i + e);
+      }
+    }
+  });
+  sum = wave_scan64(sum);
+  if (lane == 63) put(&w.sums[((int64_t)row * slices + s) * WAVES + wave], sum);
+  if (plan.mode != CUT_NONE) {
+    __syncthreads();
+    if (threadIdx.x == 0 && mine_s) place_s = atomicAdd(&w.listed[row], mine_s);
+    __syncthreads();
+    // (more than CAP in all: the list is not used, and not filled past its end)
+    for (int j = threadIdx.x; j < min(mine_s, CAP) && place_s + j < CAP; j += T)
+      put(&w.list[(int64_t)row * CAP + place_s + j], sh.few[j]);
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0: this wave's stores have reached the device's memory
+  __syncthreads();                     // ... and every wave's
+  if (threadIdx.x == 0) sh.n = atomicAdd(&w.done[row], 1);
+  __syncthreads();
+  if (sh.n != slices - 1) return;
+
+  // (asked for at once, with the list's first places, whether filled or not)
+  const int n = plan.mode == CUT_NONE ? 0 : get(&w.listed[row]);
+  unsigned long long sums[OWN], upto, before, t;
+#pragma unroll
+  for (int e = 0; e < OWN; ++e) {
+    const int c = OWN * threadIdx.x + e;
+    sums[e] = c < slices * WAVES ? get(&w.sums[(int64_t)row * slices * WAVES + c]) : 0;
+  }
+  const unsigned long long* list = w.list + (int64_t)row * CAP;
+  const unsigned long long l0 = get(&list[threadIdx.x]), l1 = get(&list[T + threadIdx.x]);
+  if (n > CAP) {
+    r.alone(by_count, by_weight, plan.goal, u, out);
+    return;
+  }
+  sh.list[threadIdx.x] = l0, sh.list[T + threadIdx.x] = l1;
+  for (int j = 2 * T + threadIdx.x; j < n; j += T) sh.list[j] = get(&list[j]);
+  __syncthreads();
   Cut cut{0, 0};
   if (plan.mode == CUT_FEW) {
     // everything from the list: the ends, then the draw by chunks of the
@@ -954,8 +991,8 @@ __global__ void __launch_bounds__(T) sample_draw_kernel(SampleArgs a, int slices
     if (w) atomicAdd(&sh.bins[(uint32_t)sh.list[j] / (uint32_t)chunk], w);
   }
   __syncthreads();
-  const int begin = r.chunk_of(u, before, t) * chunk;
-  r.draw(begin, min(begin + chunk, a.vocab), cut, before, t, out);
+  const int at = r.chunk_of(u, before, t) * chunk;
+  r.draw(at, min(at + chunk, a.vocab), cut, before, t, out);
 }
 
 // Logits of a slice: about 1024 workgroups over all rows, between 2048 and
@@ -974,11 +1011,10 @@ int slices_of(int64_t rows, int vocab) {
 template <int TYPE>
 hipError_t launch(const SampleArgs& a, hipStream_t s) {
   const int slice = slice_of(a.rows, a.vocab), slices = slices_of(a.rows, a.vocab);
-  const dim3 grid((unsigned)a.rows * (unsigned)slices), rows((unsigned)a.rows), threads(T);
+  const dim3 grid((unsigned)a.rows * (unsigned)slices), threads(T);
   hipLaunchKernelGGL(sample_scan_kernel<TYPE>, grid, threads, 0, s, a, slices, slice);
   if (a.top_k || a.top_p) hipLaunchKernelGGL(sample_bins_kernel<TYPE>, grid, threads, 0, s, a, slices, slice);
-  hipLaunchKernelGGL(sample_sums_kernel<TYPE>, grid, threads, 0, s, a, slices, slice);
-  hipLaunchKernelGGL(sample_draw_kernel<TYPE>, rows, threads, 0, s, a, slices, slice);
+  hipLaunchKernelGGL(sample_draw_kernel<TYPE>, grid, threads, 0, s, a, slices, slice);
   return hipGetLastError();
 }
 
