@@ -833,6 +833,52 @@ struct OneRow {
     return before;
   }
 
+  // Up to T entries, one a thread (~0: none), sorted: the thread's is the one of its
+  // number.
+  __device__ __forceinline__ unsigned long long sorted(unsigned long long entry, int n) const {
+    const int m = power_of_two(n);
+    if ((int)threadIdx.x < m) sh.few[threadIdx.x] = entry;
+    sort(sh.few, m);
+    return (int)threadIdx.x < n ? sh.few[threadIdx.x] : ~0ull;
+  }
+  // The token, where all that the prefix by count can hold are n <= T entries, one a
+  // thread (~0: none).
+  __device__ __forceinline__ void among(unsigned long long entry, int n, bool by_weight, float u, int32_t* out) const {
+    const int j = threadIdx.x;
+    entry = sorted(entry, n);
+    const bool live = j < n && j < set.k;
+    const double p = weigh(logit_of(key_in(entry)));
+    unsigned long long w = live ? fixed(p) : 0, total;
+    const unsigned long long before = scan(w, total) - w;
+    if (!live || (by_weight && j > 0 && !((double)before < set.p * (double)total)) || !(p >= set.least)) w = 0;
+    // in the order of the vocabulary
+    sh.bins[j] = w;
+    const unsigned long long place = sorted(j < n ? entry << 32 | (uint32_t)j : ~0ull, n);
+    w = j < n ? sh.bins[(uint32_t)place] : 0;
+    const unsigned long long at = scan(w, total) - w, t = target_of(u, total);
+    if (at <= t && t < at + w) *out = (int)(place >> 32);
+  }
+  // The end of a prefix among n <= T entries, one a thread (~0: none), that follow
+  // `plan.before` of it; what stays of them goes into the chunks' sums, sh.bins.
+  __device__ __forceinline__ Cut end_among(unsigned long long entry, int n, bool by_count, const Plan& plan, int chunk) const {
+    const int j = threadIdx.x;
+    entry = sorted(entry, n);
+    const double p = weigh(logit_of(key_in(entry)));
+    unsigned long long w = j < n ? fixed(p) : 0, total;
+    const unsigned long long before = plan.before + scan(w, total) - w;
+    auto stays = [&](int j, unsigned long long before) {
+      return j < n && (j == 0 || (by_count ? j < set.k - (int)plan.before : (double)before < plan.goal));
+    };
+    if (stays(j, before)) {
+      if (!stays(j + 1, before + w)) sh.found = entry;
+      if (w && p >= set.least) atomicAdd(&sh.bins[(uint32_t)entry / (uint32_t)chunk], w);
+    }
+    __syncthreads();
+    const unsigned long long last = sh.found;
+    __syncthreads();
+    return Cut{key_in(last), (int)(uint32_t)last};
+  }
+
   // The token, from the row's logits alone.  goal: where the prefix by weight ends,
   // if that is the only one.
   __device__ __forceinline__ void alone(bool by_count, bool by_weight, double goal, float u, int32_t* out) const {
@@ -950,6 +996,10 @@ __global__ void __launch_bounds__(T) sample_draw_kernel(SampleArgs a, int slices
   __syncthreads();
   Cut cut{0, 0};
   if (plan.mode == CUT_FEW) {
+    if (n <= T) {
+      r.among((int)threadIdx.x < n ? l0 : ~0ull, n, by_weight, u, out);
+      return;
+    }
     // everything from the list: the ends, then the draw by chunks of the
     // vocabulary
     const int last = min(plan.bin, BINS - 1);
@@ -977,18 +1027,22 @@ __global__ void __launch_bounds__(T) sample_draw_kernel(SampleArgs a, int slices
   }
 
   // the chunks' sums, and to each what it keeps of the list
-  if (n) {
+  const int chunk = slice / WAVES;
+  if (n > T) {
     r.parts(n, plan.bin, plan.bin);
     cut = r.end_in(n, plan.bin, plan.bin, !by_count, by_count ? (uint32_t)(set.k - (int)plan.before) : 1,
                    by_count ? 0 : plan.before, plan.goal, upto);
   }
 #pragma unroll
   for (int e = 0; e < OWN; ++e) sh.bins[OWN * threadIdx.x + e] = sums[e];
-  __syncthreads();
-  const int chunk = slice / WAVES;
-  for (int j = threadIdx.x; j < n; j += T) {
-    const unsigned long long w = r.kept(sh.list[j], cut);
-    if (w) atomicAdd(&sh.bins[(uint32_t)sh.list[j] / (uint32_t)chunk], w);
+  if (n > T) {
+    __syncthreads();
+    for (int j = threadIdx.x; j < n; j += T) {
+      const unsigned long long w = r.kept(sh.list[j], cut);
+      if (w) atomicAdd(&sh.bins[(uint32_t)sh.list[j] / (uint32_t)chunk], w);
+    }
+  } else if (n) {
+    cut = r.end_among((int)threadIdx.x < n ? l0 : ~0ull, n, by_count, plan, chunk);
   }
   __syncthreads();
   const int at = r.chunk_of(u, before, t) * chunk;
