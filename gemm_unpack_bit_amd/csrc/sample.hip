@@ -23,13 +23,19 @@
 //
 // Kernels.  `slices` of the vocabulary, each a workgroup, do what touches every
 // logit: sample_scan_kernel (largest and smallest), sample_bins_kernel (the
-// histogram, where a row has top-k or top-p), sample_sums_kernel (the list, and
-// the sum of what is kept for certain); a workgroup per row does the rest
-// (sample_draw_kernel).
+// histogram, where a row has top-k or top-p), sample_draw_kernel (the list, and the
+// sums of what is kept for certain); of each row, the workgroup that is the last one
+// with this does the rest.
 //
-// Bound: for one row the launches; for many the three times that a logit is read
-// (once from memory, then from the caches) and a weight's 20 operations of 64
-// bits, twice with top-p.
+// Bound: for one row the launches and what waits for one another (the largest logit,
+// the bin, the list, the draw); for many the three times that a logit is read (once
+// from memory, then from the caches), and a weight's 50 instructions, 18 of them of
+// 64 bits, at 4.5 cycles each, twice with top-p.
+//
+// Measured: one row of 128256 fp16 logits with top-p 18.6 us; 72 rows of 151643 fp32
+// ones, settings of all kinds, 49.6 us: scan 10, bins 14, draw 23.  In the last a
+// row's summing takes 2 us where little is kept and 9 where nearly all is, its end
+// 2 us for one token of the list, 4 up to 256, 8 above.
 #include "attn_common.hpp"
 #include "step.hpp"
 
@@ -37,7 +43,7 @@ namespace qg {
 namespace {
 
 constexpr int BINS = 1024;  // and at most so many chunks, of which a slice has one per wave
-constexpr int CAP = 2048;   // elements listed
+constexpr int CAP = 2032;   // elements listed (so that four workgroups' LDS fits a CU)
 constexpr int T = 256;      // threads of every workgroup
 constexpr int WAVES = T / 64, PIECE = 8, STEP = PIECE * T, MOST_SLICES = BINS / WAVES;
 constexpr int OWN = BINS / T;  // bins (or chunks) of a thread
@@ -494,9 +500,12 @@ __device__ __forceinline__ unsigned long long target_of(float u, unsigned long l
 __device__ __forceinline__ int power_of_two(int n) { return n < 2 ? 1 : 1 << (32 - __builtin_clz(n - 1)); }
 
 struct Shared {
-  unsigned long long list[CAP], few[CAP];
-  unsigned long long bins[BINS];  // of counts, weights or chunks' sums
-  uint32_t counts[BINS];
+  unsigned long long list[CAP];
+  union {  // (counts are looked at before elements are picked)
+    unsigned long long few[2048];
+    uint32_t counts[BINS];
+  };
+  unsigned long long bins[BINS];  // of weights or chunks' sums
   unsigned long long red[2 * WAVES];
   unsigned long long found;
   Plan plan;
@@ -504,7 +513,7 @@ struct Shared {
   int n, at;
 };
 
-// Sorts list[0 .. n) (n a power of two up to CAP) upwards; the whole workgroup,
+// Sorts list[0 .. n) (n a power of two up to 2048) upwards; the whole workgroup,
 // barriers on both sides.  Up to an entry a thread they stay in registers:
 // partners within a wave change places by lanes, others through the list.
 __device__ __forceinline__ void sort(unsigned long long* list, int n) {
@@ -910,7 +919,7 @@ __device__ __forceinline__ V get(const V* p) {
 // it are summed, by chunks: a wave has a run of the slice.  The row's workgroup
 // that is the last one with this then finds the token; none waits for another.
 template <int TYPE>
-__global__ void __launch_bounds__(T) sample_draw_kernel(SampleArgs a, int slices, int slice) {
+__global__ void __launch_bounds__(T, 4) sample_draw_kernel(SampleArgs a, int slices, int slice) {
   __shared__ Shared sh;
   __shared__ int mine_s, place_s;
   const int row = blockIdx.x / slices, s = blockIdx.x % slices;
@@ -1049,8 +1058,8 @@ __global__ void __launch_bounds__(T) sample_draw_kernel(SampleArgs a, int slices
   r.draw(at, min(at + chunk, a.vocab), cut, before, t, out);
 }
 
-// Logits of a slice: about 1024 workgroups over all rows, between 2048 and
-// 16384 of them each.
+// Logits of a slice: about 1024 workgroups over all rows (72 rows of 151643: 50 us;
+// 768 of them 51, 512 55, 2000 55), between 2048 and 16384 logits each.
 int slice_of(int64_t rows, int vocab) {
   const int64_t each = rows * vocab / (1024 * STEP) * STEP;
   const int64_t least = ((int64_t)vocab + MOST_SLICES * STEP - 1) / (MOST_SLICES * STEP) * STEP;
