@@ -92,7 +92,7 @@ struct AttnArgs {
   int mask_words;
   float* ws;
   float join_cost;  // of one part in units of keys, over the call's items (narrow kernel, Walk::init)
-  uint64_t nonce;  // of the call (attn_narrow.hip, last_part): 48 bits, not 0
+  uint64_t nonce;  // of the call (attn_narrow.hpp, last_part): 48 bits, not 0
 };
 
 // The choice of kernel, its split of the keys, and so the workspace, depend on

@@ -1,7 +1,7 @@
 // Attention for many query rows per key head: whole prompts over packed keys
 // and drafted trees over a paged cache.
 //
-// Mathematics as in attn_narrow.hip (query rows r = t * group + g, running
+// Mathematics as in attn_narrow.hpp (query rows r = t * group + g, running
 // maximum and sums, powers of two).
 //
 // Bound: the matrix cores (2 * head_dim multiplications for each of the two
@@ -33,7 +33,10 @@
 //   transposing reads of four neighbouring rows spread over the banks.
 //
 // A cache of 8 bits: codes come through registers, a step earlier, and become
-// values of the element type on their way into LDS; the rest is the same.
+// values of the element type on their way into LDS; the rest is the same.  Measured
+// (32 heads over 8, head_dim 128): 64-token bf16 trees of 16 rows over 1000 to 8200
+// tokens 111 us (16 bits 107), over four times as many 291 (287 to 294); 16-token
+// fp16 trees of 64 heads over 8 there 77 and 183 (16 bits 89 and 219).
 #pragma once
 
 #include <type_traits>

@@ -654,7 +654,9 @@ hipError_t launch_kv_compact(const KvArgs& c, const int32_t* pos, const int32_t*
                              const int32_t* count, const KvScratch& w, hipStream_t s) {
   if (c.k_exps) {
     // (heads that a wave takes with one look at the kept tokens: as many as
-    // leave enough waves)
+    // leave enough waves.  8 heads: 32 rows of 32 layers 7.9 us, with 1 head a
+    // wave 12.7, with 8 9.4; 16 rows of 80 layers 10.8, 18.3 and 15; one row of
+    // 32 layers 8 with any)
     int group = 1;
     while (group < 8 && group < c.heads_kv && (int64_t)c.rows * c.layers * c.heads_kv / group >= 4096) group *= 2;
     const int64_t waves = (int64_t)2 * c.layers * ((c.heads_kv + group - 1) / group);
