@@ -233,6 +233,11 @@ struct Settings {
     const float m = a.min_p ? a.min_p[row] : 0.f;
     least = m > 0.f ? (m < 1.f ? (double)m : 1.0) : 0.0;
   }
+  // finite, and at most as large as every logit whose weight passes min-p
+  __device__ __forceinline__ float under(float most) const {
+    const float l = (float)((double)most + ((double)__builtin_log2f((float)least) - 0.01) / by);
+    return least > 0.0 && fabsf(l) < __builtin_inff() ? l : LOWEST;
+  }
   __device__ __forceinline__ bool by_count(int vocab) const { return k > 0 && k < vocab; }
   __device__ __forceinline__ bool by_weight() const { return p < 1.0; }
 };
@@ -950,9 +955,10 @@ __global__ void __launch_bounds__(T, 4) sample_draw_kernel(SampleArgs a, int sli
     return;
   }
 
-  // (the logits up to the plan's bin are above this, and few others: most pieces are
-  // passed over)
-  const float near = plan.mode == CUT_NONE ? LOWEST : bin.under(plan.bin);
+  // The logits up to the plan's bin are above this, and few others: most pieces are
+  // passed over.  So are those that min-p takes out, but where top-p counts them.
+  float near = plan.mode == CUT_NONE ? LOWEST : bin.under(plan.bin);
+  if (plan.mode != CUT_FEW) near = fmaxf(near, set.under(top.most()));
   unsigned long long sum = 0;
   pieces.each([&](const float (&v)[PIECE], int i) {
     const float hi = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
