@@ -90,6 +90,18 @@ def test_norm_q8(rows, dim, dtype):
         assert len(plain) == 2 and bool((off <= 0.5 + 127 * 2 * rel).all())
 
 
+@pytest.mark.parametrize("rows,dim", [(500, 4096), (64, 1003), (3, 20000)])
+def test_codes_do_not_depend_on_the_weights_power_of_two(rows, dim):
+    """Steps far from 1 take the division itself, the others its reciprocal with two corrections: the same codes."""
+    t = torch()
+    x, r, w, _, _ = _inputs(rows, dim, t.bfloat16, 17)
+    say("rms_norm_q8, weights of far powers of two", rows, dim)
+    codes, scales, _ = q.rms_norm_q8(x, w, 1e-6, residual=r)
+    for e in (-110, -90, 60, 110):  # (all but the smallest magnitudes, whose codes are 0, stay normal numbers)
+        c, s, _ = q.rms_norm_q8(x, (w.double() * 2.0 ** e).to(t.bfloat16), 1e-6, residual=r)
+        assert t.equal(s.double(), scales.double() * 2.0 ** e) and t.equal(c, codes)
+
+
 @pytest.mark.parametrize("dim", [64, 8200])
 def test_rows_that_are_not_finite_or_zero(dim):
     t = torch()

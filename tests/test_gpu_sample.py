@@ -108,6 +108,24 @@ def test_close_keys_in_one_bin():
         check(x, u, f"outlier, both {p}", k=[30000] * 4, p=[p] * 4)
 
 
+@pytest.mark.parametrize("dtype,min_p", [("float32", 0.0), ("float32", 0.003), ("float16", 0.0)])
+def test_every_length_of_the_list(dtype, min_p):
+    """Prefixes that end after one, hundreds and thousands of tokens, by count and by weight of these."""
+    ks = [1, 2, 63, 64, 65, 255, 256, 257, 300, 511, 512, 513, 1000, 1900, 2031, 2032, 2033, 5000, 40000]
+    n = len(ks)
+    x = logits(2 * n, 60007, dtype, 41, 2.0)
+    u = [(0.37 * i) % 1.0 for i in range(2 * n)]
+    check(x, u, "list lengths", k=ks * 2, p=[1.0] * n + [0.93] * n, low=[min_p] * (2 * n))
+
+
+def test_prefixes_by_weight_alone():
+    """... and by weight alone, with min-p above, in and below the bin where they end."""
+    ps = [0.001, 0.1, 0.5, 0.9, 0.99, 0.9999]
+    x = logits(4 * len(ps), 150001, "float32", 42, 1.5)
+    u = [(0.61 * i) % 1.0 for i in range(4 * len(ps))]
+    check(x, u, "by weight", p=ps * 4, low=sum(([v] * len(ps) for v in (0.0, 0.5, 0.01, 0.0001)), []), t=[1.0, 0.7] * (2 * len(ps)))
+
+
 def test_masked_rows():
     t = torch()
     inf = float("inf")
