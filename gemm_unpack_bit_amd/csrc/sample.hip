@@ -986,8 +986,8 @@ __global__ void __launch_bounds__(T, 4) sample_draw_kernel(SampleArgs a, int sli
     for (int j = threadIdx.x; j < min(mine_s, CAP) && place_s + j < CAP; j += T)
       put(&w.list[(int64_t)row * CAP + place_s + j], sh.few[j]);
   }
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0: this wave's stores have reached the device's memory
-  __syncthreads();                     // ... and every wave's
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's stores have reached the device's memory
+  __syncthreads();                                  // ... and every wave's
   if (threadIdx.x == 0) sh.n = atomicAdd(&w.done[row], 1);
   __syncthreads();
   if (sh.n != slices - 1) return;
