@@ -651,16 +651,23 @@ struct OneRow {
     return r;
   }
 
-  // The end of a prefix anywhere in the row, by the row itself: where the list
-  // cannot say (thousands of elements in one bin, or both criteria over as many).
-  // Counts or weights by ranges of keys, each about a 1000th of the last, until
-  // the range in which the prefix ends has few elements, or one key.
-  __device__ __forceinline__ Cut search(bool by_weight, uint32_t want, double goal, unsigned long long& upto) const {
-    uint32_t low = 0, high = ~0u;
-    unsigned long long inside = 0;  // weights above `high`
+  // Chunks of the vocabulary: at most as many as bins, of at most STEP elements.
+  __device__ __forceinline__ int chunk_shift() const {
+    const int q = (a.vocab - 1) / BINS;
+    return q ? 32 - __builtin_clz(q) : 0;
+  }
+
+  // The end of a prefix in the bin `only` (-1: anywhere) among keys from `low` on, with
+  // the weights `inside` in front, by the row itself: where the list cannot say
+  // (thousands of elements in one bin, or both criteria over as many).  Counts or
+  // weights by ranges of keys, each about a 1000th of the last, until the range in
+  // which the prefix ends has few elements, or one key.
+  __device__ __forceinline__ Cut search(bool by_weight, uint32_t want, double goal, int only, uint32_t low,
+                                        unsigned long long inside, unsigned long long& upto) const {
+    uint32_t high = ~0u;
     auto in = [&](float l) {
       const uint32_t k = key_of(l);
-      return k >= low && k <= high;
+      return k >= low && k <= high && (only < 0 || bin(l) == only);
     };
     uint32_t n = 0;
     for (;;) {
@@ -676,6 +683,7 @@ struct OneRow {
       if (mine) atomicMin(&sh.key0, k0), atomicMax(&sh.key1, k1), atomicAdd(&sh.n, mine);
       __syncthreads();
       low = sh.key0, high = sh.key1, n = sh.n;
+      only = -1;  // (keys between two of a bin are in it)
       want = min(want, n);
       if (n <= CAP || low == high) break;
       const int shift = max(0, 32 - __builtin_clz(high - low) - 10);
@@ -719,24 +727,29 @@ struct OneRow {
       m = need > 0.0 ? (w ? (uint32_t)fmin(ceil(need / (double)w), (double)n) : n) : 1;
     }
     m = max(1u, min(m, n));
-    uint32_t seen = 0;
-    for (int i0 = 0; i0 < a.vocab && seen < m; i0 += STEP) {
-      const int i = i0 + PIECE * threadIdx.x;
-      float v[PIECE];
-      uint32_t mine = 0;
-      if (i < a.vocab) {
-        load_piece<TYPE>(x, i, a.vocab, v);
+    const int shift = chunk_shift();
+    for (int i = threadIdx.x; i < BINS; i += T) sh.counts[i] = 0;
+    __syncthreads();
+    each([&](float l, int i) {
+      if (key_of(l) == high) atomicAdd(&sh.counts[i >> shift], 1u);
+    });
+    __syncthreads();
+    sum_up(sh.counts);
+    const int c = first_bin([&](int i) { return sh.counts[i] >= m; });
+    const int end = min((c + 1) << shift, a.vocab), i = (c << shift) + PIECE * threadIdx.x;
+    float v[PIECE];
+    uint32_t mine = 0;
+    if (i < end) {
+      load_piece<TYPE>(x, i, end, v);
 #pragma unroll
-        for (int e = 0; e < PIECE; ++e) mine += v[e] != NEG_INF && key_of(v[e]) == high;
-      }
-      unsigned long long all;
-      uint32_t at = seen + (uint32_t)scan(mine, all) - mine;
-      if (mine)
-#pragma unroll
-        for (int e = 0; e < PIECE; ++e)
-          if (v[e] != NEG_INF && key_of(v[e]) == high && ++at == m) sh.at = i + e;
-      seen += (uint32_t)all;
+      for (int e = 0; e < PIECE; ++e) mine += v[e] != NEG_INF && key_of(v[e]) == high;
     }
+    unsigned long long all;
+    uint32_t at = (c ? sh.counts[c - 1] : 0) + (uint32_t)scan(mine, all) - mine;
+    if (mine)
+#pragma unroll
+      for (int e = 0; e < PIECE; ++e)
+        if (v[e] != NEG_INF && key_of(v[e]) == high && ++at == m) sh.at = i + e;
     __syncthreads();
     const int place = sh.at;
     __syncthreads();
@@ -893,18 +906,35 @@ struct OneRow {
     return Cut{key_in(last), (int)(uint32_t)last};
   }
 
-  // The token, from the row's logits alone.  goal: where the prefix by weight ends,
-  // if that is the only one.
-  __device__ __forceinline__ void alone(bool by_count, bool by_weight, double goal, float u, int32_t* out) const {
+  // The token, from the row's logits alone.
+  __device__ __forceinline__ void alone(bool by_count, bool by_weight, const Plan& plan, float u, int32_t* out) const {
     Cut cut{0, 0};
-    unsigned long long upto = 0;
+    unsigned long long upto = 0, total, before, t;
     if (by_count) {
-      cut = search(false, (uint32_t)set.k, 0.0, upto);
-      goal = set.p * (double)upto;
+      const bool some = plan.bin < BINS;  // (otherwise all stay)
+      unsigned long long front = 0;
+      if (some && by_weight) {
+        each([&](float l, int) {
+          if (bin(l) < plan.bin) front += fixed(weigh(l));
+        });
+        scan(front, total);
+        front = total;
+      }
+      cut = search(false, (uint32_t)set.k - (some ? (uint32_t)plan.before : 0), 0.0, some ? plan.bin : -1, 0, front, upto);
     }
-    if (by_weight) cut = search(true, 1, goal, upto);
-    const unsigned long long total = draw(0, a.vocab, cut, 0, ~0ull >> 1, out);
-    draw(0, a.vocab, cut, 0, target_of(u, total), out);
+    if (by_weight)
+      cut = search(true, 1, by_count ? set.p * (double)upto : plan.goal, by_count ? -1 : plan.bin, cut.key,
+                   by_count ? 0 : plan.before, upto);
+    const int shift = chunk_shift();
+    for (int i = threadIdx.x; i < BINS; i += T) sh.bins[i] = 0;
+    __syncthreads();
+    each([&](float l, int i) {
+      const unsigned long long w = kept((unsigned long long)~key_of(l) << 32 | (uint32_t)i, cut);
+      if (w) atomicAdd(&sh.bins[i >> shift], w);
+    });
+    __syncthreads();
+    const int c = chunk_of(u, before, t);
+    draw(c << shift, min((c + 1) << shift, a.vocab), cut, before, t, out);
   }
 };
 
@@ -951,7 +981,7 @@ __global__ void __launch_bounds__(T, 4) sample_draw_kernel(SampleArgs a, int sli
   const bool by_count = set.by_count(a.vocab), by_weight = set.by_weight();
   const Plan plan = plan_of(a, set, mine, bin.ends, sh.red, &sh.plan);
   if (plan.mode == CUT_MANY) {
-    if (s == 0) r.alone(by_count, by_weight, plan.goal, u, out);
+    if (s == 0) r.alone(by_count, by_weight, plan, u, out);
     return;
   }
 
@@ -1003,7 +1033,7 @@ __global__ void __launch_bounds__(T, 4) sample_draw_kernel(SampleArgs a, int sli
   const unsigned long long* list = w.list + (int64_t)row * CAP;
   const unsigned long long l0 = get(&list[threadIdx.x]), l1 = get(&list[T + threadIdx.x]);
   if (n > CAP) {
-    r.alone(by_count, by_weight, plan.goal, u, out);
+    r.alone(by_count, by_weight, plan, u, out);
     return;
   }
   sh.list[threadIdx.x] = l0, sh.list[T + threadIdx.x] = l1;
