@@ -706,6 +706,7 @@ struct OneRow {
       low = l > h || l < low ? low : l;
     }
     if (n <= CAP) {
+      __syncthreads();  // (every wave has read the number before it starts again at 0)
       if (threadIdx.x == 0) sh.n = 0;
       __syncthreads();
       each([&](float l, int i) {
