@@ -6,11 +6,14 @@
 
 namespace qg {
 
-// 2^(byte - 127) of an exponent byte (0 and 255 are not written by any call:
-// 2^-126 and 2^127 there)
-__device__ __forceinline__ float exp_scale(uint32_t byte) {
-  byte = byte < 1 ? 1 : byte > 254 ? 254 : byte;
-  return __uint_as_float(byte << 23);
+// An exponent byte as it counts: 0 and 255 are not written by any call, and count
+// as 1 and 254.
+__device__ __forceinline__ uint32_t exp_of(uint32_t byte) { return byte < 1 ? 1 : byte > 254 ? 254 : byte; }
+// 2^(byte - 127) of an exponent byte
+__device__ __forceinline__ float exp_scale(uint32_t byte) { return __uint_as_float(exp_of(byte) << 23); }
+// 2^(127 - e) of an exponent e from 1 to 254 (2^-127 is subnormal)
+__device__ __forceinline__ float exp_inverse(int e) {
+  return __uint_as_float(e < 254 ? (uint32_t)(254 - e) << 23 : 0x400000u);
 }
 
 // Two codes, the low or high half of `codes`, times a power of two, as two

@@ -228,9 +228,10 @@ __device__ __forceinline__ void block_heads(const KvAppendArgs& a, int b, int p0
     most = fmaxf(most, dpp<DPP_ROR4>(most));
     most = fmaxf(most, dpp<DPP_ROR8>(most));
     const int need = exp_byte(quarter_max(most));
-    const int old = had > EXP_MOST ? EXP_MOST : had < EXP_LEAST ? EXP_LEAST : had;
-    const int now = i0 && old > need ? old : need;
-    const float by = __uint_as_float((uint32_t)(254 - now) << 23);  // 2^(127 - now)
+    // (what the block has may be any exponent, below the least that is given here
+    // and above the largest too)
+    const int old = (int)exp_of(had), now = i0 && old > need ? old : need;
+    const float by = exp_inverse(now);
 #pragma unroll
     for (int x = 0; x < PASSES; ++x) {
       const int i = TP * x + lane / U;
