@@ -61,7 +61,7 @@ __device__ __forceinline__ float exp_ratio(int from, int to) {
 
 // The exponent byte of a block: the least e with amax <= 448 * 2^e (448, the
 // largest code, is 1.75 * 2^8), at least -64, plus 127.  amax is finite.
-constexpr int EXP_LEAST = 127 - 64, EXP_MOST = 127 + 120;
+constexpr int EXP_LEAST = 127 - 64;
 __device__ __forceinline__ int exp_byte(float amax) {
   const uint32_t u = __float_as_uint(amax);
   const int e = (int)(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);

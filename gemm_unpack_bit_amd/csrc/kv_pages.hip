@@ -576,14 +576,13 @@ __global__ void __launch_bounds__(256) kv_compact_move8_kernel(KvArgs c, const i
     const int64_t pool = (int64_t)c.pages << c.page_shift;
     for (int h = h0; h < min(h0 + group, c.heads_kv); ++h) {
       u4 v[PASSES];
-      int e[PASSES], most = EXP_LEAST;
+      int e[PASSES], most = 1;
 #pragma unroll
       for (int x = 0; x < PASSES; ++x) {
-        e[x] = EXP_LEAST;
+        e[x] = 1;
         if ((uint64_t)f[x] >= (uint64_t)pool || (uint64_t)t[x] >= (uint64_t)pool) continue;
         v[x] = *reinterpret_cast<const u4*>(codes + (f[x] * c.heads_kv + h) * D + 16 * (lane % U));
-        e[x] = exps[f[x] / KV_BLOCK * c.heads_kv + h];
-        e[x] = e[x] > EXP_MOST ? EXP_MOST : e[x] < EXP_LEAST ? EXP_LEAST : e[x];
+        e[x] = (int)exp_of(exps[f[x] / KV_BLOCK * c.heads_kv + h]);
         most = max(most, e[x]);
       }
 #pragma unroll

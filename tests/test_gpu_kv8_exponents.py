@@ -78,3 +78,44 @@ def test_append_in_front_of_nothing():
     assert np.array_equal(exps[0].cpu().numpy().astype(np.int64).reshape(host[0].e.shape), host[0].e) and t.equal(exps[0], exps[1])
     got = held(codes[0], exps[0], host[0]).reshape(rows, PAGE, DIM)
     assert np.array_equal(got[:, 0], host[0].v.reshape(rows, PAGE, DIM)[:, 0])
+
+
+def test_compact_between_blocks():
+    """Tokens moved between blocks under every pair of bytes: a block that gains tokens has the largest of the exponents that
+    its tokens come from, also where that is below the least that appending gives."""
+    t = torch()
+    say("kv8_compact exponents")
+    pairs = np.array([(a, b) for a in BYTES for b in BYTES])
+    rows = len(pairs)
+    cache, codes, exps, host = filled(rows, 2, pairs)
+    cache.lens.fill_(32)
+    # tokens 0 .. 3 stay, then come token 5 and 17, 20 and 31 of the second block
+    keep = [1, 13, 16, 27]
+    q.kv_compact(cache, ints([4] * rows), ints([keep] * rows), ints([len(keep)] * rows))
+    assert int(cache.status) == 0 and cache.lens.tolist() == [4 + len(keep)] * rows
+    end = 4 + len(keep)
+    for which in range(2):
+        for b in range(rows):
+            host[which].compact([2 * b, 2 * b + 1], 4, keep)
+        got_e = counts_as(exps[which].cpu().numpy()).astype(np.int64).reshape(rows, 2)
+        assert np.array_equal(got_e[:, 0], host[which].e.reshape(rows, 2)[:, 0])
+        got = held(codes[which], exps[which], host[which]).reshape(rows, 2 * PAGE, DIM)
+        assert np.array_equal(got[:, :end], host[which].v.reshape(rows, 2 * PAGE, DIM)[:, :end], equal_nan=True)
+
+
+def test_compact_takes_the_exponent_of_the_tokens_that_are_left():
+    """A block all of whose tokens come from blocks of smaller exponents has theirs afterwards."""
+    t = torch()
+    say("kv8_compact exponents: all tokens of the block replaced")
+    pairs = np.array([(a, b) for a in BYTES for b in BYTES])
+    rows = len(pairs)
+    cache, codes, exps, host = filled(rows, 2, pairs)
+    cache.lens.fill_(32)
+    keep = list(range(16, 32))
+    q.kv_compact(cache, ints([0] * rows), ints([keep] * rows), ints([16] * rows))
+    for which in range(2):
+        for b in range(rows):
+            host[which].compact([2 * b, 2 * b + 1], 0, keep)
+        assert np.array_equal(counts_as(exps[which].cpu().numpy()).astype(np.int64).reshape(rows, 2)[:, 0], counts_as(pairs[:, 1]))
+        got = held(codes[which], exps[which], host[which]).reshape(rows, 2 * PAGE, DIM)
+        assert np.array_equal(got[:, :16], host[which].v.reshape(rows, 2 * PAGE, DIM)[:, :16], equal_nan=True)
