@@ -17,8 +17,9 @@ __device__ __forceinline__ float exp_inverse(int e) {
 }
 
 // Two codes, the low or high half of `codes`, times a power of two, as two
-// 16-bit values: one instruction, exact where the type holds the value (bf16
-// always, fp16 from 2^-24 to 65504; past that infinite).
+// 16-bit values: one instruction, exact where the type holds the value (with its
+// four significant bits from 2^-21 to 65504 in fp16, from 2^-130 on in bf16),
+// rounded to nearest even below, subnormal ones too, infinite above.
 template <typename E, bool HI>
 __device__ __forceinline__ uint32_t decode2(uint32_t codes, float scale);
 template <>

@@ -246,7 +246,10 @@ int qgemv_kv8_append(int dtype, const qgemv_kv8_cache *c, int layer, int tokens,
                      const qgemv_heads *k, const qgemv_heads *v, const int32_t *cu, const int32_t *pos,
                      const float *freqs, int rot, int interleaved, const int32_t *at, const qgemv_heads *o,
                      qgemv_stream_t stream);
-/* (values past fp16's range are infinite in a read of QGEMV_F16) */
+/* Values in either type: exact where it holds them, from 2^-21 to 65504 in fp16
+ * and from 2^-130 to 2^128 in bf16; smaller ones are rounded to nearest even,
+ * larger ones infinite.  (Appending may round past that: tokens of 63488 and more
+ * in fp16, or 1.9375 * 2^127 in bf16, come back infinite.) */
 int qgemv_kv8_read(int dtype, const qgemv_kv8_cache *c, int layer, int tokens, const int32_t *cu, const int32_t *start,
                    const qgemv_heads *k, const qgemv_heads *v, qgemv_stream_t stream);
 int qgemv_kv8_fork(const qgemv_kv8_cache *c, const int32_t *parents, const qgemv_kv8_cache *out, void *ws,
@@ -255,8 +258,7 @@ int qgemv_kv8_compact(const qgemv_kv8_cache *c, const int32_t *pos, const int32_
                       const int32_t *count, void *ws, size_t ws_bytes, qgemv_stream_t stream);
 
 /* qgemv_attn_tree over a cache of 8 bits: keys and values are its values in the
- * queries' type (exact in bf16; in fp16 from 2^-24 to 65504, infinite past
- * that). */
+ * queries' type, exact or rounded as qgemv_kv8_read gives them. */
 int qgemv_attn_tree8(int dtype, const qgemv_kv8_cache *c, int layer, int tokens, int heads, float scale,
                      const qgemv_heads *q, const int32_t *cu, const int32_t *pos, const uint64_t *mask,
                      int mask_words, const qgemv_heads *o, void *ws, size_t ws_bytes, qgemv_stream_t stream);

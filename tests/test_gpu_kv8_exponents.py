@@ -119,3 +119,42 @@ def test_compact_takes_the_exponent_of_the_tokens_that_are_left():
         assert np.array_equal(counts_as(exps[which].cpu().numpy()).astype(np.int64).reshape(rows, 2)[:, 0], counts_as(pairs[:, 1]))
         got = held(codes[which], exps[which], host[which]).reshape(rows, 2 * PAGE, DIM)
         assert np.array_equal(got[:, :16], host[which].v.reshape(rows, 2 * PAGE, DIM)[:, :16], equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_read_of_every_code_under_every_byte(dtype):
+    """A value read is the cache's, rounded to nearest even where the type does not hold it (below 2^-21 in fp16, below
+    2^-130 in bf16), and infinite past the type's range."""
+    t = torch()
+    say("kv8_read: every code and byte", dtype)
+    rows = 256
+    cache, codes, exps, _ = filled(rows, 1, np.arange(rows)[:, None])
+    for c in codes:
+        c.copy_((t.arange(PAGE * DIM, device="cuda") % 256).to(t.uint8).view(1, 1, PAGE, 1, DIM).expand_as(c))
+    got = q.kv_read(cache, 0, ints([PAGE * i for i in range(rows + 1)]), ints([0] * rows), tokens=PAGE * rows, dtype=getattr(t, dtype))
+    # (exact in 32 bits, subnormal ones too, but for those past 2^128)
+    with np.errstate(over="ignore"):
+        exact = ref.values(codes[0].cpu().numpy(), counts_as(exps[0].cpu().numpy())).astype(np.float32).reshape(-1, 1, DIM)
+    want = t.from_numpy(exact).to(getattr(t, dtype))
+    for x in got:
+        x = x.cpu()
+        same = (x == want) | (x.isnan() & want.isnan())
+        assert bool(same.all()), [(float(a), float(b), float(c)) for a, b, c in
+                                  zip(x[~same][:9], want[~same][:9], t.from_numpy(exact)[~same][:9])]
+
+
+@pytest.mark.parametrize("dtype,last", [("float16", 63456.0), ("bfloat16", 247 * 2.0 ** 120)])
+def test_the_largest_values_come_back_infinite(dtype, last):
+    """The largest code that a type holds is 240 under the exponent of its largest values; from 248 on the nearest is 256."""
+    t = torch()
+    say("kv8: the largest values", dtype)
+    cache, _, _, _ = filled(2, 1, np.full((2, 1), 127))
+    x = t.full((2, 1, DIM), last, device="cuda").to(getattr(t, dtype))
+    x[1] = 248 * 2.0 ** (8 if dtype == "float16" else 120)
+    assert bool(x.isfinite().all()) and float(x[1, 0, 0]) > float(x[0, 0, 0])
+    x[1, 0, 1::2] *= -1
+    cu = ints([0, 1, 2])
+    q.kv_append(cache, 0, x, x, cu, ints([0, 0]))
+    for got in q.kv_read(cache, 0, cu, ints([0, 0]), tokens=2, dtype=x.dtype):
+        assert bool((got[0] == 240 * 2.0 ** (8 if dtype == "float16" else 120)).all())
+        assert bool((got[1, 0, ::2] == float("inf")).all()) and bool((got[1, 0, 1::2] == -float("inf")).all())
