@@ -495,11 +495,11 @@ __global__ void __launch_bounds__(T) sample_bins_kernel(SampleArgs a, int slices
 // rows
 // ---------------------------------------------------------------------------
 
-// the place of a draw in a sum of weights
+// the place of a draw in a sum of weights, below it (u past the numbers below 1
+// counts as the last of these, NaN as 0)
 __device__ __forceinline__ unsigned long long target_of(float u, unsigned long long total) {
-  const double t = (double)u * (double)total;
-  if (!(t > 0.0)) return 0;
-  return t < (double)total ? (unsigned long long)t : total - 1;
+  const double t = (double)(u < 1.f ? u : 0x1.fffffep-1f) * (double)total;
+  return u > 0.f ? (unsigned long long)t : 0;
 }
 
 __device__ __forceinline__ int power_of_two(int n) { return n < 2 ? 1 : 1 << (32 - __builtin_clz(n - 1)); }

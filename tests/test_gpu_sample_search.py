@@ -33,3 +33,19 @@ def test_searched_rows(vocab, dtype):
     for i in range(20):
         say("searched, again", vocab, dtype, i)
         assert t.equal(q.sample(*args), first)
+
+
+@pytest.mark.parametrize("vocab", [2, 3000, 40007])
+def test_numbers_of_one_and_more(vocab):
+    """u of 1 and more counts as the largest number below 1, so a last token of less than 2^-24 of the weights is not
+    drawn for it."""
+    t = torch()
+    say("sample: u of 1 and more", vocab)
+    x = t.full((6, vocab), -27.0, device="cuda")  # 1.9e-12 each: together less than 2^-24, each more than 2^-42
+    x[:, vocab // 2 - 1] = 0.0
+    x[5] = 0.0
+    u = [1.0, 1.5, float("inf"), 3e38, 0.99999994, 1.0]
+    want = [vocab // 2 - 1] * 5 + [vocab - 1]
+    for more in ({}, dict(top_k=t.full((6,), vocab, dtype=t.int32, device="cuda")), dict(top_p=t.ones(6, device="cuda")),
+                 dict(min_p=t.full((6,), 1e-20, device="cuda"))):
+        assert q.sample(x, t.tensor(u, device="cuda"), **more).tolist() == want, more
