@@ -1120,6 +1120,8 @@ hipError_t launch(const SampleArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// (Past 2^24 logits a slice has 16384, and with fewer there are at most 2048 slices
+// and one a row: fewer than 2^23 are asked for where rows * ceil(vocab / 16384) is.)
 bool sample_fits(int rows, int vocab) { return (int64_t)rows * slices_of(rows, vocab) < 1 << 23 && rows < 1 << 21; }
 size_t sample_ws_bytes(int rows, int vocab) { return work_bytes(rows, slices_of(rows, vocab)); }
 
