@@ -197,8 +197,8 @@ int qgemv_attn_tree(int dtype, const qgemv_kv_cache *c, int layer, int tokens, i
  *               and strides)
  * Token cu[b] + i goes to position pos[b] + i of row b (pos from
  * qgemv_kv_reserve).  Tokens of rows at -1 and tokens of no row are skipped, in
- * o too; keys and values at a position without a page are.  The sum of tokens
- * * (heads + heads_kv) is at most about 2^28 (SHAPE).
+ * o too; keys and values at a position without a page are.  tokens * (heads +
+ * 2 * heads_kv + 8) + 32 * rows * heads_kv is below 2^29 - 64 (SHAPE otherwise).
  * Checks, in order: null, dtype, cache, rot, shape, alignment, overlap.
  * ------------------------------------------------------------------------ */
 int qgemv_kv_append(int dtype, const qgemv_kv_cache *c, int layer, int tokens, int heads, const qgemv_heads *q,
@@ -208,7 +208,8 @@ int qgemv_kv_append(int dtype, const qgemv_kv_cache *c, int layer, int tokens, i
 
 /* Copies tokens of the cache into packed arrays: token cu[b] + i of k and v
  * becomes position start[b] + i of row b (rows at -1, tokens of no row and
- * positions without a page are skipped: k and v stay as they were there). */
+ * positions without a page are skipped: k and v stay as they were there).  Up to
+ * 2^26 - 4 tokens (SHAPE otherwise). */
 int qgemv_kv_read(const qgemv_kv_cache *c, int layer, int tokens, const int32_t *cu, const int32_t *start,
                   const qgemv_heads *k, const qgemv_heads *v, qgemv_stream_t stream);
 

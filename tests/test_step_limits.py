@@ -40,3 +40,41 @@ def test_sample_strides(L):
     assert sample(L, 180000, 1000, 1 << 40) == q.ERR_WORKSPACE and sample(L, 182000, 1000, 1 << 40) == q.ERR_SHAPE
     assert sample(L, 2, 1000, 0) == q.ERR_WORKSPACE and sample(L, 2, 1000, -1) == q.ERR_SHAPE
     assert sample(L, 1, 1000, -1) == q.ERR_WORKSPACE  # (that of a single row is not looked at)
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("data", v), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("layers", "pages", "page_size", "heads_kv", "head_dim", "rows", "max_pages")]
+    _fields_ += [(n, v) for n in ("k", "v", "tables", "lens", "refs", "status")]
+
+
+class Cache8(ctypes.Structure):
+    _fields_ = Cache._fields_[:9] + [("k_exps", v), ("v_exps", v)] + Cache._fields_[9:]
+
+
+def cache(eight, rows, kv):
+    kind = Cache8 if eight else Cache
+    return ctypes.byref(kind(1, 10, 16, kv, 64, rows, 4, *[FAKE * (10 + i) for i in range(8 if eight else 6)]))
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_append(L, eight):
+    call = L.qgemv_kv8_append if eight else L.qgemv_kv_append
+    for heads, kv, rows in ((0, 1, 1), (8, 1, 300), (32, 8, 48), (64, 8, 65535), (1000, 100, 5000)):
+        most = ((1 << 29) - 65 - 32 * rows * kv) // (heads + 2 * kv + 8)
+        h = lambda n, at: ctypes.byref(Heads(FAKE + at, n * 64, 64))  # noqa: E731
+        for tokens in (most - 1, most, most + 1, most + 2):
+            got = call(0, cache(eight, rows, kv), 0, tokens, heads, h(heads, 0), h(kv, 8), h(kv, 0), v(FAKE), v(FAKE), v(0), 0, 0, v(0),
+                       h(heads, 0), v(0))
+            assert got == (q.ERR_ALIGN if tokens <= most else q.ERR_SHAPE), (heads, kv, rows, tokens)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_read(L, eight):
+    h = lambda at: ctypes.byref(Heads(FAKE + at, 128, 64))  # noqa: E731
+    for tokens, want in (((1 << 26) - 4, q.ERR_ALIGN), ((1 << 26) - 3, q.ERR_SHAPE)):
+        more = (cache(eight, 3, 2), 0, tokens, v(FAKE), v(FAKE), h(8), h(0), v(0))
+        assert (L.qgemv_kv8_read(0, *more) if eight else L.qgemv_kv_read(*more)) == want
