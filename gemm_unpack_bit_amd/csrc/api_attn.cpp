@@ -191,6 +191,13 @@ bool apart(const Pools& p, std::initializer_list<Span> others) {
     if (overlap(p, x)) return false;
   return true;
 }
+// whether no pool (or its exponents) lies over another one
+bool distinct(const Pools& p) {
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (qg::overlap(p.of[i], p.of[j])) return false;
+  return true;
+}
 Span tables_of(const Cache& c) { return span(c.tables, (int64_t)4 * c.rows * c.max_pages); }
 Span lens_of(const Cache& c) { return span(c.lens, c.lens ? (int64_t)4 * c.rows : 0); }
 Span refs_of(const Cache& c) { return span(c.refs, c.refs ? (int64_t)4 * c.pages : 0); }
@@ -424,7 +431,8 @@ int kv_fork(const Cache& c, const int32_t* parents, const Cache& out, void* ws,
       !apart({tables_of(out), lens_of(out), kv_scratch(rows, c.pages, ws), refs_of(c), status_of(c)},
              {sp, tables_of(c), lens_of(c)}) ||
       !apart(pools(c), {sp, tables_of(c), lens_of(c), tables_of(out), lens_of(out), kv_scratch(rows, c.pages, ws), refs_of(c),
-                        status_of(c)}))
+                        status_of(c)}) ||
+      (c.bits8 && !distinct(pools(c))))
     return QGEMV_ERR_VALUE;
   qg::KvScratch w;
   if ((rc = scratch(rows, c.pages, ws, ws_bytes, &w))) return rc;
@@ -443,7 +451,8 @@ int kv_compact(const Cache& c, const int32_t* pos, const int32_t* keep, int max_
              sc = span(count, (int64_t)4 * c.rows), sw = kv_scratch(c.rows, c.pages, ws);
   // (a row's length is written after its position and count are read: pos may be lens)
   if (!apart({sw, tables_of(c), refs_of(c), status_of(c)}, {sp, sk, sc, lens_of(c)}) ||
-      !apart(pools(c), {sp, sk, sc, lens_of(c), sw, tables_of(c), refs_of(c), status_of(c)}))
+      !apart(pools(c), {sp, sk, sc, lens_of(c), sw, tables_of(c), refs_of(c), status_of(c)}) ||
+      (c.bits8 && !distinct(pools(c))))
     return QGEMV_ERR_VALUE;
   qg::KvScratch w;
   if ((rc = scratch(c.rows, c.pages, ws, ws_bytes, &w))) return rc;
@@ -492,6 +501,7 @@ int kv_append(int dtype, const Cache& c, int layer, int tokens, int heads, const
                         span(at, at ? (int64_t)4 * tokens : 0)};
   for (const Span& x : small)
     if (overlap(p, x) || overlap(so, x)) return QGEMV_ERR_VALUE;
+  if (!distinct(p)) return QGEMV_ERR_VALUE;
   if (!apart(p, {so, span(q, tokens, heads, c.head_dim), span(k, tokens, c.heads_kv, c.head_dim),
                  span(v, tokens, c.heads_kv, c.head_dim)}))
     return QGEMV_ERR_VALUE;

@@ -113,7 +113,8 @@ typedef struct {
 
 /* Every call: QGEMV_ERR_VALUE where something that it writes (its results, the
  * workspace, the state above) overlaps something else that it writes or reads;
- * kv_compact's pos, keep and count may lie in lens. */
+ * kv_compact's pos, keep and count may lie in lens.  (qgemv_kv_write, _fork and
+ * _compact do not look whether k and v lie over each other.) */
 
 /* Scratch of kv_reserve, kv_fork and kv_compact: [dev], 16-byte aligned, no
  * initial contents.  rows: the larger of the caches' rows. */
