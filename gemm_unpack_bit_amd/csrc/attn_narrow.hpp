@@ -34,10 +34,11 @@
 // (Codes), which become values of the element type (e4m3.hpp) when they are used;
 // a tile of 16 keys is one block, with one exponent for its keys and one for its
 // values.  Measured: 32 rows of 4500 keys on average, 64 heads over 8, 72 us, of
-// 18000 239 us (5.1 TB/s; 16-bit keys 115 and 410 us).  What bounds it is memory:
-// before the loads were marked as read once only, they alone, without any
-// products, took 75 and 256 of 79 and 262 us, whether one step or two were on
-// their way, in pages of 16 as in pages of 256.
+// 18000 239 us (4.3 and 5.1 TB/s; 16-bit keys 115 and 410 us, 5.3 and 5.8).  What
+// bounds it is the codes' way from memory, though not its rate: before the loads
+// were marked as read once only, they alone, without any products, took 75 and 256
+// of 79 and 262 us, whether one step or two were on their way, in pages of 16 as
+// in pages of 256.
 #pragma once
 
 #include <type_traits>

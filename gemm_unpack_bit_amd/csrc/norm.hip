@@ -13,7 +13,7 @@
 // us instead of 66, and the 8-bit form for 16 waves did not fit its registers.
 //
 // Measured (bf16 or fp16, with a residual): 5003 rows of 8192 66 us (328 MB, 5.0
-// TB/s, as a large copy), one row of 4096 3.2 us.  Outputs past the caches
+// TB/s, as a large copy), in 8 bits 68 us (287 MB), one row of 4096 3.2 us.  Outputs past the caches
 // (non-temporal) took 62 us, but what reads them next lost that again.
 #include "attn_common.hpp"
 #include "step.hpp"
