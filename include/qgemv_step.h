@@ -53,8 +53,9 @@ int qgemv_rms_norm(int dtype, int rows, int dim, float eps, const qgemv_rows *x,
 
 /* The same with y in 8 bits, as qgemv_w4a8_rows takes it:
  *     step[r] = max_d |y[r, d]| / 127,  y8[r, d] = rint(y[r, d] / step[r])
- * from y in fp32 (it is not rounded to 16 bits first).  A row of zeros has step
- * 0 and codes 0; one whose y is not finite throughout has step NaN and codes 0.
+ * from y in fp32 (it is not rounded to 16 bits first).  A row whose y is 0
+ * throughout has step 0 and codes 0; one whose y is not finite throughout (zeros
+ * with an eps of 0 among them) has step NaN and codes 0.
  *   y8 [dev]    int8 [rows][dim]
  *   step [dev]  fp32 [rows]
  * y8 and step may not overlap anything else (VALUE). */
