@@ -98,10 +98,11 @@ int qgemv_w4a8_rows(int M, int N, int K, const int8_t *x8, const float *step, co
  * these are.  Weights are held to 2^-42 of the largest (smaller ones round to 0
  * or that), worked out in 64 bits; they add up exactly.
  *
- * 1 <= vocab <= 2^21, rows below 2^21, rows * ceil(vocab / 16384) below 2^23, row
- * not negative, at most 2^40 and rows * row at most 2 * 10^17 (SHAPE otherwise; the
- * workspace size is 0 then); rows of 0 does nothing.  Checks, in order: null, type (UNSUPPORTED), shape, alignment,
- * overlap of token or ws with anything else (VALUE), workspace.
+ * 1 <= vocab <= 2^21, rows below 2^21 and rows * ceil(vocab / 16384) below 2^23
+ * (SHAPE otherwise, and a workspace size of 0); row not negative, at most 2^40, and
+ * rows * row at most 2 * 10^17 (SHAPE).  rows of 0 does nothing.  Checks, in order:
+ * null, type (UNSUPPORTED), shape, alignment, overlap of token or ws with anything
+ * else (VALUE), workspace.
  * ------------------------------------------------------------------------ */
 #define QGEMV_F32 2
 size_t qgemv_sample_workspace_bytes(int rows, int vocab);
